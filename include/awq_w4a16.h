@@ -52,6 +52,12 @@ enum awq_status {
   AWQ_ERR_HIP = -6          /* the HIP runtime reported an error */
 };
 
+/* Element types of the entry points that take one (16-bit types as raw storage). */
+enum awq_type { AWQ_F16 = 0, AWQ_BF16 = 1, AWQ_F32 = 2 };
+
+/* Scores of awq_moe_route. */
+enum awq_score { AWQ_SOFTMAX = 0, AWQ_SIGMOID = 1 };
+
 /* Human-readable name of a status code; never NULL, static storage. */
 const char* awq_status_string(int status);
 
@@ -214,7 +220,7 @@ int awq_gemm_bf16(const void* x_bf16, const int32_t* qweight, const int32_t* qze
  * + j (token t = s / topk) computes
  *   y[s, :] = x[t, :] . dequant(W[expert_ids[s]])      (fp16, fp32 accumulation)
  * The expert's activation function and the weighted sum over a token's topk slots
- * come after this product and are not part of it.
+ * are not part of it (awq_moe_gate_up, awq_moe_down).
  *
  * awq_moe_tiles: table entries for S = T * topk slots, E experts and tiles of
  * block_rows rows: ceil(S / block_rows) + E (an upper bound of sum over experts of
@@ -259,6 +265,81 @@ int awq_moe_gemm(const void* x_f16, const int32_t* qweight, const int32_t* qzero
                  const void* scales_f16, const int32_t* expert_ids,
                  int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int64_t group_size,
                  void* y_f16, struct ihipStream_t* stream);
+
+/*
+ * Routing: the experts of each token and their weights, from the router's logits.
+ *   logits       device [T, E] of logits_type (AWQ_F16, AWQ_BF16, AWQ_F32), rows row_stride
+ *                elements apart (row_stride >= E)
+ *   bias         device fp32 [E], or NULL: added to the scores for the choice, not in the weights
+ *   score        AWQ_SOFTMAX: s = exp(l) / sum exp(l);  AWQ_SIGMOID: s = 1 / (1 + exp(-l))
+ *   groups       the experts form that many groups of E / groups consecutive ones (1: none);
+ *                a group is worth its largest s + bias (group_top 1) or the sum of its two
+ *                largest (group_top 2; of the one, where only one can be chosen), and only the
+ *                experts of the best topk_groups groups are considered
+ *   topk         experts per token, the largest s + bias first
+ *   renormalize  nonzero: the weights are divided by their sum over the token's experts
+ *   scale        factor of the weights
+ *   weights      device fp32 [T, topk]: s of the chosen experts (divided, scaled)
+ *   expert_ids   device int32 [T, topk]
+ * Equal s + bias (equal group worths) go to the lowest index; the comparison is that of the
+ * exact values: without a bias of the logits themselves, otherwise of sums in fp64.  An
+ * expert whose logit (or s + bias) is -inf is never chosen; slots left without an expert
+ * get id -1, which the products below do not route, and weight 0.  A row that holds a NaN,
+ * or for the softmax +inf, gets ids -1 and NaN weights.
+ * Limits: E % groups == 0, topk <= topk_groups * (E / groups) (AWQ_ERR_SHAPE); E <= 1024,
+ * topk <= 64, groups <= 64, T <= 2^24 (AWQ_ERR_UNSUPPORTED).  T == 0 enqueues nothing.
+ */
+int awq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int64_t row_stride,
+                  const float* bias, int score, int64_t groups, int64_t topk_groups, int group_top,
+                  int64_t topk, int renormalize, float scale, float* weights, int32_t* expert_ids,
+                  struct ihipStream_t* stream);
+
+/*
+ * The gated MLP of routed experts, and its two halves.  Slot s = t * topk + j of token t goes
+ * to expert e = expert_ids[s]:
+ *   awq_moe_gate_up   h[s, i] = silu(x[t] . W[e][:, i]) * (x[t] . W[e][:, inner + i])
+ *   awq_moe_down      y[t, :] = sum over j of weights[t, j] * (h[s] . W[e])
+ *   awq_moe_mlp       both, h kept in the workspace, rounded to the activation type
+ * with silu(v) = v / (1 + exp(-v)).
+ *   act            AWQ_F16 or AWQ_BF16: the type of x, h and y (scales stay fp16)
+ *   x              device [T, K];  h device [T * topk, inner];  y device [T, N]
+ *   gate_up weight qweight int32 [E, K, 2 inner / 8], qzeros [E, G, 2 inner / 8], scales fp16
+ *                  [E, G, 2 inner]: the gate's columns first, then the up projection's
+ *   down weight    qweight int32 [E, K, N / 8] and so on; K = inner for awq_moe_mlp
+ *   expert_ids     device int32 [T * topk]; ids outside [0, E) are not routed: their h rows are
+ *                  left as they are, and they add nothing to y (a token without any gets zeros)
+ *   weights        device fp32 [T, topk]
+ *   workspace      device memory of at least awq_moe_workspace bytes, 16-byte aligned, for this
+ *                  call alone until its work on the stream is done.  It needs no contents and
+ *                  keeps none.  (The caller's, not the library's: two graphs captured on one
+ *                  stream may then be replayed side by side, and a capture's first call needs
+ *                  no earlier one.)
+ * The products are sums of x times the integers (q - z), scaled per group in fp32 and not
+ * rounded before the activation or the sum over a token's slots: h and y are rounded once.
+ * The result is deterministic.  A NaN or infinity in a row of x or h reaches only that row's
+ * token.
+ * Limits: those of awq_gemm for each product with M = T * topk (inner % 32 == 0 as well),
+ * 1 <= E <= 1024, topk >= 1, x and h below 4 GiB.  T == 0 enqueues nothing.
+ *
+ * awq_moe_workspace: bytes for gate_up (N = 0), down (K = 0, inner = its K) or mlp; the
+ * negative status that the call would return for these sizes.  Host-only.
+ */
+int64_t awq_moe_workspace(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
+                          int64_t group_size);
+int awq_moe_gate_up(const void* x, int act, const int32_t* qweight, const int32_t* qzeros,
+                    const void* scales_f16, const int32_t* expert_ids,
+                    int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t group_size,
+                    void* h, void* workspace, int64_t workspace_bytes, struct ihipStream_t* stream);
+int awq_moe_down(const void* h, int act, const int32_t* qweight, const int32_t* qzeros,
+                 const void* scales_f16, const int32_t* expert_ids, const float* weights,
+                 int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int64_t group_size,
+                 void* y, void* workspace, int64_t workspace_bytes, struct ihipStream_t* stream);
+int awq_moe_mlp(const void* x, int act, const int32_t* up_qweight, const int32_t* up_qzeros,
+                const void* up_scales_f16, const int32_t* down_qweight, const int32_t* down_qzeros,
+                const void* down_scales_f16, const int32_t* expert_ids, const float* weights,
+                int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
+                int64_t group_size, void* y, void* workspace, int64_t workspace_bytes,
+                struct ihipStream_t* stream);
 
 /*
  * Round-to-nearest writer of the GEMM pack: quantise an fp16 weight in groups of

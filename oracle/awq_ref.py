@@ -354,6 +354,77 @@ def moe_gemm_ref(x, qweights, qzeros, scales, expert_ids, topk: int, group_size:
     return y
 
 
+def route_ref(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+    """Routing in float64, one token at a time: (weights [T, topk], ids [T, topk]).
+
+    Scores: softmax or sigmoid of the logits.  Choice: score + bias, larger first, ties to the
+    lower index; a logit of -inf is never chosen.  Groups of E / groups consecutive experts,
+    worth their best choice or the sum of their two best (of one, where only one can be
+    chosen); only the best topk_groups are considered.  Unfilled slots: id -1, weight 0.  A row
+    with a NaN (softmax: or +inf): ids -1, weights NaN."""
+    logits = np.asarray(logits, dtype=np.float64)
+    T, E = logits.shape
+    per = E // groups
+    weights = np.zeros((T, topk))
+    ids = np.full((T, topk), -1, dtype=np.int64)
+    for t in range(T):
+        l = logits[t]
+        if np.isnan(l).any() or (score == "softmax" and np.isposinf(l).any()):
+            weights[t] = np.nan
+            continue
+        open_ = ~np.isneginf(l)
+        if not open_.any():
+            continue
+        with np.errstate(over="ignore", under="ignore"):
+            if score == "softmax":
+                s = np.where(open_, np.exp(l - l.max()), 0.0)
+                s /= s.sum()
+            else:
+                s = 1.0 / (1.0 + np.exp(-l))
+        # Without a bias the order of the scores is that of the logits, also where scores of
+        # different logits round to the same float64.
+        choice = l if bias is None and (groups == 1 or group_top == 1) else s + (0.0 if bias is None else bias)
+        ranked = [e for e in sorted(range(E), key=lambda e: (-choice[e], e)) if open_[e] and not np.isneginf(choice[e])]
+        worth = {}
+        for g in range(groups):
+            mine = [e for e in ranked if e // per == g]
+            if mine:
+                worth[g] = sum(choice[e] for e in mine[:group_top])
+        kept = sorted(worth, key=lambda g: (-worth[g], g))[:topk_groups]
+        chosen = [e for e in ranked if e // per in kept][:topk]
+        if not chosen:
+            continue
+        w = s[chosen]
+        if renormalize:
+            if score == "softmax":  # a quotient: any common factor may be taken out first
+                w = np.exp(l[chosen] - l[chosen].max())
+            else:
+                w = np.exp(np.minimum(l[chosen], 0) - min(l[chosen].max(), 0.0)) / (1.0 + np.exp(-np.abs(l[chosen])))
+            w = w / w.sum()
+        weights[t, :len(chosen)] = w * scale
+        ids[t, :len(chosen)] = chosen
+    return weights, ids
+
+
+def gate_up_ref(x, qweights, qzeros, scales, expert_ids, topk: int, group_size: int) -> np.ndarray:
+    """h[s] = silu(gate) * up in float64, gate and up the two halves of moe_gemm_ref's columns."""
+    both = moe_gemm_ref(x, qweights, qzeros, scales, expert_ids, topk, group_size)
+    gate, up = np.split(both, 2, axis=1)
+    with np.errstate(over="ignore"):
+        return gate / (1.0 + np.exp(-gate)) * up
+
+
+def down_ref(h, qweights, qzeros, scales, expert_ids, weights, topk: int, group_size: int) -> np.ndarray:
+    """y[t] = sum over j of weights[t, j] * (h[t topk + j] . W) in float64; slots with an id
+    outside the experts add nothing."""
+    ids = np.asarray(expert_ids).astype(np.int64).ravel()
+    E = np.asarray(qweights).shape[0]
+    v = moe_gemm_ref(h, qweights, qzeros, scales, ids, 1, group_size)
+    w = np.where((ids >= 0) & (ids < E), np.asarray(weights, dtype=np.float64).ravel(), 0.0)
+    return (v * w[:, None]).reshape(ids.size // topk, topk, -1).sum(axis=1)
+
+
 def quantize_rtn(W, group_size: int, sym: bool = False):
     """Round-to-nearest writer: fp16 W [K, N] -> (qweight [K, N/8], qzeros [G, N/8],
     scales fp16 [G, N]) in the GEMM layout, so that dequant_ref gives back

@@ -19,6 +19,9 @@ AWQ_ERR_ALIGN = -4
 AWQ_ERR_UNSUPPORTED = -5
 AWQ_ERR_HIP = -6
 
+AWQ_F16, AWQ_BF16, AWQ_F32 = 0, 1, 2  # enum awq_type
+AWQ_SOFTMAX, AWQ_SIGMOID = 0, 1  # enum awq_score
+
 # Every function include/awq_w4a16.h declares, with its ctypes signature.
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -34,6 +37,12 @@ SIGNATURES = {
     "awq_moe_tiles": (ctypes.c_int64, [_i64, _i64, _i64]),
     "awq_moe_align": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "awq_moe_gemm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp]),
+    "awq_moe_route": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _i64, ctypes.c_int,
+                                     _i64, ctypes.c_int, ctypes.c_float, _vp, _vp, _vp]),
+    "awq_moe_workspace": (ctypes.c_int64, [_i64] * 7),
+    "awq_moe_gate_up": (ctypes.c_int, [_vp, ctypes.c_int] + [_vp] * 4 + [_i64] * 6 + [_vp, _vp, _i64, _vp]),
+    "awq_moe_down": (ctypes.c_int, [_vp, ctypes.c_int] + [_vp] * 5 + [_i64] * 6 + [_vp, _vp, _i64, _vp]),
+    "awq_moe_mlp": (ctypes.c_int, [_vp, ctypes.c_int] + [_vp] * 8 + [_i64] * 7 + [_vp, _vp, _i64, _vp]),
     "awq_gemm_bf16": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
     "awq_gemm_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
     "awq_gemm_plan": (ctypes.c_int, [_i64, _i64, _i64, _i64,

@@ -404,6 +404,151 @@ int awq_moe_gemm(const void* x_f16, const int32_t* qweight, const int32_t* qzero
   return e == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
 }
 
+int awq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int64_t row_stride, const float* bias,
+                  int score, int64_t groups, int64_t topk_groups, int group_top, int64_t topk, int renormalize,
+                  float scale, float* weights, int32_t* expert_ids, struct ihipStream_t* stream) {
+  const int st = plan_route(T, E, row_stride, groups, topk_groups, group_top, topk);
+  if (st != AWQ_OK) return st;
+  if (logits_type != AWQ_F16 && logits_type != AWQ_BF16 && logits_type != AWQ_F32) return AWQ_ERR_UNSUPPORTED;
+  if (score != AWQ_SOFTMAX && score != AWQ_SIGMOID) return AWQ_ERR_UNSUPPORTED;
+  if (T == 0) return AWQ_OK;
+  if (!logits || !weights || !expert_ids) return AWQ_ERR_NULL;
+  const uintptr_t unit = logits_type == AWQ_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % unit != 0 || reinterpret_cast<uintptr_t>(bias) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(weights) % 4 != 0 || reinterpret_cast<uintptr_t>(expert_ids) % 4 != 0)
+    return AWQ_ERR_ALIGN;
+  RouteArgs a;
+  a.logits = logits;
+  a.bias = bias;
+  a.weights = weights;
+  a.ids = expert_ids;
+  a.T = T;
+  a.row_stride = row_stride;
+  a.E = (int)E;
+  a.type = logits_type;
+  a.topk = (int)topk;
+  a.groups = (int)groups;
+  a.topk_groups = (int)topk_groups;
+  a.group_top = group_top;
+  a.softmax = score == AWQ_SOFTMAX;
+  a.renormalize = renormalize != 0;
+  a.scale = scale;
+  return awq::launch_route(a, stream) == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
+}
+
+int64_t awq_moe_workspace(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
+                          int64_t group_size) {
+  if (K < 0 || N < 0 || (K == 0 && N == 0)) return AWQ_ERR_SHAPE;
+  ExpertsPlan p;
+  const int st = plan_experts(T, topk, E, K, inner, N, group_size, K > 0, N > 0, p);
+  return st == AWQ_OK ? p.workspace_bytes() : st;
+}
+
+namespace {
+
+// The packed weight of one half: [E, K, n] as the header lays it out.
+struct Packed {
+  const int32_t *qweight, *qzeros;
+  const void* scales;
+  int check() const {
+    if (!qweight || !qzeros || !scales) return AWQ_ERR_NULL;
+    return aligned16(qweight) && aligned16(qzeros) && aligned16(scales) ? AWQ_OK : AWQ_ERR_ALIGN;
+  }
+};
+
+// The gated half (up), the second half (down), or both with h between them in the workspace.
+int experts_common(const void* x, int act, const Packed* up, const Packed* down, const int32_t* ids,
+                   const float* weights, int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
+                   int64_t group_size, void* out, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  ExpertsPlan p;
+  int st = plan_experts(T, topk, E, K, inner, N, group_size, up != nullptr, down != nullptr, p);
+  if (st != AWQ_OK) return st;
+  if (act != AWQ_F16 && act != AWQ_BF16) return AWQ_ERR_UNSUPPORTED;
+  if (T == 0) return AWQ_OK;
+  if (!x || !ids || !out || !workspace || (down && !weights)) return AWQ_ERR_NULL;
+  for (const Packed* w : {up, down})
+    if (w && (st = w->check()) != AWQ_OK) return st;
+  if (!aligned16(x) || !aligned16(out) || !aligned16(workspace)) return AWQ_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(ids) % 4 != 0 || reinterpret_cast<uintptr_t>(weights) % 4 != 0) return AWQ_ERR_ALIGN;
+  if (workspace_bytes < p.workspace_bytes()) return AWQ_ERR_UNSUPPORTED;
+
+  const int64_t S = T * topk;
+  char* ws = static_cast<char*>(workspace);
+  const ExpertTilePlan& first = up ? p.up : p.down;
+  int32_t* table = reinterpret_cast<int32_t*>(ws);
+  int32_t* offsets = table + 4 * first.tiles;
+  int32_t* sorted = offsets + E + 1;
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.sorted_bytes);
+  float* sums = reinterpret_cast<float*>(ws + p.sorted_bytes + p.h_bytes);
+  ExpertProduct q{};
+  q.ids = ids;
+  q.S = (int)S;
+  q.E = (int)E;
+  q.bf16 = act == AWQ_BF16;
+  hipError_t e = awq::launch_moe_align(ids, (int)S, (int)E, first.block_rows, (int)first.tiles, offsets, sorted,
+                                       table, stream);
+  if (e == hipSuccess && up) {
+    q.x = static_cast<const uint16_t*>(x);
+    q.row_div = (int)topk;
+    q.qweight = reinterpret_cast<const uint32_t*>(up->qweight);
+    q.qzeros = reinterpret_cast<const uint32_t*>(up->qzeros);
+    q.scales = static_cast<const uint16_t*>(up->scales);
+    q.K = (int)K;
+    q.N = (int)inner;
+    q.g = eff_group(K, group_size);
+    q.gated = true;
+    q.h = down ? h : static_cast<uint16_t*>(out);
+    e = awq::launch_expert_tiles(q, p.up, sorted, table, stream);
+  }
+  if (e == hipSuccess && down) {
+    q.x = up ? h : static_cast<const uint16_t*>(x);
+    q.row_div = 1;
+    q.qweight = reinterpret_cast<const uint32_t*>(down->qweight);
+    q.qzeros = reinterpret_cast<const uint32_t*>(down->qzeros);
+    q.scales = static_cast<const uint16_t*>(down->scales);
+    q.K = (int)inner;
+    q.N = (int)N;
+    q.g = eff_group(inner, group_size);
+    q.gated = false;
+    q.sums = sums;
+    e = awq::launch_expert_tiles(q, p.down, sorted, table, stream);
+    if (e == hipSuccess)
+      e = awq::launch_expert_combine(sums, ids, weights, (int)T, (int)topk, (int)E, (int)N, q.bf16,
+                                     static_cast<uint16_t*>(out), stream);
+  }
+  return e == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
+}
+
+}  // namespace
+
+int awq_moe_gate_up(const void* x, int act, const int32_t* qweight, const int32_t* qzeros, const void* scales_f16,
+                    const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner,
+                    int64_t group_size, void* h, void* workspace, int64_t workspace_bytes,
+                    struct ihipStream_t* stream) {
+  const Packed up{qweight, qzeros, scales_f16};
+  return experts_common(x, act, &up, nullptr, expert_ids, nullptr, T, topk, E, K, inner, 0, group_size, h, workspace,
+                        workspace_bytes, stream);
+}
+
+int awq_moe_down(const void* h, int act, const int32_t* qweight, const int32_t* qzeros, const void* scales_f16,
+                 const int32_t* expert_ids, const float* weights, int64_t T, int64_t topk, int64_t E, int64_t K,
+                 int64_t N, int64_t group_size, void* y, void* workspace, int64_t workspace_bytes,
+                 struct ihipStream_t* stream) {
+  const Packed down{qweight, qzeros, scales_f16};
+  return experts_common(h, act, nullptr, &down, expert_ids, weights, T, topk, E, 0, K, N, group_size, y, workspace,
+                        workspace_bytes, stream);
+}
+
+int awq_moe_mlp(const void* x, int act, const int32_t* up_qweight, const int32_t* up_qzeros,
+                const void* up_scales_f16, const int32_t* down_qweight, const int32_t* down_qzeros,
+                const void* down_scales_f16, const int32_t* expert_ids, const float* weights, int64_t T, int64_t topk,
+                int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size, void* y, void* workspace,
+                int64_t workspace_bytes, struct ihipStream_t* stream) {
+  const Packed up{up_qweight, up_qzeros, up_scales_f16}, down{down_qweight, down_qzeros, down_scales_f16};
+  return experts_common(x, act, &up, &down, expert_ids, weights, T, topk, E, K, inner, N, group_size, y, workspace,
+                        workspace_bytes, stream);
+}
+
 int awq_gemm(const void* x_f16, const int32_t* qweight, const int32_t* qzeros, const void* scales_f16,
              const void* bias_f16, int64_t M, int64_t K, int64_t N, int64_t group_size, void* y_f16,
              struct ihipStream_t* stream) {

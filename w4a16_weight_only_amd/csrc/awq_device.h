@@ -129,6 +129,35 @@ __device__ __forceinline__ uint32_t zero_code(uint32_t zw, int j) {
 
 __device__ __forceinline__ half2v splat(_Float16 v) { return half2v{v, v}; }
 
+// 16 bytes per lane from global memory straight into LDS (global_load_lds_dwordx4):
+// lane l's data lands at lds + 16 l; lds must be the same for the whole wave.  Issued
+// as inline assembly, so the compiler does not track these loads: the kernel waits for
+// them itself (vmcnt) before anyone reads what they wrote.  M0 takes the LDS byte
+// address (the low 32 bits of the generic address of a __shared__ object).
+__device__ __forceinline__ void load_lds16(const void* src, const void* lds) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)));
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(m0)
+               : "memory", "m0");
+}
+
+// The same load from a wave-uniform 64-bit base (scalar registers) plus a 32-bit
+// per-lane byte offset: the base advances with scalar adds, so the per-load address
+// math stays off the vector ALU.
+__device__ __forceinline__ void load_lds16_s(const void* sbase, uint32_t voff, const void* lds) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(m0)
+               : "memory", "m0");
+}
+
+// MFMA of one 32x32x16 block; a and b hold fp16 or (BF16) bfloat16 bit patterns.
+template <bool BF16>
+__device__ __forceinline__ floatx16 mfma32(const half8v& a, const half8v& b, const floatx16& c) {
+  if constexpr (BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
 // ---- Split-K sums in 64-bit fixed point, one word per output element.
 // Each of the `splits` workgroups that share an output element adds its fp32 partial p
 // with one returning atomic; the word is zero between calls (the workgroup that

@@ -82,4 +82,43 @@ hipError_t launch_tile(const uint16_t* x, const int32_t* qweight, const int32_t*
                        const uint16_t* scales, const uint16_t* bias, int M, int K, int N, int g,
                        const TilePlan& p, bool bf16, float* partial, uint16_t* y, hipStream_t stream);
 
+// Routing of tokens to experts (awq_moe_route): logits [T, E] of type 0 fp16, 1 bfloat16,
+// 2 fp32, rows row_stride elements apart; weights fp32 and ids int32 [T, topk].
+struct RouteArgs {
+  const void* logits;
+  const float* bias;  // [E] or NULL
+  float* weights;
+  int32_t* ids;
+  int64_t T, row_stride;
+  int E, type, topk, groups, topk_groups, group_top;
+  bool softmax, renormalize;
+  float scale;
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+
+// One product of routed rows with their experts' weights (awq_moe_gate_up, awq_moe_down).
+// Slot s of the S routed slots multiplies row s / row_div of x by the weight of expert
+// ids[s]: N output columns, or, gated, N pairs of columns (n, N + n) of a 2 N wide weight,
+// which leave as silu(first) * second in h [S, N] (rounded to the activation type).  Without
+// the gate the fp32 products go to sums [S, N].  Slots with an id outside [0, E) are not
+// written.
+struct ExpertProduct {
+  const uint16_t* x;
+  const uint32_t* qweight;
+  const uint32_t* qzeros;
+  const uint16_t* scales;
+  const int32_t* ids;
+  int row_div, S, E, K, N, g;
+  bool gated, bf16;
+  uint16_t* h;
+  float* sums;
+};
+// Row tiles over slots sorted by expert (table and sorted as launch_moe_align gives them).
+hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertTilePlan& tp, const int32_t* sorted,
+                               const int32_t* table, hipStream_t stream);
+// y[t, n] = sum over j of weights[t, j] * sums[t topk + j, n], in the order of j, over the
+// slots with an id in [0, E); rounded once to the activation type.
+hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
+                                 int N, bool bf16, uint16_t* y, hipStream_t stream);
+
 }  // namespace awq

@@ -446,6 +446,66 @@ int plan_moe(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int64_t g
   return AWQ_OK;
 }
 
+int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t topk_groups, int group_top,
+               int64_t topk) {
+  if (T < 0 || E < 1 || row_stride < E || groups < 1 || topk < 1 || topk_groups < 1) return AWQ_ERR_SHAPE;
+  if (E % groups != 0 || topk_groups > groups || (group_top != 1 && group_top != 2)) return AWQ_ERR_SHAPE;
+  if (topk > topk_groups * (E / groups)) return AWQ_ERR_SHAPE;
+  if (E > 1024 || topk > kRouteMaxTopk || groups > kRouteMaxGroups || T > kMaxDim) return AWQ_ERR_UNSUPPORTED;
+  if (row_stride > (int64_t(1) << 40)) return AWQ_ERR_UNSUPPORTED;
+  return AWQ_OK;
+}
+
+namespace {
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+int plan_expert_tiles(int64_t S, int64_t E, int64_t N, bool gated, ExpertTilePlan& p) {
+  const int64_t cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
+  p.block_rows = kExpertTileRows;
+  p.tiles = moe_tiles(S, E, p.block_rows);
+  p.grid = p.tiles * ((N + cols - 1) / cols);
+  p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
+  return grid_fits(p.grid, 1, 256) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
+                 bool up, bool down, ExpertsPlan& p) {
+  p = ExpertsPlan{};
+  if (T < 0 || topk < 1 || E < 1) return AWQ_ERR_SHAPE;
+  if (inner < 1 || inner > kMaxDim) return inner < 1 ? AWQ_ERR_SHAPE : AWQ_ERR_UNSUPPORTED;
+  if (T > kMaxDim || topk > kMaxDim || E > 1024) return AWQ_ERR_UNSUPPORTED;
+  const int64_t S = T * topk;
+  if (up) {
+    const int st = limits_check(S, K, 2 * inner, group_size);
+    if (st != AWQ_OK) return st;
+    if (inner % 32 != 0) return AWQ_ERR_UNSUPPORTED;  // the halves meet on a whole 16-byte piece
+    if (T * K * 2 >= k2p32) return AWQ_ERR_UNSUPPORTED;  // gathered rows use 32-bit offsets
+  }
+  if (down) {
+    const int st = limits_check(S, inner, N, group_size);
+    if (st != AWQ_OK) return st;
+    if (S * inner * 2 >= k2p32) return AWQ_ERR_UNSUPPORTED;
+    if (T * (N / 4) + 256 >= k2p32) return AWQ_ERR_UNSUPPORTED;  // one thread per four outputs
+  }
+  if (T == 0) return AWQ_OK;
+  if (up) {
+    const int st = plan_expert_tiles(S, E, inner, true, p.up);
+    if (st != AWQ_OK) return st;
+    p.sorted_bytes = p.up.table_bytes;
+    if (down) p.h_bytes = round_up(S * inner * 2, 256);
+  }
+  if (down) {
+    const int st = plan_expert_tiles(S, E, N, false, p.down);
+    if (st != AWQ_OK) return st;
+    p.sorted_bytes = p.down.table_bytes;
+    p.sums_bytes = round_up(S * N * 4, 256);
+  }
+  return AWQ_OK;
+}
+
 int plan_rtn(int64_t K, int64_t N, int64_t group_size, int sym, RtnPlan& p) {
   p = RtnPlan{};
   const int st = format_check(K, N, group_size);

@@ -174,4 +174,32 @@ int64_t moe_tiles(int64_t S, int64_t E, int64_t block_rows);
 // Every check of awq_moe_gemm's sizes and, for T > 0, its plan.
 int plan_moe(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int64_t group_size, int cus, MoePlan& mp);
 
+// awq_moe_route: at most kRouteMaxTopk experts a token and kRouteMaxGroups groups.
+constexpr int64_t kRouteMaxTopk = 64;
+constexpr int64_t kRouteMaxGroups = 64;
+int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t topk_groups, int group_top,
+               int64_t topk);
+
+// One product of routed rows with their experts' weights (gated: N pairs of columns of a
+// 2 N wide weight), over slots sorted by expert in row tiles of block_rows.
+struct ExpertTilePlan {
+  int block_rows = 0;
+  int64_t tiles = 0;    // table entries
+  int64_t grid = 0;     // workgroups
+  int64_t table_bytes = 0;  // table, offsets and sorted slots
+};
+constexpr int kExpertTileRows = 128;
+constexpr int kExpertTileCols = 256;  // weight columns of a workgroup
+// The gated MLP of routed experts and its two halves: which products it makes, and the
+// caller's workspace, in this order: the slots sorted by expert, h of the first product (mlp)
+// and the fp32 sums of the second.
+struct ExpertsPlan {
+  ExpertTilePlan up, down;
+  int64_t sorted_bytes = 0, h_bytes = 0, sums_bytes = 0;
+  int64_t workspace_bytes() const { return sorted_bytes + h_bytes + sums_bytes; }
+};
+// K -> I gated (up) and K2 -> N (down) halves; a half that is not there has N = 0.
+int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
+                 bool up, bool down, ExpertsPlan& p);
+
 }  // namespace awq
