@@ -25,8 +25,8 @@ PROBE_PATH = os.path.join(HERE, "libawq_probe.so")
 # for the sanitizer sweep of the planner).
 HOST_SOURCES = ["awq_plan.cpp"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
-SOURCES = ["awq_api.hip", "awq_decode.hip", "awq_dequant.hip", "awq_experts.hip", "awq_moe.hip", "awq_quant.hip",
-           "awq_route.hip", "awq_skinny.hip", "awq_tile.hip"]
+SOURCES = ["awq_api.hip", "awq_decode.hip", "awq_dequant.hip", "awq_experts.hip", "awq_experts_stream.hip",
+           "awq_moe.hip", "awq_quant.hip", "awq_route.hip", "awq_skinny.hip", "awq_tile.hip"]
 ARCH = "gfx950"
 
 

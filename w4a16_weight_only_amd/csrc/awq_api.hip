@@ -440,7 +440,7 @@ int64_t awq_moe_workspace(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t
                           int64_t group_size) {
   if (K < 0 || N < 0 || (K == 0 && N == 0)) return AWQ_ERR_SHAPE;
   ExpertsPlan p;
-  const int st = plan_experts(T, topk, E, K, inner, N, group_size, K > 0, N > 0, p);
+  const int st = plan_experts(T, topk, E, K, inner, N, group_size, query_cus(), K > 0, N > 0, p);
   return st == AWQ_OK ? p.workspace_bytes() : st;
 }
 
@@ -461,7 +461,7 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
                    const float* weights, int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
                    int64_t group_size, void* out, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   ExpertsPlan p;
-  int st = plan_experts(T, topk, E, K, inner, N, group_size, up != nullptr, down != nullptr, p);
+  int st = plan_experts(T, topk, E, K, inner, N, group_size, query_cus(), up != nullptr, down != nullptr, p);
   if (st != AWQ_OK) return st;
   if (act != AWQ_F16 && act != AWQ_BF16) return AWQ_ERR_UNSUPPORTED;
   if (T == 0) return AWQ_OK;
@@ -474,10 +474,6 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
 
   const int64_t S = T * topk;
   char* ws = static_cast<char*>(workspace);
-  const ExpertTilePlan& first = up ? p.up : p.down;
-  int32_t* table = reinterpret_cast<int32_t*>(ws);
-  int32_t* offsets = table + 4 * first.tiles;
-  int32_t* sorted = offsets + E + 1;
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.sorted_bytes);
   float* sums = reinterpret_cast<float*>(ws + p.sorted_bytes + p.h_bytes);
   ExpertProduct q{};
@@ -485,35 +481,50 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
   q.S = (int)S;
   q.E = (int)E;
   q.bf16 = act == AWQ_BF16;
-  hipError_t e = awq::launch_moe_align(ids, (int)S, (int)E, first.block_rows, (int)first.tiles, offsets, sorted,
-                                       table, stream);
-  if (e == hipSuccess && up) {
+  q.sums = sums;
+  // Slots sorted by expert, in blocks of the product's rows; kept for the next product where
+  // that takes the same blocks.
+  int sorted_for = 0;
+  auto product = [&](const Packed& w, const ExpertPlan& ep) {
+    q.qweight = reinterpret_cast<const uint32_t*>(w.qweight);
+    q.qzeros = reinterpret_cast<const uint32_t*>(w.qzeros);
+    q.scales = static_cast<const uint16_t*>(w.scales);
+    int32_t* table = reinterpret_cast<int32_t*>(ws);
+    int32_t* offsets = table + 4 * ep.tiles;
+    int32_t* sorted = offsets + E + 1;
+    if (ep.ranked) return awq::launch_expert_stream(q, ep, nullptr, nullptr, stream);
+    if (sorted_for != ep.block_rows) {
+      const hipError_t e = awq::launch_moe_align(ids, (int)S, (int)E, ep.block_rows, (int)ep.tiles, offsets, sorted,
+                                                 table, stream);
+      if (e != hipSuccess) return e;
+      sorted_for = ep.block_rows;
+    }
+    return ep.stream ? awq::launch_expert_stream(q, ep, sorted, table, stream)
+                     : awq::launch_expert_tiles(q, ep, sorted, table, stream);
+  };
+  hipError_t e = hipSuccess;
+  if (up) {
     q.x = static_cast<const uint16_t*>(x);
     q.row_div = (int)topk;
-    q.qweight = reinterpret_cast<const uint32_t*>(up->qweight);
-    q.qzeros = reinterpret_cast<const uint32_t*>(up->qzeros);
-    q.scales = static_cast<const uint16_t*>(up->scales);
     q.K = (int)K;
     q.N = (int)inner;
     q.g = eff_group(K, group_size);
     q.gated = true;
     q.h = down ? h : static_cast<uint16_t*>(out);
-    e = awq::launch_expert_tiles(q, p.up, sorted, table, stream);
+    e = product(*up, p.up);
+    if (e == hipSuccess && p.up.splits > 1)
+      e = awq::launch_expert_gate(sums, ids, (int)S, (int)E, (int)inner, p.up.splits, q.bf16, q.h, stream);
   }
   if (e == hipSuccess && down) {
     q.x = up ? h : static_cast<const uint16_t*>(x);
     q.row_div = 1;
-    q.qweight = reinterpret_cast<const uint32_t*>(down->qweight);
-    q.qzeros = reinterpret_cast<const uint32_t*>(down->qzeros);
-    q.scales = static_cast<const uint16_t*>(down->scales);
     q.K = (int)inner;
     q.N = (int)N;
     q.g = eff_group(inner, group_size);
     q.gated = false;
-    q.sums = sums;
-    e = awq::launch_expert_tiles(q, p.down, sorted, table, stream);
+    e = product(*down, p.down);
     if (e == hipSuccess)
-      e = awq::launch_expert_combine(sums, ids, weights, (int)T, (int)topk, (int)E, (int)N, q.bf16,
+      e = awq::launch_expert_combine(sums, ids, weights, (int)T, (int)topk, (int)E, (int)N, p.down.splits, q.bf16,
                                      static_cast<uint16_t*>(out), stream);
   }
   return e == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;

@@ -27,9 +27,6 @@ constexpr int kThreads = 256;
 constexpr int kFM = 2, kFN = 4;  // 32 x 32 blocks of a wave: 64 rows x 128 columns
 constexpr int kWaveRows = 32 * kFM;
 
-// silu(g) u.
-__device__ __forceinline__ float gate(float g, float u) { return g / (1.f + __expf(-g)) * u; }
-
 // LDS rows of the staged integers: column c's 64 k values take 128 bytes, 16-byte chunk o at
 // position o ^ b_swz(c) of row b_row(c).  Writers hold one chunk of columns 8 w + j for 16
 // consecutive w at a time and readers one chunk of 16 consecutive columns: both reach all
@@ -244,7 +241,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(const ExpertPr
           const int n = n0 + tcol(j) + lc;
           if (n < N)
             p.h[slot * N + n] =
-                float_to_act<BF16>(gate(acc[i][j][r] * unit[j], acc[i][j + kFN / 2][r] * unit[j + kFN / 2]));
+                float_to_act<BF16>(gated(acc[i][j][r] * unit[j], acc[i][j + kFN / 2][r] * unit[j + kFN / 2]));
         }
       } else {
 #pragma unroll
@@ -256,7 +253,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(const ExpertPr
     }
 }
 
-hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertTilePlan& tp, const int32_t* sorted,
+hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertPlan& tp, const int32_t* sorted,
                                const int32_t* table, hipStream_t stream) {
   const int cols = p.gated ? kCols / 2 : kCols;
   const int n_tiles = (p.N + cols - 1) / cols;
@@ -274,36 +271,59 @@ hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertTilePlan& tp,
   return hipGetLastError();
 }
 
-// y[t] = sum over j of weights[t, j] * sums[t topk + j]: one thread per four columns, the
-// slots in order, so the bits do not depend on the schedule.
-template <bool BF16>
+// y[t] = sum over j of weights[t, j] * (sum over splits of sums[split][t topk + j]).  A
+// workgroup takes 256 / PARTS groups of four columns; PARTS threads share one, each adding
+// every PARTS-th (slot, split) term in order, and meet in LDS in order: the bits do not
+// depend on the schedule.  PARTS > 1 where there are few columns in all, so that the loads of
+// a column group are in flight together.
+template <bool BF16, int PARTS>
 __global__ __launch_bounds__(256) void expert_combine_kernel(const float* __restrict__ sums,
                                                              const int32_t* __restrict__ ids,
-                                                             const float* __restrict__ weights, int64_t quads,
-                                                             int topk, int E, int N, uint16_t* __restrict__ y) {
+                                                             const float* __restrict__ weights, int64_t quads, int S,
+                                                             int topk, int E, int N, int splits,
+                                                             uint16_t* __restrict__ y) {
   typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (q >= quads) return;
+  __shared__ floatx4 meet[PARTS > 1 ? 256 : 1];
+  const int part = threadIdx.x % PARTS;
+  const int64_t q_raw = (int64_t)blockIdx.x * (256 / PARTS) + threadIdx.x / PARTS;
+  const int64_t q = q_raw < quads ? q_raw : quads - 1;
   const int64_t t = q / (N / 4);
   const int n = 4 * (int)(q - t * (N / 4));
   floatx4 a = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < topk; ++j) {
+#pragma unroll 4
+  for (int i = part; i < topk * splits; i += PARTS) {
+    const int j = i / splits, sp = i - j * splits;
     const int64_t s = t * topk + j;
     const int e = ids[s];
-    if (e >= 0 && e < E) a += weights[s] * *reinterpret_cast<const floatx4*>(sums + s * N + n);
+    if (e >= 0 && e < E) a += weights[s] * *reinterpret_cast<const floatx4*>(sums + ((int64_t)sp * S + s) * N + n);
   }
-  *reinterpret_cast<u32x2_t*>(y + t * N + n) = u32x2_t{pack_act2<BF16>(a[0], a[1]), pack_act2<BF16>(a[2], a[3])};
+  if constexpr (PARTS > 1) {
+    meet[threadIdx.x] = a;
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i) a += meet[threadIdx.x + i];
+  }
+  if (q_raw < quads)
+    *reinterpret_cast<u32x2_t*>(y + t * N + n) = u32x2_t{pack_act2<BF16>(a[0], a[1]), pack_act2<BF16>(a[2], a[3])};
 }
 
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
-                                 int N, bool bf16, uint16_t* y, hipStream_t stream) {
+                                 int N, int splits, bool bf16, uint16_t* y, hipStream_t stream) {
   const int64_t quads = (int64_t)T * (N / 4);
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, sums, ids, weights, quads,
-                       topk, E, N, y);
+  auto go = [&](auto kern, int parts) {
+    const int64_t per = 256 / parts;
+    hipLaunchKernelGGL(kern, dim3((unsigned)((quads + per - 1) / per)), dim3(256), 0, stream, sums, ids, weights,
+                       quads, T * topk, topk, E, N, splits, y);
   };
-  if (bf16) go(expert_combine_kernel<true>);
-  else go(expert_combine_kernel<false>);
+  const bool few = quads * 8 <= 65536 && topk * splits > 2;  // fewer threads than the card holds
+  if (bf16) {
+    if (few) go(expert_combine_kernel<true, 8>, 8);
+    else go(expert_combine_kernel<true, 1>, 1);
+  } else {
+    if (few) go(expert_combine_kernel<false, 8>, 8);
+    else go(expert_combine_kernel<false, 1>, 1);
+  }
   return hipGetLastError();
 }
 

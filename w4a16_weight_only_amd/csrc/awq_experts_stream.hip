@@ -1,0 +1,375 @@
+// Few rows per routed expert: bandwidth-bound streaming of the experts' packed weights.
+//
+// A workgroup takes up to 16 routed rows of one expert (an entry), 256 columns (gated: the
+// same 256 of both halves) and one K split.  Its four waves each take a run of 32-row
+// k-steps; gated, even waves take the gate's columns and odd ones the up projection's.  On
+// v_mfma_f32_16x16x32 lane l = 16 q + c loads words 2 c, 2 c + 1 of rows 8 q .. 8 q + 7 (16
+// lanes: 128 contiguous bytes of a row) and unpacks them into operands of exact integers, 16
+// columns x 8 rows; its row of x is row l % 16 of the entry.
+//   fp16       operand q - z
+//   bfloat16   (no packed bfloat16 addition on this chip) operand 128 + q, and one more MFMA
+//              against ones for the rows' sums of x:  x . (128 + q) - (128 + z) x . 1
+// The running sums are in units of the current group's scale u: a group boundary multiplies
+// them by u / u' (a second set of 64 accumulator registers, scaled group by group, spills).
+// A scale of zero cannot be a unit: the unit stays, and the column's sums are put aside in LDS
+// when such a group begins and taken back when it ends (rare; a loop body with zeroed operands
+// would cost every group registers).
+// Group data (zeros and scales) comes with the first k-step of a group in the same ring of
+// two k-steps, so a wave never waits for it alone.
+// The waves meet in LDS.  With one split a gated workgroup writes h; otherwise fp32 sums
+// [split][slot][column] leave for the next kernel, which adds the splits in order.
+//
+// Which rows a workgroup has: up to 64 slots, every wave ranks them itself (one slot per
+// lane); above, the table of launch_moe_align in blocks of 16 rows.
+#include "awq_device.h"
+#include "awq_kernels.h"
+
+namespace awq {
+
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kPF = 2;           // k-steps in flight per wave
+constexpr int kYld = kExpertStreamCols + 4;  // floats of a staged output row
+
+// Entry v of a lane's 16 columns: word v / 8, byte (v / 2) % 4, nibble v % 2.
+__device__ constexpr int col_of(int v) { return (v & 1) ? hi_col((v >> 1) & 3) : lo_col((v >> 1) & 3); }
+
+struct Step {
+  u32x2 w[8];        // rows 8 q .. 8 q + 7
+  half8v x;          // x[row][8 q ..]
+  u32x2 z;           // group data, with the first k-step of a group (or of the run)
+  half8v s0, s1;
+};
+
+// The 16 MFMAs of a k-step.
+template <bool BF16>
+__device__ __forceinline__ void multiply(const Step& st, const uint32_t (&zs)[16], const UnpackConsts& uk,
+                                         floatx4 (&part)[16], floatx4& sx) {
+  if constexpr (BF16) {
+    const uint32_t one2 = 0x3F803F80u;  // bfloat16 pair (1, 1)
+    sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.x),
+                                                 __builtin_bit_cast(bf16x8, u32x4{one2, one2, one2, one2}), sx, 0, 0,
+                                                 0);
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      u32x4 lo, hi;
+      const int il = 8 * w + 2 * t, ih = il + 1;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t ra = st.w[2 * p][w], rb = st.w[2 * p + 1][w];
+        uint32_t pb;
+        if (t == 0) pb = pair_byte<0>(ra, rb);
+        else if (t == 1) pb = pair_byte<1>(ra, rb);
+        else if (t == 2) pb = pair_byte<2>(ra, rb);
+        else pb = pair_byte<3>(ra, rb);
+        lo[p] = BF16 ? lo_magic_bf16(pb, uk) : as_u32(lo_minus_zero(pb, as_h2(zs[il]), uk));
+        hi[p] = BF16 ? hi_magic_bf16(pb, uk) : as_u32(hi_minus_zero(pb, as_h2(zs[ih]), uk));
+      }
+      if constexpr (BF16) {
+        const bf16x8 x = __builtin_bit_cast(bf16x8, st.x);
+        part[il] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, lo), part[il], 0, 0, 0);
+        part[ih] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, hi), part[ih], 0, 0, 0);
+      } else {
+        part[il] = __builtin_amdgcn_mfma_f32_16x16x32_f16(st.x, __builtin_bit_cast(half8v, lo), part[il], 0, 0, 0);
+        part[ih] = __builtin_amdgcn_mfma_f32_16x16x32_f16(st.x, __builtin_bit_cast(half8v, hi), part[ih], 0, 0, 0);
+      }
+    }
+}
+
+// Rows of a workgroup's entry: its expert, how many, and their slots (LDS).
+struct Entry {
+  int expert, rows;
+};
+
+// Entries of at most 64 slots, ranked by each wave (lane l: slot l): the slots of an expert,
+// in order, in blocks of 16; entries in the order of their first slot.  rows 0: no such entry.
+__device__ __forceinline__ Entry rank_entry(const int32_t* ids, int S, int E, int entry, int lane, int32_t* slots) {
+  const int id = lane < S ? ids[lane] : -1;
+  const bool routed = id >= 0 && id < E;
+  int rank = 0;  // among the lower slots of the same expert
+  for (int j = 0; j < S; ++j) rank += (j < lane && __builtin_amdgcn_readlane(id, j) == id) ? 1 : 0;
+  uint64_t leads = __ballot(routed && (rank & 15) == 0);
+  if (entry >= __builtin_popcountll(leads)) return Entry{0, 0};
+  for (int i = 0; i < entry; ++i) leads &= leads - 1;
+  const int lead = __builtin_ctzll(leads);
+  const int expert = __builtin_amdgcn_readlane(id, lead);
+  const int first = __builtin_amdgcn_readlane(rank, lead);
+  const bool mine = routed && id == expert && rank >= first && rank < first + 16;
+  if (mine) slots[rank - first] = lane;  // every wave writes the same
+  return Entry{expert, (int)__builtin_popcountll(__ballot(mine))};
+}
+
+}  // namespace
+
+// RL: lanes whose sums are kept, 16 per four rows (an entry never has more than RL / 4 rows).
+template <bool GATED, bool BF16, int RL>
+__global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const ExpertProduct p, int entries, int tiles,
+                                                                    int splits, int steps,
+                                                                    const int32_t* __restrict__ sorted,
+                                                                    const int32_t* __restrict__ table) {
+  constexpr int PARTS = GATED ? kWaves / 2 : kWaves;  // waves along K
+  __shared__ union {
+    floatx4 red[kWaves][16][RL];  // [wave][column entry][lane]
+    float ys[RL / 4][GATED ? 2 : 1][kYld];
+  } sh;
+  __shared__ int32_t slots[16];
+
+  // Block order: splits fastest, then column tiles, then entries.
+  const int split = blockIdx.x % splits;
+  const int b = blockIdx.x / splits;
+  const int tile = b % tiles;
+  const int entry = b / tiles;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, c = lane & 15;
+  Entry en;
+  if (table == nullptr) {
+    en = rank_entry(p.ids, p.S, p.E, entry, lane, slots);
+  } else {
+    en.expert = table[4 * entry];
+    en.rows = en.expert < 0 ? 0 : table[4 * entry + 2];
+    if (lane < en.rows) slots[lane] = sorted[table[4 * entry + 1] + lane];
+  }
+  if (en.rows == 0) return;  // the same in every wave
+  __syncthreads();
+
+  const int K = p.K, N = p.N;
+  const int half = GATED ? (wave & 1) : 0;
+  const int part_of = GATED ? wave >> 1 : wave;
+  const int NW = (GATED ? 2 * N : N) >> 3;
+  const int G = K / p.g, gsteps = p.g / 32;
+  const uint32_t* qweight = p.qweight + (int64_t)en.expert * K * NW;
+  const uint32_t* qzeros = p.qzeros + (int64_t)en.expert * G * NW;
+  const uint16_t* scales = p.scales + (int64_t)en.expert * G * NW * 8;
+
+  // Columns past N read the tile's first ones and are not stored.
+  const int wc_in = tile * (kExpertStreamCols / 8) + 2 * c;
+  const int wc = (wc_in < (N >> 3) ? wc_in : tile * (kExpertStreamCols / 8)) + half * (N >> 3);
+  const int xrow = slots[c < en.rows ? c : 0] / p.row_div;
+  const uint32_t x_off = ((uint32_t)xrow * (uint32_t)K + 8u * q) * 2u;
+  const uint32_t row_bytes = (uint32_t)NW * 4u;
+  const uint32_t w_off = (uint32_t)(8 * q) * row_bytes + (uint32_t)wc * 4u;
+  const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint32_t*>(qweight), (short)0, (int)(row_bytes * (uint32_t)K), 0x00020000);
+
+  const int T = K / 32;
+  const int s0 = split * PARTS * steps;
+  const int kb = min(T, s0 + part_of * steps), ke = min(T, kb + steps);
+
+  auto issue = [&](Step& st, int ks) {
+    if (ks == kb || ks % gsteps == 0) {
+      const int64_t at = (int64_t)(ks / gsteps) * NW + wc;
+      st.z = *reinterpret_cast<const u32x2*>(qzeros + at);
+      st.s0 = *reinterpret_cast<const half8v*>(scales + 8 * at);
+      st.s1 = *reinterpret_cast<const half8v*>(scales + 8 * at + 8);
+    }
+    const uint32_t r0 = (uint32_t)ks * 32u;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      st.w[r] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wrs, w_off, (r0 + r) * row_bytes, 2));
+    st.x = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(p.x) + (uint64_t)x_off + r0 * 2u);
+  };
+
+  floatx4 part[16];
+  floatx4 sx = {0.f, 0.f, 0.f, 0.f};
+  uint32_t zs[16];
+  half8v unit[2];    // the columns' current units
+  uint32_t nil = 0;  // columns whose scale is zero in the current group
+  bool any_nil = false;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    part[v] = floatx4{0.f, 0.f, 0.f, 0.f};
+    zs[v] = 0;
+    unit[v >> 3][v & 7] = (_Float16)1.f;
+  }
+  // A group ends: sums of columns without a scale are those from before it.
+  auto leave = [&] {
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+      if constexpr (BF16) part[v] -= __builtin_bit_cast(float, zs[v]) * sx;
+    if (any_nil) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const floatx4 kept = sh.red[wave][v][lane % RL];
+        if ((nil >> v) & 1) part[v] = kept;
+      }
+    }
+  };
+  // A group begins: the sums so far change units (there are none when the run begins).
+  auto enter = [&](const Step& st, bool begin) {
+    nil = 0;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const _Float16 s = v < 8 ? st.s0[col_of(v)] : st.s1[col_of(v)];
+      const _Float16 old = unit[v >> 3][v & 7];
+      const bool none = s == (_Float16)0.f;
+      const _Float16 now = none ? old : s;
+      if (!begin) {
+        part[v] *= (float)old * __builtin_amdgcn_rcpf((float)now);
+      }
+      unit[v >> 3][v & 7] = now;
+      nil |= none ? 1u << v : 0u;
+      const uint32_t z = zero_code(st.z[v >> 3], col_of(v));
+      if constexpr (BF16) {
+        zs[v] = __builtin_bit_cast(uint32_t, 128.0f + (float)z);
+      } else {
+        const uint32_t h = (v & 1) ? (0xD400u | (z << 4)) : (0xE400u | z);  // -(64 + z), -(1024 + z)
+        zs[v] = h | (h << 16);
+      }
+    }
+    sx = floatx4{0.f, 0.f, 0.f, 0.f};
+    any_nil = __builtin_amdgcn_ballot_w64(nil != 0) != 0;
+    if (any_nil && lane < RL) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) sh.red[wave][v][lane] = part[v];
+    }
+  };
+  const UnpackConsts uk = unpack_consts();
+  Step ring[kPF];
+#pragma unroll
+  for (int j = 0; j < kPF; ++j)
+    if (kb + j < ke) issue(ring[j], kb + j);
+  for (int base = kb; base < ke; base += kPF) {
+#pragma unroll
+    for (int j = 0; j < kPF; ++j) {
+      const int ks = base + j;
+      if (ks < ke) {
+        if (ks == kb || ks % gsteps == 0) {
+          if (ks != kb) leave();
+          enter(ring[j], ks == kb);
+        }
+        multiply<BF16>(ring[j], zs, uk, part, sx);
+        if (ks + kPF < ke) issue(ring[j], ks + kPF);
+      }
+    }
+  }
+  if (kb < ke) leave();
+#pragma unroll
+  for (int v = 0; v < 16; ++v) part[v] *= (float)unit[v >> 3][v & 7];
+
+  // Waves -> LDS, then one thread per (column entry, lane of rows): four rows of one column.
+  if (lane < RL) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) sh.red[wave][v][lane] = part[v];
+  }
+  __syncthreads();
+  constexpr int SLOTS = 16 * RL / kThreads;  // sums per thread: 1, 2 or 4
+  floatx4 sum[SLOTS][GATED ? 2 : 1];
+#pragma unroll
+  for (int k = 0; k < SLOTS; ++k) {
+    const int i = tid + k * kThreads;
+    const int v = (i >> 4) & 15, ln = (i >> 8) * 16 + (i & 15);
+#pragma unroll
+    for (int hf = 0; hf < (GATED ? 2 : 1); ++hf) {
+      floatx4 a = sh.red[hf][v][ln];
+#pragma unroll
+      for (int w = 1; w < PARTS; ++w) a += sh.red[GATED ? 2 * w + hf : w][v][ln];
+      sum[k][hf] = a;
+    }
+  }
+  __syncthreads();  // the sums are in registers: their LDS takes the output rows
+  const bool finish = GATED && splits == 1;
+#pragma unroll
+  for (int k = 0; k < SLOTS; ++k) {
+    const int i = tid + k * kThreads;
+    const int v = (i >> 4) & 15, cc = i & 15;
+    const int col = 8 * (2 * cc + (v >> 3)) + col_of(v);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * (i >> 8) + r;
+      if constexpr (GATED) {
+        sh.ys[row][0][col] = finish ? gated(sum[k][0][r], sum[k][1][r]) : sum[k][0][r];
+        sh.ys[row][1][col] = sum[k][1][r];
+      } else {
+        sh.ys[row][0][col] = sum[k][0][r];
+      }
+    }
+  }
+  __syncthreads();
+  const int n0 = tile * kExpertStreamCols;
+  if (finish) {
+    for (int i = tid; i < en.rows * (kExpertStreamCols / 8); i += kThreads) {
+      const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
+      if (n0 + cp < N) {
+        const float* y = &sh.ys[row][0][cp];
+        *reinterpret_cast<u32x4*>(p.h + (int64_t)slots[row] * N + n0 + cp) =
+            u32x4{pack_act2<BF16>(y[0], y[1]), pack_act2<BF16>(y[2], y[3]), pack_act2<BF16>(y[4], y[5]),
+                  pack_act2<BF16>(y[6], y[7])};
+      }
+    }
+  } else {
+    constexpr int HALVES = GATED ? 2 : 1;
+    float* out = p.sums + (int64_t)split * p.S * (HALVES * N);
+    for (int i = tid; i < en.rows * HALVES * (kExpertStreamCols / 4); i += kThreads) {
+      const int row = i / (HALVES * kExpertStreamCols / 4);
+      const int r = i - row * (HALVES * kExpertStreamCols / 4);
+      const int hf = r / (kExpertStreamCols / 4), cp = 4 * (r % (kExpertStreamCols / 4));
+      if (n0 + cp < N)
+        *reinterpret_cast<floatx4*>(out + ((int64_t)slots[row] * HALVES + hf) * N + n0 + cp) =
+            *reinterpret_cast<const floatx4*>(&sh.ys[row][hf][cp]);
+    }
+  }
+}
+
+hipError_t launch_expert_stream(const ExpertProduct& p, const ExpertPlan& ep, const int32_t* sorted,
+                                const int32_t* table, hipStream_t stream) {
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)ep.grid), dim3(kThreads), 0, stream, p, (int)ep.tiles, ep.col_tiles,
+                       ep.splits, ep.steps, sorted, table);
+  };
+#define AWQ_STREAM(GATED, BF16)                                            \
+  do {                                                                     \
+    if (ep.rows == 4) go(expert_stream_kernel<GATED, BF16, 16>);           \
+    else if (ep.rows == 8) go(expert_stream_kernel<GATED, BF16, 32>);      \
+    else go(expert_stream_kernel<GATED, BF16, 64>);                        \
+  } while (0)
+  if (p.gated) {
+    if (p.bf16) AWQ_STREAM(true, true);
+    else AWQ_STREAM(true, false);
+  } else {
+    if (p.bf16) AWQ_STREAM(false, true);
+    else AWQ_STREAM(false, false);
+  }
+#undef AWQ_STREAM
+  return hipGetLastError();
+}
+
+// h = silu(gate) up from the splits' sums [splits][S][2 N], four columns per thread.
+template <bool BF16>
+__global__ __launch_bounds__(256) void expert_gate_kernel(const float* __restrict__ sums,
+                                                          const int32_t* __restrict__ ids, int64_t quads, int S, int E,
+                                                          int N, int splits, uint16_t* __restrict__ h) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const int64_t s = i / (N / 4);
+  const int n = 4 * (int)(i - s * (N / 4));
+  const int e = ids[s];
+  if (e < 0 || e >= E) return;
+  const float* at = sums + s * 2 * N + n;
+  const int64_t stride = (int64_t)S * 2 * N;
+  const floatx4 g = sum_splits<8>(at, stride, splits), u = sum_splits<8>(at + N, stride, splits);
+  *reinterpret_cast<u32x2*>(h + s * N + n) = u32x2{pack_act2<BF16>(gated(g[0], u[0]), gated(g[1], u[1])),
+                                                  pack_act2<BF16>(gated(g[2], u[2]), gated(g[3], u[3]))};
+}
+
+hipError_t launch_expert_gate(const float* sums, const int32_t* ids, int S, int E, int N, int splits, bool bf16,
+                              uint16_t* h, hipStream_t stream) {
+  const int64_t quads = (int64_t)S * (N / 4);
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, sums, ids, quads, S, E, N,
+                       splits, h);
+  };
+  if (bf16) go(expert_gate_kernel<true>);
+  else go(expert_gate_kernel<false>);
+  return hipGetLastError();
+}
+
+}  // namespace awq

@@ -114,11 +114,19 @@ struct ExpertProduct {
   float* sums;
 };
 // Row tiles over slots sorted by expert (table and sorted as launch_moe_align gives them).
-hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertTilePlan& tp, const int32_t* sorted,
+hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertPlan& tp, const int32_t* sorted,
                                const int32_t* table, hipStream_t stream);
-// y[t, n] = sum over j of weights[t, j] * sums[t topk + j, n], in the order of j, over the
-// slots with an id in [0, E); rounded once to the activation type.
+// Few rows per expert: sums are [splits][S][N], or gated with splits > 1 [splits][S][2 N]
+// (then launch_expert_gate makes h of them).  table NULL: at most 64 slots, ranked by the
+// kernel itself.
+hipError_t launch_expert_stream(const ExpertProduct& p, const ExpertPlan& ep, const int32_t* sorted,
+                                const int32_t* table, hipStream_t stream);
+// h[s] = silu(gate) * up of the splits' sums [splits][S][2 N], for slots with an id in [0, E).
+hipError_t launch_expert_gate(const float* sums, const int32_t* ids, int S, int E, int N, int splits, bool bf16,
+                              uint16_t* h, hipStream_t stream);
+// y[t, n] = sum over j of weights[t, j] * the splits' sum of sums[split][t topk + j, n], in a
+// fixed order, over the slots with an id in [0, E); rounded once to the activation type.
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
-                                 int N, bool bf16, uint16_t* y, hipStream_t stream);
+                                 int N, int splits, bool bf16, uint16_t* y, hipStream_t stream);
 
 }  // namespace awq

@@ -460,19 +460,54 @@ namespace {
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-int plan_expert_tiles(int64_t S, int64_t E, int64_t N, bool gated, ExpertTilePlan& p) {
-  const int64_t cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
-  p.block_rows = kExpertTileRows;
-  p.tiles = moe_tiles(S, E, p.block_rows);
-  p.grid = p.tiles * ((N + cols - 1) / cols);
-  p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
+// Entries of at most `rows` rows that S slots over E experts can make: an expert with slots
+// has one per `rows` of them, so at most one each for min(E, S) experts and one more per
+// full block.
+int64_t entry_bound(int64_t S, int64_t E, int64_t rows) {
+  const int64_t experts = E < S ? E : S;
+  const int64_t b = experts + S / rows;
+  return b < S ? b : S;
+}
+
+int plan_expert(int64_t S, int64_t E, int64_t K, int64_t N, int cus, bool gated, ExpertPlan& p) {
+  p = ExpertPlan{};
+  const int64_t wide = gated ? 2 * N : N;
+  // 32-bit byte offsets into one expert's weight.
+  p.stream = S <= 16 * E && K * (wide / 2) < k2p32 - 4096;
+  if (p.stream) {
+    p.ranked = S <= kExpertRankSlots;
+    p.rows = S <= 4 ? 4 : S <= 8 ? 8 : 16;
+    p.block_rows = 16;
+    p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
+    p.tiles = p.ranked ? entry_bound(S, E, 16) : moe_tiles(S, E, 16);
+    const int64_t active = E < S ? E : S;  // experts with rows, about
+    const int64_t parts = gated ? 2 : 4;
+    const int64_t T = K / 32;
+    int64_t splits = (4 * (int64_t)cus + active * p.col_tiles - 1) / (active * p.col_tiles);
+    const int64_t most = T / (2 * parts) > 1 ? T / (2 * parts) : 1;
+    if (splits > most) splits = most;
+    if (splits > 16) splits = 16;
+    p.steps = (int)((T + splits * parts - 1) / (splits * parts));
+    p.splits = (int)((T + p.steps * parts - 1) / (p.steps * parts));
+    p.grid = p.tiles * p.col_tiles * p.splits;
+    p.sums_bytes = gated && p.splits == 1 ? 0 : round_up(p.splits * S * wide * 4, 256);
+    if (!p.ranked) p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
+  } else {
+    const int64_t cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
+    p.rows = p.block_rows = kExpertTileRows;
+    p.tiles = moe_tiles(S, E, p.block_rows);
+    p.col_tiles = (int)((N + cols - 1) / cols);
+    p.grid = p.tiles * p.col_tiles;
+    p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
+    p.sums_bytes = gated ? 0 : round_up(S * N * 4, 256);
+  }
   return grid_fits(p.grid, 1, 256) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
 }
 
 }  // namespace
 
 int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
-                 bool up, bool down, ExpertsPlan& p) {
+                 int cus, bool up, bool down, ExpertsPlan& p) {
   p = ExpertsPlan{};
   if (T < 0 || topk < 1 || E < 1) return AWQ_ERR_SHAPE;
   if (inner < 1 || inner > kMaxDim) return inner < 1 ? AWQ_ERR_SHAPE : AWQ_ERR_UNSUPPORTED;
@@ -491,17 +526,19 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
     if (T * (N / 4) + 256 >= k2p32) return AWQ_ERR_UNSUPPORTED;  // one thread per four outputs
   }
   if (T == 0) return AWQ_OK;
+  if (cus < 1) cus = 1;
   if (up) {
-    const int st = plan_expert_tiles(S, E, inner, true, p.up);
+    const int st = plan_expert(S, E, K, inner, cus, true, p.up);
     if (st != AWQ_OK) return st;
     p.sorted_bytes = p.up.table_bytes;
+    p.sums_bytes = p.up.sums_bytes;
     if (down) p.h_bytes = round_up(S * inner * 2, 256);
   }
   if (down) {
-    const int st = plan_expert_tiles(S, E, N, false, p.down);
+    const int st = plan_expert(S, E, inner, N, cus, false, p.down);
     if (st != AWQ_OK) return st;
-    p.sorted_bytes = p.down.table_bytes;
-    p.sums_bytes = round_up(S * N * 4, 256);
+    if (p.down.table_bytes > p.sorted_bytes) p.sorted_bytes = p.down.table_bytes;
+    if (p.down.sums_bytes > p.sums_bytes) p.sums_bytes = p.down.sums_bytes;
   }
   return AWQ_OK;
 }

@@ -181,25 +181,36 @@ int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t
                int64_t topk);
 
 // One product of routed rows with their experts' weights (gated: N pairs of columns of a
-// 2 N wide weight), over slots sorted by expert in row tiles of block_rows.
-struct ExpertTilePlan {
-  int block_rows = 0;
-  int64_t tiles = 0;    // table entries
-  int64_t grid = 0;     // workgroups
+// 2 N wide weight).  Entries are up to `rows` routed rows of one expert:
+//   stream   few rows per expert: 4, 8 or 16 rows kept, workgroups over (entry, column tile
+//            of 256 columns, K split); each wave of a workgroup takes `steps` k-steps of 32
+//   tiles    otherwise: 128 x 256 row tiles over the sorted slots, one split
+struct ExpertPlan {
+  bool stream = false;
+  bool ranked = false;      // stream: the kernel ranks the slots itself, no table
+  int rows = 0;             // rows kept per entry
+  int block_rows = 0;       // rows of a table entry
+  int64_t tiles = 0;        // entries the grid covers
+  int col_tiles = 0;
+  int splits = 1, steps = 0;
+  int64_t grid = 0;         // workgroups
   int64_t table_bytes = 0;  // table, offsets and sorted slots
+  int64_t sums_bytes = 0;   // fp32 sums of all splits
 };
 constexpr int kExpertTileRows = 128;
-constexpr int kExpertTileCols = 256;  // weight columns of a workgroup
+constexpr int kExpertTileCols = 256;    // weight columns of a workgroup
+constexpr int kExpertStreamCols = 256;  // columns of a workgroup (gated: of each half)
+constexpr int64_t kExpertRankSlots = 64;  // slots a wave can rank, one per lane
 // The gated MLP of routed experts and its two halves: which products it makes, and the
 // caller's workspace, in this order: the slots sorted by expert, h of the first product (mlp)
-// and the fp32 sums of the second.
+// and the fp32 sums (the first product's are dead when the second's are written).
 struct ExpertsPlan {
-  ExpertTilePlan up, down;
+  ExpertPlan up, down;
   int64_t sorted_bytes = 0, h_bytes = 0, sums_bytes = 0;
   int64_t workspace_bytes() const { return sorted_bytes + h_bytes + sums_bytes; }
 };
-// K -> I gated (up) and K2 -> N (down) halves; a half that is not there has N = 0.
+// K -> I gated (up) and inner -> N (down) products.
 int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
-                 bool up, bool down, ExpertsPlan& p);
+                 int cus, bool up, bool down, ExpertsPlan& p);
 
 }  // namespace awq
