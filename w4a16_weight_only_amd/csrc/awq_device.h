@@ -158,8 +158,11 @@ __device__ __forceinline__ floatx16 mfma32(const half8v& a, const half8v& b, con
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// silu(g) u.
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+// silu(g) u, the quotient by a reciprocal good to one step (an exact division is a dozen
+// instructions, and this is a tile's epilogue).
+__device__ __forceinline__ float gated(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u;
+}
 
 // ---- Split-K sums in 64-bit fixed point, one word per output element.
 // Each of the `splits` workgroups that share an output element adds its fp32 partial p

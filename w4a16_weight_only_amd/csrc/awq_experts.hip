@@ -8,11 +8,22 @@
 // set of accumulators and no rounding of weights).  A scale of zero cannot be a unit: the
 // unit stays and that group's (q - z) of the column are staged as zeros.
 //
-// Workgroup: 128 rows x 256 weight columns (gated: 128 columns of each half, so that a wave
-// holds both of a pair), 4 waves of 64 x 128, v_mfma_f32_32x32x16.  Per k-tile of 64 the x
-// rows go straight to LDS; each thread unpacks 8 rows of one packed word column (8 columns)
-// and writes the integers to LDS with k innermost, so each weight is unpacked once per
-// workgroup.  Two workgroups share a compute unit: one multiplies while the other unpacks.
+// Workgroup: 8 waves as 2 (rows) x 4 (columns), 256 weight columns (gated: 128 of each half,
+// so that a wave holds both of a pair) by 256, 192, 128 or 64 rows, whichever holds the entry; a
+// wave's part is 32 FM x 64 of v_mfma_f32_32x32x16.  Per k-tile of 64 the x rows go straight
+// to LDS; each thread unpacks 4 rows of one packed word column (8 columns) and writes the
+// integers to LDS with k innermost, so a weight is unpacked once per workgroup.
+//
+// The two waves of a SIMD take turns: while one multiplies (the 4 FM MFMAs of half a k-tile,
+// operands in registers; beside the first half's, in their shadow, it unpacks and stages its
+// share of k-tile t + 1), the other reads its next operands from LDS.  At a group boundary it
+// also rescales the sums of its first 32 columns; those of the other 32 follow in the shadow of
+// the first MFMAs (wherever a group may begin, by 1 where none does: a second copy of the MFMAs
+// without it makes the compiler move accumulators about).  A barrier ends each turn, and the
+// second four waves are one turn behind.
+// x is loaded two k-tiles ahead (three LDS buffers), words three (registers).
+#include <type_traits>
+
 #include "awq_device.h"
 #include "awq_kernels.h"
 
@@ -20,42 +31,62 @@ namespace awq {
 
 namespace {
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
 constexpr int kBK = 64;
 constexpr int kRows = kExpertTileRows;
 constexpr int kCols = kExpertTileCols;
-constexpr int kThreads = 256;
-constexpr int kFM = 2, kFN = 4;  // 32 x 32 blocks of a wave: 64 rows x 128 columns
-constexpr int kWaveRows = 32 * kFM;
+constexpr int kThreads = 512;
+constexpr int kFN = 2;  // 32 x 32 column blocks of a wave
+constexpr int kWM = 2, kWN = 4;
+static_assert(kWN * kFN * 32 == kCols && kWM * 4 * 32 == kRows, "8 waves cover the tile");
 
-// LDS rows of the staged integers: column c's 64 k values take 128 bytes, 16-byte chunk o at
-// position o ^ b_swz(c) of row b_row(c).  Writers hold one chunk of columns 8 w + j for 16
-// consecutive w at a time and readers one chunk of 16 consecutive columns: both reach all
-// sixteen 16-byte slots of the 64 banks.
-__device__ __forceinline__ int b_row(int c) { return c ^ ((c >> 3) & 1); }
-__device__ __forceinline__ int b_swz(int c) { return (c ^ (c >> 4)) & 7; }
+// LDS: three k-tiles of x, then two of the staged integers.
+//   x         row r: 128 bytes (64 k), 16-byte chunk c at position c ^ ((r / 2) % 8)
+//   integers  column c: 128 bytes at row c ^ ((c / 8) % 2), chunk o at position o ^ swz(c),
+//             swz(c) = (c ^ (c / 16)) % 8
+// A 16-byte read serves 16 lanes from the 64 banks: 16 consecutive rows (or columns) of one
+// chunk fall on all sixteen 16-byte slots, and so do the writes of one chunk of columns 8 w + j
+// for 16 consecutive w.  Chunks and columns differ in address bits that rows do not reach, so a
+// thread keeps one address each and flips bits of it: chunk c + 2 s is address ^ (32 s), column
+// 8 w + j of a writer's word is address ^ (144 j).
+constexpr int kATile = kRows * kBK * 2;
+constexpr int kBTile = kCols * kBK * 2;
+constexpr int kBBase = 3 * kATile;
+constexpr int kLdsBytes = kBBase + 2 * kBTile;
+static_assert(kLdsBytes <= 160 * 1024, "the compute unit's LDS");
+__device__ __forceinline__ int b_addr(int c, int chunk) {
+  return (c ^ ((c >> 3) & 1)) * (2 * kBK) + 16 * (chunk ^ ((c ^ (c >> 4)) & 7));
+}
+
+// 16 bytes per lane from a buffer (bounds-checked: past its end nothing is read) straight into
+// LDS: lane l's data lands at lds + 16 l.  Not tracked by the compiler: the kernel waits itself.
+__device__ __forceinline__ void load_lds16_buffer(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
+               "s"(soff), "s"(lds)
+               : "memory", "m0");
+}
+// Raw buffer descriptor of `bytes` bytes at a uniform address.
+__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) & 0xFFFFu,
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
 
 }  // namespace
 
-template <bool GATED, bool BF16>
-__global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(const ExpertProduct p, int n_tiles, int tiles,
-                                                                  const int32_t* __restrict__ sorted,
-                                                                  const int32_t* __restrict__ table) {
-  __shared__ __attribute__((aligned(16))) uint16_t As[2][kRows * kBK];
-  __shared__ __attribute__((aligned(16))) uint16_t Bs[kCols * kBK];
-  __shared__ int32_t slots[kRows];
-
-  const int entry = blockIdx.x / n_tiles;
-  const int tile = blockIdx.x - entry * n_tiles;
-  if (entry >= tiles) return;
-  const int e = table[4 * entry];
-  if (e < 0) return;  // an unused entry: the whole workgroup leaves before any barrier
-  const int first = table[4 * entry + 1];
-  const int rows = table[4 * entry + 2];
-
+// FM: 32-row blocks of a wave; the entry has at most 64 FM rows.  BEGINS: groups
+// begin at even k-tiles only (2: g is a multiple of 128, or there is one group), at any k-tile
+// (1: a multiple of 64), or also in the middle of one (0).
+template <int FM, bool GATED, bool BF16, int BEGINS>
+__device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, int e, int first, int rows, int tile,
+                                            const int32_t* __restrict__ sorted) {
+  constexpr int kWaveRows = 32 * FM;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / kWN, wn = wave % kWN;
   const int lc = lane & 31;
   const int K = p.K, N = p.N;
   const int NW = (GATED ? 2 * N : N) >> 3;  // packed words of a weight row
@@ -64,193 +95,357 @@ __global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(const ExpertPr
   const uint32_t* qzeros = p.qzeros + (int64_t)e * G * NW;
   const uint16_t* scales = p.scales + (int64_t)e * G * NW * 8;
   const int n0 = tile * (GATED ? kCols / 2 : kCols);
+  const int KT = (K + kBK - 1) / kBK;
 
-  for (int r = tid; r < kRows; r += kThreads) slots[r] = sorted[first + min(r, rows - 1)];
-
-  // x rows: wave w stages rows 32 w .. 32 w + 31, 8 rows a load; lane l fetches chunk
+  // x rows: wave w stages rows 8 FM w .. 8 FM w + 8 FM - 1, 8 rows a load; lane l fetches chunk
   // (l % 8) ^ ((row / 2) % 8) of row l / 8 of the eight (rows past the entry repeat its last).
-  uint32_t a_off[4];
-  int a_ch[4];
+  // The upper chunks of a last k-tile of 32 are the next row's, or past the end of x, and are
+  // not multiplied; so are k-tiles past the last.
+  const u32x4 xrs = buffer_of(p.x, (uint32_t)p.S / (uint32_t)p.row_div * (uint32_t)K * 2u);
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds);
+  uint32_t a_off[FM];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = 32 * wave + 8 * j + (lane >> 3);
+  for (int j = 0; j < FM; ++j) {
+    const int r = 8 * (FM * wave + j) + (lane >> 3);
     const int row = sorted[first + min(r, rows - 1)] / p.row_div;
-    a_ch[j] = (lane & 7) ^ ((r >> 1) & 7);
-    a_off[j] = ((uint32_t)row * (uint32_t)K + 8u * (uint32_t)a_ch[j]) * 2u;
+    a_off[j] = ((uint32_t)row * (uint32_t)K + 8u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7))) * 2u;
   }
-  auto load_a = [&](int buf, int k0) {
-    const bool part = K - k0 < kBK;  // the last 32 of K: the upper chunks re-read the lower
+  auto load_a = [&](int buf, int kt) {
+    const uint32_t at = lds0 + (uint32_t)(buf * kATile + FM * wave * 1024);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      load_lds16_s(p.x + k0, a_off[j] - (part && a_ch[j] >= 4 ? 64u : 0u), &As[buf][(32 * wave + 8 * j) * kBK]);
+    for (int j = 0; j < FM; ++j) load_lds16_buffer(xrs, a_off[j], (uint32_t)kt * (kBK * 2u), at + 1024u * j);
   };
 
-  // This thread's share of the weights: rows 8 o .. 8 o + 7 of packed column pw.
-  const int o = tid >> 5, w = tid & 31;
+  // This thread's share of the weights: rows 4 o .. 4 o + 3 of a k-tile, packed column pw.  A
+  // wave has 8 rows, one chunk; its lanes' halves of the chunk alternate with the column so
+  // that 32 lanes' 8-byte writes fill all banks.  Rows past K read as zeros.
+  const int w = lane & 31;
+  const int o_half = (lane >> 5) ^ ((w >> 4) & 1);
   const int half_words = N >> 3;
   int pw;
   if constexpr (GATED) pw = min(n0 / 8 + (w & 15), half_words - 1) + (w >> 4) * half_words;
   else pw = min(n0 / 8 + w, half_words - 1);
-  uint32_t words[8], zword;
-  u32x4 sraw;
-  auto load_b = [&](int k0) {
-    const int k = min(k0 + 8 * o, K - 8);
+  const uint32_t row_bytes = (uint32_t)NW * 4u;
+  const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint32_t*>(qweight), (short)0, (int)(row_bytes * (uint32_t)K), 0x00020000);
+  const uint32_t w_off = (uint32_t)(8 * wave + 4 * o_half) * row_bytes + (uint32_t)pw * 4u;
+  auto load_words = [&](uint32_t (&words)[4], int kt) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) words[r] = qweight[(int64_t)(k + r) * NW + pw];
-    const int gi = k / p.g;
+    for (int r = 0; r < 4; ++r)
+      words[r] = __builtin_amdgcn_raw_buffer_load_b32(wrs, w_off, (uint32_t)(kt * kBK + r) * row_bytes, 0);
+  };
+  uint32_t zword;
+  u32x4 sraw;
+  auto load_group = [&](int gi) {
     zword = qzeros[(int64_t)gi * NW + pw];
     sraw = *reinterpret_cast<const u32x4*>(scales + ((int64_t)gi * NW + pw) * 8);
   };
   const UnpackConsts uk = unpack_consts();
-  auto stage_b = [&] {
-    // Columns with a scale of zero (either sign) keep zeros instead of (q - z).
-    uint32_t nil = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = sraw[i] & 0x7FFF7FFFu;
-      nil |= (v - 0x00010001u) & ~v & 0x80008000u;
-    }
-    const bool any_nil = __builtin_amdgcn_ballot_w64(nil != 0) != 0;
-    auto put = [&](int c, half2v (&v)[4]) {
-      u32x4 d;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = BF16 ? pack_bf16x2((float)v[i][0], (float)v[i][1]) : as_u32(v[i]);
-      if (any_nil && ((sraw[c >> 1] >> (16 * (c & 1))) & 0x7FFFu) == 0) d = u32x4{0u, 0u, 0u, 0u};
-      const int col = 8 * w + c;
-      *reinterpret_cast<u32x4*>(&Bs[b_row(col) * kBK + 8 * (o ^ b_swz(col))]) = d;
-    };
+  uint32_t zs[8];     // the operands' zero terms, by nibble
+  uint32_t nil = 0;   // columns whose scale is zero (either sign): staged as zeros
+  bool any_nil = false;
+  auto enter_group = [&] {
+    nil = 0;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint32_t zl = 0xE400u | zero_code(zword, lo_col(t)), zh = 0xD400u | (zero_code(zword, hi_col(t)) << 4);
-      const half2v offl = as_h2(zl | (zl << 16)), offh = as_h2(zh | (zh << 16));
-      half2v lo[4], hi[4];
+      zs[2 * t] = zl | (zl << 16);
+      zs[2 * t + 1] = zh | (zh << 16);
+    }
+    uint32_t zero = 0;  // a half of zero, either sign: the halves' borrow trick
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t pb;
-        if (t == 0) pb = pair_byte<0>(words[2 * i], words[2 * i + 1]);
-        else if (t == 1) pb = pair_byte<1>(words[2 * i], words[2 * i + 1]);
-        else if (t == 2) pb = pair_byte<2>(words[2 * i], words[2 * i + 1]);
-        else pb = pair_byte<3>(words[2 * i], words[2 * i + 1]);
-        lo[i] = lo_minus_zero(pb, offl, uk);
-        hi[i] = hi_minus_zero(pb, offh, uk);
-      }
-      put(lo_col(t), lo);
-      put(hi_col(t), hi);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = sraw[i] & 0x7FFF7FFFu;
+      zero |= (v - 0x00010001u) & ~v & 0x80008000u;
+    }
+    any_nil = __builtin_amdgcn_ballot_w64(zero != 0) != 0;
+    if (any_nil) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) nil |= ((sraw[c >> 1] >> (16 * (c & 1))) & 0x7FFFu) == 0 ? 1u << c : 0u;
     }
   };
-
-  // This wave's columns: block j, column of the tile tcol(j) + lc.
-  auto tcol = [&](int j) {
-    if constexpr (GATED) return (j >= kFN / 2 ? kCols / 2 : 0) + 32 * (wn * (kFN / 2) + j % (kFN / 2));
-    else return 32 * (wn * kFN + j);
+  // Where this thread's four values of its column c go.
+  const int b_write = kBBase + b_addr(8 * w, wave) + 8 * o_half;
+  auto b_at = [&](int buf, int c) { return reinterpret_cast<u32x2_t*>(lds + ((b_write + buf * kBTile) ^ (144 * c))); };
+  // Byte t of the words: two columns of the staged tile.
+  auto stage = [&](const uint32_t (&words)[4], int buf, int t) {
+    half2v lo[2], hi[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t pb;
+      if (t == 0) pb = pair_byte<0>(words[2 * i], words[2 * i + 1]);
+      else if (t == 1) pb = pair_byte<1>(words[2 * i], words[2 * i + 1]);
+      else if (t == 2) pb = pair_byte<2>(words[2 * i], words[2 * i + 1]);
+      else pb = pair_byte<3>(words[2 * i], words[2 * i + 1]);
+      lo[i] = lo_minus_zero(pb, as_h2(zs[2 * t]), uk);
+      hi[i] = hi_minus_zero(pb, as_h2(zs[2 * t + 1]), uk);
+    }
+    auto put = [&](int c, const half2v (&v)[2]) {
+      u32x2_t d;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) d[i] = BF16 ? pack_bf16x2((float)v[i][0], (float)v[i][1]) : as_u32(v[i]);
+      *b_at(buf, c) = d;
+    };
+    put(lo_col(t), lo);
+    put(hi_col(t), hi);
   };
+  // Columns without a scale (rare) are staged once more, as zeros.
+  auto stage_nil = [&](int buf) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if ((nil >> c) & 1) *b_at(buf, c) = u32x2_t{0u, 0u};
+  };
+
+  // This wave's columns: block j, columns tcol(j) + lc of the tile.
+  auto tcol = [&](int j) { return GATED ? 32 * wn + j * (kCols / 2) : 32 * (wn * kFN + j); };
   int scol[kFN];  // column of the scales
 #pragma unroll
-  for (int j = 0; j < kFN; ++j) {
-    if constexpr (GATED) scol[j] = min(n0 + 32 * (wn * (kFN / 2) + j % (kFN / 2)) + lc, N - 1) + (j >= kFN / 2 ? N : 0);
-    else scol[j] = min(n0 + tcol(j) + lc, N - 1);
-  }
+  for (int j = 0; j < kFN; ++j)
+    scol[j] = GATED ? min(n0 + 32 * wn + lc, N - 1) + j * N : min(n0 + tcol(j) + lc, N - 1);
   uint16_t s_next[kFN];
   auto load_scales = [&](int gi) {
 #pragma unroll
     for (int j = 0; j < kFN; ++j) s_next[j] = scales[(int64_t)min(gi, G - 1) * NW * 8 + scol[j]];
   };
 
-  floatx16 acc[kFM][kFN];
+  floatx16 acc[FM][kFN];
   float unit[kFN];
 #pragma unroll
   for (int j = 0; j < kFN; ++j) {
     unit[j] = 1.f;
 #pragma unroll
-    for (int i = 0; i < kFM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   }
 
-  load_scales(0);
-  load_b(0);
-  load_a(0, 0);
+  // Operands of half a k-tile: two k16 steps.
+  half8v fa[2][FM], fb[2][kFN];
+  const int r0 = wm * kWaveRows + lc;
+  const int a_read = r0 * (2 * kBK) + 16 * ((lane >> 5) ^ ((r0 >> 1) & 7));
+  int b_read[kFN];
+#pragma unroll
+  for (int j = 0; j < kFN; ++j) b_read[j] = kBBase + b_addr(tcol(j) + lc, lane >> 5);
+  auto read = [&](int abuf, int bbuf, int hf) {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const int flip = 32 * (2 * hf + st);
+#pragma unroll
+      for (int j = 0; j < kFN; ++j)
+        fb[st][j] = *reinterpret_cast<const half8v*>(lds + ((b_read[j] ^ flip) + bbuf * kBTile));
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        fa[st][i] = *reinterpret_cast<const half8v*>(lds + ((a_read ^ flip) + abuf * kATile + 32 * i * (2 * kBK)));
+    }
+  };
+  // A group boundary: new units; the factors of the old sums.
   int group = 0, boundary = 0;
-  const int KT = (K + kBK - 1) / kBK;
-  for (int kt = 0; kt < KT; ++kt) {
-    const int k0 = kt * kBK;
-    stage_b();
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (kt + 1 < KT) {
-      load_a((kt + 1) & 1, k0 + kBK);
-      load_b(k0 + kBK);
+  float ratio[kFN];
+  auto change_units = [&] {
+    boundary += p.g;
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) {
+      const float s = act_to_float<false>(s_next[j]);
+      const float u = s == 0.f ? unit[j] : s;
+      ratio[j] = unit[j] * __builtin_amdgcn_rcpf(u);
+      unit[j] = u;
     }
-    const uint16_t* A = As[kt & 1];
+    load_scales(++group);
+  };
+  auto rescale = [&](int j) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int kk = k0 + 32 * hf;
-      if (kk >= K) break;  // uniform: the last k-tile may hold 32 rows
-      if (kk == boundary) {
-        boundary += p.g;
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) {
-          const float s = act_to_float<false>(s_next[j]);
-          const float u = s == 0.f ? unit[j] : s;
-          const float ratio = unit[j] * __builtin_amdgcn_rcpf(u);
-          if (group > 0) {
+      for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio[j];
+  };
+  // The 4 FM MFMAs of half a k-tile.  SCALE: the second column block's sums still await their
+  // factor; the first block's MFMAs go first.  STAGE: with the unpacking of the next k-tile, 8 LDS
+  // writes and about 40 vector instructions (88 with the conversions to bfloat16).  The matrix
+  // core works on one MFMA while the next share of vector instructions issues.
+  auto multiply = [&](auto scale, auto stages, const uint32_t (&next)[4], int to) {
+    constexpr bool SCALE = decltype(scale)::value, STAGE = decltype(stages)::value;
+    if constexpr (SCALE) rescale(1);
 #pragma unroll
-            for (int i = 0; i < kFM; ++i)
+    for (int st = 0; st < 2; ++st)
 #pragma unroll
-              for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio;
-          }
-          unit[j] = u;
-        }
-        ++group;
-        load_scales(group);
-      }
+      for (int j = 0; j < kFN; ++j)
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const int ch = 4 * hf + 2 * st + (lane >> 5);
-        half8v a[kFM], b[kFN];
+        for (int i = 0; i < FM; ++i) acc[i][j] = mfma32<BF16>(fa[st][i], fb[st][j], acc[i][j]);
+    if constexpr (STAGE) {
 #pragma unroll
-        for (int i = 0; i < kFM; ++i) {
-          const int r = wm * kWaveRows + 32 * i + lc;
-          a[i] = *reinterpret_cast<const half8v*>(&A[r * kBK + 8 * (ch ^ ((r >> 1) & 7))]);
-        }
+      for (int t = 0; t < 4; ++t) stage(next, to, t);
+    }
+    constexpr int kHalf = FM * kFN;  // MFMAs of one k16 step
+    constexpr int kStageValu = STAGE ? (BF16 ? 96 : 48) : 0;
+    if constexpr (SCALE) {
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) {
-          const int c = tcol(j) + lc;
-          b[j] = *reinterpret_cast<const half8v*>(&Bs[b_row(c) * kBK + 8 * (ch ^ b_swz(c))]);
-        }
-#pragma unroll
-        for (int i = 0; i < kFM; ++i)
-#pragma unroll
-          for (int j = 0; j < kFN; ++j) acc[i][j] = mfma32<BF16>(a[i], b[j], acc[i][j]);
+      for (int i = 0; i < kHalf; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x002, 10, 0);  // VALU
       }
     }
-    __syncthreads();
-  }
+    if constexpr (STAGE) {
+      constexpr int kLeft = SCALE ? kHalf : 2 * kHalf;
+#pragma unroll
+      for (int i = 0; i < kLeft; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, (kStageValu + kLeft - 1) / kLeft, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, (8 + kLeft - 1) / kLeft, 0);  // LDS writes
+      }
+    }
+  };
+  // Turns end at a barrier; a wave's LDS writes of the turn are done.
+  auto turn = [] {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Group whose zeros this wave unpacks with (its 8 rows of a k-tile lie in one), where it
+  // ends, and how many groups on the wave's next one is.
+  const int row_half = 32 * (wave >> 2);
+  const int stride = p.g == 32 ? 2 : 1;
+  int pg = p.g == 32 ? wave >> 2 : 0;
+  int pend = (pg + 1) * p.g;
 
+  uint32_t words[2][4];  // of k-tiles t + 1 and t + 2, by parity
+  load_group(min(pg, G - 1));
+  load_words(words[0], 0);
+  load_words(words[1], 1);
+  load_scales(0);
+  load_a(0, 0);
+  enter_group();
+  load_group(min(pg + stride, G - 1));
+#pragma unroll
+  for (int t = 0; t < 4; ++t) stage(words[0], 0, t);
+  if (any_nil) stage_nil(0);
+  if (kBK + row_half >= pend) {  // the zeros of k-tile 1
+    enter_group();
+    pg += stride;
+    pend += stride * p.g;
+    load_group(min(pg + stride, G - 1));
+  }
+  load_words(words[0], 2);
+  load_a(1, 1);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (wave >= 4) turn();  // one turn behind
+
+  int ab = 0;  // LDS buffer of this k-tile's x
+  auto body = [&](int kt, auto parity, uint32_t (&next)[4]) {
+    constexpr int buf = decltype(parity)::value;  // kt % 2
+    const int k0 = kt * kBK;
+    const bool full = k0 + 32 < K;  // the last k-tile may hold 32 rows
+    using yes = std::true_type;
+    using no = std::false_type;
+    read(ab, buf, 0);
+    constexpr bool kBegin = BEGINS < 2 || buf == 0;
+    if constexpr (kBegin) {
+      ratio[1] = 1.f;
+      if (k0 == boundary) {
+        change_units();
+        rescale(0);
+      }
+    }
+    turn();
+    multiply(std::integral_constant<bool, kBegin>{}, yes{}, next, buf ^ 1);
+    if (any_nil) stage_nil(buf ^ 1);
+    turn();
+    if (full) read(ab, buf, 1);
+    if constexpr (BEGINS == 0) {
+      ratio[1] = 1.f;
+      if (full && k0 + 32 == boundary) {
+        change_units();
+        rescale(0);
+      }
+    }
+    if (k0 + 2 * kBK + row_half >= pend) {  // the zeros of k-tile kt + 2, which is staged next
+      enter_group();  // loaded when the last group began
+      pg += stride;
+      pend += stride * p.g;
+      load_group(min(pg + stride, G - 1));
+    }
+    // Behind this turn's waits for scales and zeros: they count back from the newest load the
+    // compiler knows, would take these in, and wait for memory (12288 slots of 1408 -> 2048,
+    // g32: 266 -> 219 us).
+    load_a(ab == 0 ? 2 : ab - 1, kt + 2);
+    // x of k-tile kt + 1 has landed: the words of kt + 2 and FM loads of kt + 2 are younger.
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FM + 4) : "memory");
+    turn();
+    if (full) multiply(std::integral_constant<bool, BEGINS == 0>{}, no{}, next, 0);
+    load_words(next, kt + 3);
+    turn();
+    ab = ab == 2 ? 0 : ab + 1;
+  };
+  int kt = 0;
+  for (; kt + 1 < KT; kt += 2) {
+    body(kt, std::integral_constant<int, 0>{}, words[1]);
+    body(kt + 1, std::integral_constant<int, 1>{}, words[0]);
+  }
+  if (kt < KT) body(kt, std::integral_constant<int, 0>{}, words[1]);
+  if (wave < 4) turn();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last k-tile have landed
+  __syncthreads();
+
+  // The LDS tiles are dead: the entry's slots go there, and gated the rounded outputs, so that
+  // h is written in 16-byte pieces of rows.
+  int32_t* slots = reinterpret_cast<int32_t*>(lds);
+  for (int r = tid; r < rows; r += kThreads) slots[r] = sorted[first + r];
   // 32 x 32 block: register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
+  auto row_of = [&](int i, int r) { return wm * kWaveRows + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); };
+  if constexpr (GATED) {
+    constexpr int kOut = kCols / 2;  // output columns of the tile
+    constexpr int kLd = kOut + 8;    // halves of a staged row
+    uint16_t* ys = reinterpret_cast<uint16_t*>(lds + kRows * 4);
 #pragma unroll
-  for (int i = 0; i < kFM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = wm * kWaveRows + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      if (row >= rows) continue;
-      const int64_t slot = slots[row];
-      if constexpr (GATED) {
+      for (int r = 0; r < 16; ++r)
+        ys[row_of(i, r) * kLd + tcol(0) + lc] =
+            float_to_act<BF16>(gated(acc[i][0][r] * unit[0], acc[i][1][r] * unit[1]));
+    __syncthreads();
+    for (int q = tid; q < rows * (kOut / 8); q += kThreads) {
+      const int row = q / (kOut / 8), c = 8 * (q % (kOut / 8));
+      if (n0 + c < N)
+        *reinterpret_cast<u32x4*>(p.h + (int64_t)slots[row] * N + n0 + c) =
+            *reinterpret_cast<const u32x4*>(&ys[row * kLd + c]);
+    }
+  } else {
+    __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kFN / 2; ++j) {
-          const int n = n0 + tcol(j) + lc;
-          if (n < N)
-            p.h[slot * N + n] =
-                float_to_act<BF16>(gated(acc[i][j][r] * unit[j], acc[i][j + kFN / 2][r] * unit[j + kFN / 2]));
-        }
-      } else {
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = row_of(i, r);
+        if (row >= rows) continue;
+        float* out = p.sums + (int64_t)slots[row] * N;
 #pragma unroll
         for (int j = 0; j < kFN; ++j) {
           const int n = n0 + tcol(j) + lc;
-          if (n < N) p.sums[slot * N + n] = acc[i][j][r] * unit[j];
+          if (n < N) out[n] = acc[i][j][r] * unit[j];
         }
       }
-    }
+  }
+}
+
+template <bool GATED, bool BF16, int BEGINS>
+__global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(const ExpertProduct p, int n_tiles, int tiles,
+                                                                  const int32_t* __restrict__ sorted,
+                                                                  const int32_t* __restrict__ table) {
+  __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
+  // Every (entry, column tile) twice: the entries of more than 128 rows in the first half of
+  // the grid, the others in the second, so that the short ones fill the last round.
+  const int small = blockIdx.x >= (uint32_t)(tiles * n_tiles);
+  const int block = blockIdx.x - small * tiles * n_tiles;
+  const int entry = block / n_tiles;
+  const int tile = block - entry * n_tiles;
+  const int e = table[4 * entry];
+  const int first = table[4 * entry + 1];
+  const int rows = table[4 * entry + 2];
+  if (e < 0 || (rows > 128) == small) return;  // the whole workgroup, before any barrier
+  if (rows > 192) expert_tile<4, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
+  else if (rows > 128) expert_tile<3, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
+  else if (rows > 64) expert_tile<2, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
+  else expert_tile<1, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
 }
 
 hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertPlan& tp, const int32_t* sorted,
@@ -261,13 +456,16 @@ hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertPlan& tp, con
     hipLaunchKernelGGL(kern, dim3((unsigned)tp.grid), dim3(kThreads), 0, stream, p, n_tiles, (int)tp.tiles, sorted,
                        table);
   };
-  if (p.gated) {
-    if (p.bf16) go(expert_tile_kernel<true, true>);
-    else go(expert_tile_kernel<true, false>);
-  } else {
-    if (p.bf16) go(expert_tile_kernel<false, true>);
-    else go(expert_tile_kernel<false, false>);
-  }
+  auto pick = [&](auto gated, auto bf16) {
+    constexpr bool G = decltype(gated)::value, B = decltype(bf16)::value;
+    if (p.g % (2 * kBK) == 0 || p.g == p.K) go(expert_tile_kernel<G, B, 2>);
+    else if (p.g % kBK == 0) go(expert_tile_kernel<G, B, 1>);
+    else go(expert_tile_kernel<G, B, 0>);
+  };
+  using yes = std::true_type;
+  using no = std::false_type;
+  if (p.gated) p.bf16 ? pick(yes{}, yes{}) : pick(yes{}, no{});
+  else p.bf16 ? pick(no{}, yes{}) : pick(no{}, no{});
   return hipGetLastError();
 }
 

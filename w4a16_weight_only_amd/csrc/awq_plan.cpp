@@ -497,11 +497,11 @@ int plan_expert(int64_t S, int64_t E, int64_t K, int64_t N, int cus, bool gated,
     p.rows = p.block_rows = kExpertTileRows;
     p.tiles = moe_tiles(S, E, p.block_rows);
     p.col_tiles = (int)((N + cols - 1) / cols);
-    p.grid = p.tiles * p.col_tiles;
+    p.grid = 2 * p.tiles * p.col_tiles;  // long entries, then short ones
     p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
     p.sums_bytes = gated ? 0 : round_up(S * N * 4, 256);
   }
-  return grid_fits(p.grid, 1, 256) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
+  return grid_fits(p.grid, 1, p.stream ? 256 : 512) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -517,12 +517,12 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
     const int st = limits_check(S, K, 2 * inner, group_size);
     if (st != AWQ_OK) return st;
     if (inner % 32 != 0) return AWQ_ERR_UNSUPPORTED;  // the halves meet on a whole 16-byte piece
-    if (T * K * 2 >= k2p32) return AWQ_ERR_UNSUPPORTED;  // gathered rows use 32-bit offsets
+    if (T * K * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // gathered rows use 32-bit offsets
   }
   if (down) {
     const int st = limits_check(S, inner, N, group_size);
     if (st != AWQ_OK) return st;
-    if (S * inner * 2 >= k2p32) return AWQ_ERR_UNSUPPORTED;
+    if (S * inner * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;
     if (T * (N / 4) + 256 >= k2p32) return AWQ_ERR_UNSUPPORTED;  // one thread per four outputs
   }
   if (T == 0) return AWQ_OK;

@@ -184,7 +184,7 @@ int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t
 // 2 N wide weight).  Entries are up to `rows` routed rows of one expert:
 //   stream   few rows per expert: 4, 8 or 16 rows kept, workgroups over (entry, column tile
 //            of 256 columns, K split); each wave of a workgroup takes `steps` k-steps of 32
-//   tiles    otherwise: 128 x 256 row tiles over the sorted slots, one split
+//   tiles    otherwise: row tiles of up to 256 x 256 over the sorted slots, one split
 struct ExpertPlan {
   bool stream = false;
   bool ranked = false;      // stream: the kernel ranks the slots itself, no table
@@ -197,7 +197,7 @@ struct ExpertPlan {
   int64_t table_bytes = 0;  // table, offsets and sorted slots
   int64_t sums_bytes = 0;   // fp32 sums of all splits
 };
-constexpr int kExpertTileRows = 128;
+constexpr int kExpertTileRows = 256;
 constexpr int kExpertTileCols = 256;    // weight columns of a workgroup
 constexpr int kExpertStreamCols = 256;  // columns of a workgroup (gated: of each half)
 constexpr int64_t kExpertRankSlots = 64;  // slots a wave can rank, one per lane
