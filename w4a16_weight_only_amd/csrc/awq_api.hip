@@ -35,10 +35,13 @@ int device_cus() {
 // Compute units for host-only plan queries: the current device's, or 256 (MI355X)
 // when no device is visible.
 int query_cus() {
-  int count = 0;
-  if (hipGetDeviceCount(&count) == hipSuccess && count > 0) return device_cus();
-  (void)hipGetLastError();
-  return 256;
+  static const bool visible = [] {
+    int count = 0;
+    const bool any = hipGetDeviceCount(&count) == hipSuccess && count > 0;
+    if (!any) (void)hipGetLastError();
+    return any;
+  }();
+  return visible ? device_cus() : 256;
 }
 
 // Library-owned split-K workspace, one per (device, stream), in two buffers:

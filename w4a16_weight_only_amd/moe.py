@@ -11,18 +11,27 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .linear import _check_tensor, _ptr, _stream, validate
+from .linear import _check_tensor, validate
 
 _TYPES = {torch.float16: _lib.AWQ_F16, torch.bfloat16: _lib.AWQ_BF16, torch.float32: _lib.AWQ_F32}
 _SCORES = {"softmax": _lib.AWQ_SOFTMAX, "sigmoid": _lib.AWQ_SIGMOID}
+
+# A decoding step's calls are a few microseconds each on the GPU, so the checks below look at
+# each tensor once and leave the wording of a refusal to functions that only a refusal reaches.
+
+
+def _is(t, dtype, device):
+    """A contiguous tensor of this type on this device."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()
 
 
 def _check_act(name, t):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.float16, torch.bfloat16):
+    if t.dtype is not torch.float16 and t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
-    _check_tensor(name, t, t.dtype)
+    if t.device.type != "cuda" or not t.is_contiguous():
+        _check_tensor(name, t, t.dtype)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
 
@@ -30,27 +39,41 @@ def _check_act(name, t):
 def _check_layer(name, layer, K, group_size, device):
     """The packed weight's experts and columns."""
     qweight, qzeros, scales = layer
+    if _is(qweight, torch.int32, device) and _is(qzeros, torch.int32, device) and _is(scales, torch.float16, device):
+        shape = qweight.shape
+        if len(shape) == 3 and shape[1] == K and K > 0:
+            E, _, words = shape
+            G = 1 if group_size == -1 else K // group_size if group_size > 0 else 0
+            if qzeros.shape == (E, G, words) and scales.shape == (E, G, 8 * words):
+                return E, 8 * words  # a group size that does not divide K is the library's to refuse
+    _refuse_layer(name, qweight, qzeros, scales, K, group_size, device)
+
+
+def _refuse_layer(name, qweight, qzeros, scales, K, group_size, device):
     _check_tensor(f"{name} qweight", qweight, torch.int32, device)
     _check_tensor(f"{name} qzeros", qzeros, torch.int32, device)
     _check_tensor(f"{name} scales", scales, torch.float16, device)
     if qweight.dim() != 3 or qzeros.dim() != 3 or scales.dim() != 3:
         raise ValueError(f"{name}: qweight, qzeros and scales must be stacked per expert")
     E, rows, words = qweight.shape
-    if rows != K or qzeros.shape[0] != E or scales.shape[0] != E:
+    if rows != K or qzeros.shape[0] != E or scales.shape[0] != E or E < 1:
         raise ValueError(f"{name}: expert weight shapes disagree with each other or with {K} input features")
     validate(K, words * 8, group_size, qweight[0], qzeros[0], scales[0])
-    return E, words * 8
+    raise ValueError(f"{name}: unsupported shapes")
 
 
 def _check_ids(expert_ids, device, tokens=None):
-    _check_tensor("expert_ids", expert_ids, torch.int32, device)
-    if expert_ids.dim() != 2 or (tokens is not None and expert_ids.shape[0] != tokens) or expert_ids.shape[1] < 1:
+    if not _is(expert_ids, torch.int32, device):
+        _check_tensor("expert_ids", expert_ids, torch.int32, device)
+    shape = expert_ids.shape
+    if len(shape) != 2 or (tokens is not None and shape[0] != tokens) or shape[1] < 1:
         raise ValueError("expert_ids must be [T, topk]" + ("" if tokens is None else f" with T = {tokens}"))
-    return expert_ids.shape
+    return shape
 
 
 def _check_weights(weights, ids_shape, device):
-    _check_tensor("weights", weights, torch.float32, device)
+    if not _is(weights, torch.float32, device):
+        _check_tensor("weights", weights, torch.float32, device)
     if weights.shape != ids_shape:
         raise ValueError(f"weights must be {list(ids_shape)}")
 
@@ -58,17 +81,42 @@ def _check_weights(weights, ids_shape, device):
 def _output(out, shape, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _check_tensor("out", out, dtype, device)
-    if tuple(out.shape) != shape:
+    if not _is(out, dtype, device):
+        _check_tensor("out", out, dtype, device)
+    if out.shape != shape:
         raise ValueError(f"out must be {list(shape)}")
     return out
 
 
+def _call(fn, name, device, *args):
+    """fn(*args, stream) with the tensors' device current; the stream is that device's current one."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        _lib.check(status, name)
+
+
+_sizes = {}  # workspace bytes by device and the call's sizes
+
+
 def _workspace(device, *sizes):
-    need = _lib.load().awq_moe_workspace(*sizes)
-    if need < 0:
-        _lib.check(need, "awq_moe_workspace")
-    return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    """(tensor, bytes) on the current stream.  The size follows from the call's sizes and the
+    device's compute units; decoding repeats them, so it is asked for once."""
+    key = (device.index, sizes)
+    need = _sizes.get(key)
+    if need is None:
+        with torch.cuda.device(device):
+            need = _lib.load().awq_moe_workspace(*sizes)
+        if need < 0:
+            _lib.check(need, "awq_moe_workspace")
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        _sizes[key] = need = max(need, 16)
+    return torch.empty(need, dtype=torch.uint8, device=device), need
 
 
 def awq_moe_route(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
@@ -97,19 +145,18 @@ def awq_moe_route(logits: torch.Tensor, topk: int, *, score: str = "softmax", bi
     T, E = logits.shape
     stride = logits.stride(0) if T > 1 else E
     if bias is not None:
-        _check_tensor("bias", bias, torch.float32, dev)
-        if tuple(bias.shape) != (E,):
+        if not _is(bias, torch.float32, dev):
+            _check_tensor("bias", bias, torch.float32, dev)
+        if bias.shape != (E,):
             raise ValueError(f"bias must be [{E}]")
     if topk < 1:
         raise ValueError("topk must be at least 1")
     weights, ids = out if out is not None else (None, None)
     weights = _output(weights, (T, topk), torch.float32, dev)
     ids = _output(ids, (T, topk), torch.int32, dev)
-    with torch.cuda.device(dev):
-        st = _lib.load().awq_moe_route(_ptr(logits), _TYPES[logits.dtype], T, E, stride, _ptr(bias), _SCORES[score],
-                                       groups, topk_groups, group_top, topk, int(bool(renormalize)), scale,
-                                       _ptr(weights), _ptr(ids), _stream(dev))
-    _lib.check(st, "awq_moe_route")
+    _call(_lib.load().awq_moe_route, "awq_moe_route", dev, logits.data_ptr(), _TYPES[logits.dtype], T, E, stride,
+          None if bias is None else bias.data_ptr(), _SCORES[score], groups, topk_groups, group_top, topk,
+          1 if renormalize else 0, scale, weights.data_ptr(), ids.data_ptr())
     return weights, ids
 
 
@@ -128,12 +175,10 @@ def awq_moe_gate_up(x: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor
         raise ValueError("gate_up: the columns must be two equal halves of whole words")
     inner = N // 2
     out = _output(out, (T * topk, inner), x.dtype, dev)
-    with torch.cuda.device(dev):
-        ws = _workspace(dev, T, topk, E, K, inner, 0, group_size)
-        st = _lib.load().awq_moe_gate_up(_ptr(x), _TYPES[x.dtype], _ptr(qweight), _ptr(qzeros), _ptr(scales),
-                                         _ptr(expert_ids), T, topk, E, K, inner, group_size, _ptr(out), _ptr(ws),
-                                         ws.numel(), _stream(dev))
-    _lib.check(st, "awq_moe_gate_up")
+    ws, nbytes = _workspace(dev, T, topk, E, K, inner, 0, group_size)
+    _call(_lib.load().awq_moe_gate_up, "awq_moe_gate_up", dev, x.data_ptr(), _TYPES[x.dtype], qweight.data_ptr(),
+          qzeros.data_ptr(), scales.data_ptr(), expert_ids.data_ptr(), T, topk, E, K, inner, group_size,
+          out.data_ptr(), ws.data_ptr(), nbytes)
     return out
 
 
@@ -152,12 +197,10 @@ def awq_moe_down(h: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor, s
         raise ValueError(f"expert_ids must name an expert for each of the {S} rows of h")
     _check_weights(weights, expert_ids.shape, dev)
     out = _output(out, (T, N), h.dtype, dev)
-    with torch.cuda.device(dev):
-        ws = _workspace(dev, T, topk, E, 0, K, N, group_size)
-        st = _lib.load().awq_moe_down(_ptr(h), _TYPES[h.dtype], _ptr(qweight), _ptr(qzeros), _ptr(scales),
-                                      _ptr(expert_ids), _ptr(weights), T, topk, E, K, N, group_size, _ptr(out),
-                                      _ptr(ws), ws.numel(), _stream(dev))
-    _lib.check(st, "awq_moe_down")
+    ws, nbytes = _workspace(dev, T, topk, E, 0, K, N, group_size)
+    _call(_lib.load().awq_moe_down, "awq_moe_down", dev, h.data_ptr(), _TYPES[h.dtype], qweight.data_ptr(),
+          qzeros.data_ptr(), scales.data_ptr(), expert_ids.data_ptr(), weights.data_ptr(), T, topk, E, K, N,
+          group_size, out.data_ptr(), ws.data_ptr(), nbytes)
     return out
 
 
@@ -179,12 +222,10 @@ def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.
     _, topk = _check_ids(expert_ids, dev, T)
     _check_weights(weights, expert_ids.shape, dev)
     out = _output(out, (T, N), x.dtype, dev)
-    with torch.cuda.device(dev):
-        ws = _workspace(dev, T, topk, E, K, inner, N, group_size)
-        st = _lib.load().awq_moe_mlp(_ptr(x), _TYPES[x.dtype], *map(_ptr, gate_up), *map(_ptr, down),
-                                     _ptr(expert_ids), _ptr(weights), T, topk, E, K, inner, N, group_size, _ptr(out),
-                                     _ptr(ws), ws.numel(), _stream(dev))
-    _lib.check(st, "awq_moe_mlp")
+    ws, nbytes = _workspace(dev, T, topk, E, K, inner, N, group_size)
+    _call(_lib.load().awq_moe_mlp, "awq_moe_mlp", dev, x.data_ptr(), _TYPES[x.dtype],
+          *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down], expert_ids.data_ptr(), weights.data_ptr(),
+          T, topk, E, K, inner, N, group_size, out.data_ptr(), ws.data_ptr(), nbytes)
     return out
 
 
