@@ -88,19 +88,33 @@ struct Entry {
   int expert, rows;
 };
 
+// Set bits of mask below this lane.
+__device__ __forceinline__ int bits_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
 // Entries of at most 64 slots, ranked by each wave (lane l: slot l): the slots of an expert,
 // in order, in blocks of 16; entries in the order of their first slot.  rows 0: no such entry.
+// A lane's mask of slots with its expert comes from one ballot per bit of the id (a loop over
+// the slots took 5 us of 64 slots' 20).
 __device__ __forceinline__ Entry rank_entry(const int32_t* ids, int S, int E, int entry, int lane, int32_t* slots) {
   const int id = lane < S ? ids[lane] : -1;
   const bool routed = id >= 0 && id < E;
-  int rank = 0;  // among the lower slots of the same expert
-  for (int j = 0; j < S; ++j) rank += (j < lane && __builtin_amdgcn_readlane(id, j) == id) ? 1 : 0;
-  uint64_t leads = __ballot(routed && (rank & 15) == 0);
-  if (entry >= __builtin_popcountll(leads)) return Entry{0, 0};
-  for (int i = 0; i < entry; ++i) leads &= leads - 1;
-  const int lead = __builtin_ctzll(leads);
-  const int expert = __builtin_amdgcn_readlane(id, lead);
-  const int first = __builtin_amdgcn_readlane(rank, lead);
+  const uint64_t live = __ballot(routed);
+  uint64_t same = live;
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {  // E <= 1024
+    const uint64_t set = __ballot((id >> b) & 1);
+    same &= ((id >> b) & 1) ? set : ~set;
+  }
+  const int rank = bits_below(same);  // among the lower slots of the same expert
+  const bool lead = routed && (rank & 15) == 0;
+  const uint64_t leads = __ballot(lead);
+  const uint64_t found = __ballot(lead && bits_below(leads) == entry);
+  if (found == 0) return Entry{0, 0};
+  const int at = __builtin_ctzll(found);
+  const int expert = __builtin_amdgcn_readlane(id, at);
+  const int first = __builtin_amdgcn_readlane(rank, at);
   const bool mine = routed && id == expert && rank >= first && rank < first + 16;
   if (mine) slots[rank - first] = lane;  // every wave writes the same
   return Entry{expert, (int)__builtin_popcountll(__ballot(mine))};
@@ -164,9 +178,14 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   const int s0 = split * PARTS * steps;
   const int kb = min(T, s0 + part_of * steps), ke = min(T, kb + steps);
 
+  // Groups of the k-step loaded next and of the one multiplied next, and where they end.
+  const int g0 = kb / gsteps;
+  int load_group = g0 - 1, load_end = kb, use_end = kb;
   auto issue = [&](Step& st, int ks) {
-    if (ks == kb || ks % gsteps == 0) {
-      const int64_t at = (int64_t)(ks / gsteps) * NW + wc;
+    if (ks == load_end) {
+      ++load_group;
+      load_end = (load_group + 1) * gsteps;
+      const int64_t at = (int64_t)load_group * NW + wc;
       st.z = *reinterpret_cast<const u32x2*>(qzeros + at);
       st.s0 = *reinterpret_cast<const half8v*>(scales + 8 * at);
       st.s1 = *reinterpret_cast<const half8v*>(scales + 8 * at + 8);
@@ -242,9 +261,10 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
     for (int j = 0; j < kPF; ++j) {
       const int ks = base + j;
       if (ks < ke) {
-        if (ks == kb || ks % gsteps == 0) {
+        if (ks == use_end) {
           if (ks != kb) leave();
           enter(ring[j], ks == kb);
+          use_end = ks == kb ? (g0 + 1) * gsteps : use_end + gsteps;
         }
         multiply<BF16>(ring[j], zs, uk, part, sx);
         if (ks + kPF < ke) issue(ring[j], ks + kPF);

@@ -469,8 +469,40 @@ int64_t entry_bound(int64_t S, int64_t E, int64_t rows) {
   return b < S ? b : S;
 }
 
-int plan_expert(int64_t S, int64_t E, int64_t K, int64_t N, int cus, bool gated, ExpertPlan& p) {
+// K splits of a streaming plan.  In tenths of a microsecond (MI355X): a workgroup alone on a
+// compute unit takes 7 per k-step and wave, two together 12, and each round of two 30 for its
+// fixed part, so the busiest compute unit's n workgroups decide; every split also writes and
+// reads its fp32 sums once (4 TB/s), and splits of a gated product cost the kernel that joins
+// them.  Measured against forced split counts, us per call: one token through 8 x 4096 -> 14336,
+// gated: 1, 2, 3, 4, 9 splits 56, 35.6, 36.5, 32.5, 34.3 (4 chosen: 448 workgroups); 45 tokens
+// over 64 x 2048 -> 1408: 1, 2, 3, 9 splits 65.3, 67.4, 70.5, 71.3 (1 chosen).
+void choose_splits(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t wide, int64_t cus, bool gated, ExpertPlan& p) {
+  // Experts with rows, about, where a token's are distinct: E (1 - (1 - topk / E)^T).
+  const int64_t S = T * topk;
+  double idle = 1.0;
+  for (int64_t t = 0; t < T && idle > 1e-3; ++t) idle *= topk < E ? 1.0 - (double)topk / (double)E : 0.0;
+  int64_t active = (int64_t)((double)E * (1.0 - idle) + 0.5);
+  if (active < 1) active = 1;
+  const int64_t parts = gated ? 2 : 4;  // waves of a workgroup along K
+  const int64_t ksteps = K / 32;
+  int64_t best = -1;
+  for (int64_t want = 1; want <= kExpertMaxSplits; ++want) {
+    const int64_t steps = (ksteps + want * parts - 1) / (want * parts);
+    const int64_t splits = (ksteps + steps * parts - 1) / (steps * parts);
+    const int64_t n = (active * p.col_tiles * splits + cus - 1) / cus;
+    int64_t cost = steps * (12 * (n / 2) + 7 * (n % 2)) + 30 * ((n + 1) / 2);
+    if (!gated || splits > 1) cost += splits * S * wide / 50000;
+    if (gated && splits > 1) cost += 45;
+    if (best >= 0 && cost >= best) continue;
+    best = cost;
+    p.steps = (int)steps;
+    p.splits = (int)splits;
+  }
+}
+
+int plan_expert(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int cus, bool gated, ExpertPlan& p) {
   p = ExpertPlan{};
+  const int64_t S = T * topk;
   const int64_t wide = gated ? 2 * N : N;
   // 32-bit byte offsets into one expert's weight.
   p.stream = S <= 16 * E && K * (wide / 2) < k2p32 - 4096;
@@ -480,15 +512,7 @@ int plan_expert(int64_t S, int64_t E, int64_t K, int64_t N, int cus, bool gated,
     p.block_rows = 16;
     p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
     p.tiles = p.ranked ? entry_bound(S, E, 16) : moe_tiles(S, E, 16);
-    const int64_t active = E < S ? E : S;  // experts with rows, about
-    const int64_t parts = gated ? 2 : 4;
-    const int64_t T = K / 32;
-    int64_t splits = (4 * (int64_t)cus + active * p.col_tiles - 1) / (active * p.col_tiles);
-    const int64_t most = T / (2 * parts) > 1 ? T / (2 * parts) : 1;
-    if (splits > most) splits = most;
-    if (splits > 16) splits = 16;
-    p.steps = (int)((T + splits * parts - 1) / (splits * parts));
-    p.splits = (int)((T + p.steps * parts - 1) / (p.steps * parts));
+    choose_splits(T, topk, E, K, wide, cus, gated, p);
     p.grid = p.tiles * p.col_tiles * p.splits;
     p.sums_bytes = gated && p.splits == 1 ? 0 : round_up(p.splits * S * wide * 4, 256);
     if (!p.ranked) p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
@@ -528,14 +552,14 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
   if (T == 0) return AWQ_OK;
   if (cus < 1) cus = 1;
   if (up) {
-    const int st = plan_expert(S, E, K, inner, cus, true, p.up);
+    const int st = plan_expert(T, topk, E, K, inner, cus, true, p.up);
     if (st != AWQ_OK) return st;
     p.sorted_bytes = p.up.table_bytes;
     p.sums_bytes = p.up.sums_bytes;
     if (down) p.h_bytes = round_up(S * inner * 2, 256);
   }
   if (down) {
-    const int st = plan_expert(S, E, inner, N, cus, false, p.down);
+    const int st = plan_expert(T, topk, E, inner, N, cus, false, p.down);
     if (st != AWQ_OK) return st;
     if (p.down.table_bytes > p.sorted_bytes) p.sorted_bytes = p.down.table_bytes;
     if (p.down.sums_bytes > p.sums_bytes) p.sums_bytes = p.down.sums_bytes;

@@ -200,6 +200,7 @@ struct ExpertPlan {
 constexpr int kExpertTileRows = 256;
 constexpr int kExpertTileCols = 256;    // weight columns of a workgroup
 constexpr int kExpertStreamCols = 256;  // columns of a workgroup (gated: of each half)
+constexpr int64_t kExpertMaxSplits = 32;
 constexpr int64_t kExpertRankSlots = 64;  // slots a wave can rank, one per lane
 // The gated MLP of routed experts and its two halves: which products it makes, and the
 // caller's workspace, in this order: the slots sorted by expert, h of the first product (mlp)
