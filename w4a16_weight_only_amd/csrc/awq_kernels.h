@@ -93,8 +93,9 @@ struct RouteArgs {
   int E, type, topk, groups, topk_groups, group_top;
   bool softmax, renormalize;
   float scale;
+  bool wide;  // set by the launch
 };
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+hipError_t launch_route(RouteArgs a, hipStream_t stream);
 
 // One product of routed rows with their experts' weights (awq_moe_gate_up, awq_moe_down).
 // Slot s of the S routed slots multiplies row s / row_div of x by the weight of expert
