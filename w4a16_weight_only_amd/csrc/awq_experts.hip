@@ -472,28 +472,39 @@ hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertPlan& tp, con
 // y[t] = sum over j of weights[t, j] * (sum over splits of sums[split][t topk + j]).  A
 // workgroup takes 256 / PARTS groups of four columns; PARTS threads share one, each adding
 // every PARTS-th (slot, split) term in order, and meet in LDS in order: the bits do not
-// depend on the schedule.  PARTS > 1 where there are few columns in all, so that the loads of
-// a column group are in flight together.
+// depend on the schedule.  PARTS > 1 where there are few columns in all.  Four terms' loads go
+// out together, whether routed or not (the sums of a slot that is not are memory no one wrote,
+// and are dropped), so a term's latency is not the next one's.
 template <bool BF16, int PARTS>
 __global__ __launch_bounds__(256) void expert_combine_kernel(const float* __restrict__ sums,
                                                              const int32_t* __restrict__ ids,
                                                              const float* __restrict__ weights, int64_t quads, int S,
                                                              int topk, int E, int N, int splits,
                                                              uint16_t* __restrict__ y) {
-  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
   __shared__ floatx4 meet[PARTS > 1 ? 256 : 1];
   const int part = threadIdx.x % PARTS;
   const int64_t q_raw = (int64_t)blockIdx.x * (256 / PARTS) + threadIdx.x / PARTS;
   const int64_t q = q_raw < quads ? q_raw : quads - 1;
   const int64_t t = q / (N / 4);
   const int n = 4 * (int)(q - t * (N / 4));
+  const int terms = topk * splits;
   floatx4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = part; i < topk * splits; i += PARTS) {
-    const int j = i / splits, sp = i - j * splits;
-    const int64_t s = t * topk + j;
-    const int e = ids[s];
-    if (e >= 0 && e < E) a += weights[s] * *reinterpret_cast<const floatx4*>(sums + ((int64_t)sp * S + s) * N + n);
+  for (int i0 = part; i0 < terms; i0 += 4 * PARTS) {
+    floatx4 v[4];
+    float w[4];
+    int e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u * PARTS, terms - 1);
+      const int j = splits == 1 ? i : i / splits;
+      const int64_t s = t * topk + j;
+      e[u] = ids[s];
+      w[u] = weights[s];
+      v[u] = *reinterpret_cast<const floatx4*>(sums + ((int64_t)(i - j * splits) * S + s) * N + n);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * PARTS < terms && e[u] >= 0 && e[u] < E) a += w[u] * v[u];
   }
   if constexpr (PARTS > 1) {
     meet[threadIdx.x] = a;
@@ -506,6 +517,8 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const float* __rest
     *reinterpret_cast<u32x2_t*>(y + t * N + n) = u32x2_t{pack_act2<BF16>(a[0], a[1]), pack_act2<BF16>(a[2], a[3])};
 }
 
+constexpr int64_t kFewQuads = 32768;
+
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
                                  int N, int splits, bool bf16, uint16_t* y, hipStream_t stream) {
   const int64_t quads = (int64_t)T * (N / 4);
@@ -514,7 +527,7 @@ hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const fl
     hipLaunchKernelGGL(kern, dim3((unsigned)((quads + per - 1) / per)), dim3(256), 0, stream, sums, ids, weights,
                        quads, T * topk, topk, E, N, splits, y);
   };
-  const bool few = quads * 8 <= 65536 && topk * splits > 2;  // fewer threads than the card holds
+  const bool few = quads <= kFewQuads && topk * splits > 2;
   if (bf16) {
     if (few) go(expert_combine_kernel<true, 8>, 8);
     else go(expert_combine_kernel<true, 1>, 1);

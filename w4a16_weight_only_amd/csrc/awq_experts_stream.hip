@@ -1,26 +1,30 @@
 // Few rows per routed expert: bandwidth-bound streaming of the experts' packed weights.
 //
-// A workgroup takes up to 16 routed rows of one expert (an entry), 256 columns (gated: the
-// same 256 of both halves) and one K split.  Its four waves each take a run of 32-row
+// A workgroup takes up to 16 or 32 routed rows of one expert (an entry), 256 columns (gated:
+// the same 256 of both halves) and one K split.  Its four waves each take a run of 32-row
 // k-steps; gated, even waves take the gate's columns and odd ones the up projection's.  On
 // v_mfma_f32_16x16x32 lane l = 16 q + c loads words 2 c, 2 c + 1 of rows 8 q .. 8 q + 7 (16
 // lanes: 128 contiguous bytes of a row) and unpacks them into operands of exact integers, 16
-// columns x 8 rows; its row of x is row l % 16 of the entry.
+// columns x 8 rows; its rows of x are rows l % 16 (and 16 + l % 16: an operand unpacked once
+// serves both blocks of 16 rows) of the entry.
 //   fp16       operand q - z
 //   bfloat16   (no packed bfloat16 addition on this chip) operand 128 + q, and one more MFMA
 //              against ones for the rows' sums of x:  x . (128 + q) - (128 + z) x . 1
 // The running sums are in units of the current group's scale u: a group boundary multiplies
 // them by u / u' (a second set of 64 accumulator registers, scaled group by group, spills).
-// A scale of zero cannot be a unit: the unit stays, and the column's sums are put aside in LDS
-// when such a group begins and taken back when it ends (rare; a loop body with zeroed operands
-// would cost every group registers).
-// Group data (zeros and scales) comes with the first k-step of a group in the same ring of
-// two k-steps, so a wave never waits for it alone.
+// A scale of zero cannot be a unit: the unit stays, and the column's operands become zeros, by
+// its codes replaced with its zero code (fp16), or cleared together with its 128 (bfloat16: a
+// difference of rounded sums would not be zero).  That is rare, and outside the MFMAs' code: a
+// second copy of those makes the compiler move accumulators about.
+// A ring of two k-steps is in flight, and with each a group's zeros and scales where one begins.
+// bfloat16 sums of 32 rows leave no registers for two sets of those: there the next group's are
+// asked for when a group begins (both ways: 64 tokens through 8 x 4096 -> 14336 209 -> 187 us in
+// bfloat16, which had spilled; one token through 64 x 2048 -> 1408 25.0 -> 27.0 in fp16).
 // The waves meet in LDS.  With one split a gated workgroup writes h; otherwise fp32 sums
 // [split][slot][column] leave for the next kernel, which adds the splits in order.
 //
 // Which rows a workgroup has: up to 64 slots, every wave ranks them itself (one slot per
-// lane); above, the table of launch_moe_align in blocks of 16 rows.
+// lane); above, the table of launch_moe_align in blocks of 16 or 32 rows.
 #include "awq_device.h"
 #include "awq_kernels.h"
 
@@ -38,22 +42,24 @@ constexpr int kYld = kExpertStreamCols + 4;  // floats of a staged output row
 // Entry v of a lane's 16 columns: word v / 8, byte (v / 2) % 4, nibble v % 2.
 __device__ constexpr int col_of(int v) { return (v & 1) ? hi_col((v >> 1) & 3) : lo_col((v >> 1) & 3); }
 
+template <int RB>
 struct Step {
   u32x2 w[8];        // rows 8 q .. 8 q + 7
-  half8v x;          // x[row][8 q ..]
-  u32x2 z;           // group data, with the first k-step of a group (or of the run)
-  half8v s0, s1;
+  half8v x[RB];      // x[row][8 q ..], a row of each block
 };
 
-// The 16 MFMAs of a k-step.
-template <bool BF16>
-__device__ __forceinline__ void multiply(const Step& st, const uint32_t (&zs)[16], const UnpackConsts& uk,
-                                         floatx4 (&part)[16], floatx4& sx) {
+// The 16 RB MFMAs of a k-step.  zs: per column, fp16: -(1024 + z) or -(64 + z) twice (low or high
+// nibble); bfloat16: 128 twice, or zeros for a column without a scale.
+template <bool BF16, int RB>
+__device__ __forceinline__ void multiply(const Step<RB>& st, const uint32_t (&zs)[16], const UnpackConsts& uk,
+                                         floatx4 (&part)[RB][16], floatx4 (&sx)[RB]) {
   if constexpr (BF16) {
     const uint32_t one2 = 0x3F803F80u;  // bfloat16 pair (1, 1)
-    sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.x),
-                                                 __builtin_bit_cast(bf16x8, u32x4{one2, one2, one2, one2}), sx, 0, 0,
-                                                 0);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      sx[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.x[rb]),
+                                                       __builtin_bit_cast(bf16x8, u32x4{one2, one2, one2, one2}),
+                                                       sx[rb], 0, 0, 0);
   }
 #pragma unroll
   for (int w = 0; w < 2; ++w)
@@ -63,25 +69,35 @@ __device__ __forceinline__ void multiply(const Step& st, const uint32_t (&zs)[16
       const int il = 8 * w + 2 * t, ih = il + 1;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const uint32_t ra = st.w[2 * p][w], rb = st.w[2 * p + 1][w];
+        const uint32_t wa = st.w[2 * p][w], wb = st.w[2 * p + 1][w];
         uint32_t pb;
-        if (t == 0) pb = pair_byte<0>(ra, rb);
-        else if (t == 1) pb = pair_byte<1>(ra, rb);
-        else if (t == 2) pb = pair_byte<2>(ra, rb);
-        else pb = pair_byte<3>(ra, rb);
-        lo[p] = BF16 ? lo_magic_bf16(pb, uk) : as_u32(lo_minus_zero(pb, as_h2(zs[il]), uk));
-        hi[p] = BF16 ? hi_magic_bf16(pb, uk) : as_u32(hi_minus_zero(pb, as_h2(zs[ih]), uk));
+        if (t == 0) pb = pair_byte<0>(wa, wb);
+        else if (t == 1) pb = pair_byte<1>(wa, wb);
+        else if (t == 2) pb = pair_byte<2>(wa, wb);
+        else pb = pair_byte<3>(wa, wb);
+        lo[p] = BF16 ? (pb & uk.mlo) | zs[il] : as_u32(lo_minus_zero(pb, as_h2(zs[il]), uk));
+        hi[p] = BF16 ? ((pb >> 4) & uk.mlo) | zs[ih] : as_u32(hi_minus_zero(pb, as_h2(zs[ih]), uk));
       }
-      if constexpr (BF16) {
-        const bf16x8 x = __builtin_bit_cast(bf16x8, st.x);
-        part[il] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, lo), part[il], 0, 0, 0);
-        part[ih] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, hi), part[ih], 0, 0, 0);
-      } else {
-        part[il] = __builtin_amdgcn_mfma_f32_16x16x32_f16(st.x, __builtin_bit_cast(half8v, lo), part[il], 0, 0, 0);
-        part[ih] = __builtin_amdgcn_mfma_f32_16x16x32_f16(st.x, __builtin_bit_cast(half8v, hi), part[ih], 0, 0, 0);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        if constexpr (BF16) {
+          const bf16x8 x = __builtin_bit_cast(bf16x8, st.x[rb]);
+          part[rb][il] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, lo), part[rb][il], 0, 0, 0);
+          part[rb][ih] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, hi), part[rb][ih], 0, 0, 0);
+        } else {
+          const half8v x = st.x[rb];
+          part[rb][il] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, __builtin_bit_cast(half8v, lo), part[rb][il], 0, 0, 0);
+          part[rb][ih] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, __builtin_bit_cast(half8v, hi), part[rb][ih], 0, 0, 0);
+        }
       }
     }
 }
+
+// Zeros and scales of a group, for a lane's two words.
+struct GroupData {
+  u32x2 z;
+  half8v s[2];
+};
 
 // Rows of a workgroup's entry: its expert, how many, and their slots (LDS).
 struct Entry {
@@ -94,9 +110,10 @@ __device__ __forceinline__ int bits_below(uint64_t mask) {
 }
 
 // Entries of at most 64 slots, ranked by each wave (lane l: slot l): the slots of an expert,
-// in order, in blocks of 16; entries in the order of their first slot.  rows 0: no such entry.
+// in order, in blocks of ROWS; entries in the order of their first slot.  rows 0: no such entry.
 // A lane's mask of slots with its expert comes from one ballot per bit of the id (a loop over
 // the slots took 5 us of 64 slots' 20).
+template <int ROWS>
 __device__ __forceinline__ Entry rank_entry(const int32_t* ids, int S, int E, int entry, int lane, int32_t* slots) {
   const int id = lane < S ? ids[lane] : -1;
   const bool routed = id >= 0 && id < E;
@@ -108,22 +125,23 @@ __device__ __forceinline__ Entry rank_entry(const int32_t* ids, int S, int E, in
     same &= ((id >> b) & 1) ? set : ~set;
   }
   const int rank = bits_below(same);  // among the lower slots of the same expert
-  const bool lead = routed && (rank & 15) == 0;
+  const bool lead = routed && rank % ROWS == 0;
   const uint64_t leads = __ballot(lead);
   const uint64_t found = __ballot(lead && bits_below(leads) == entry);
   if (found == 0) return Entry{0, 0};
   const int at = __builtin_ctzll(found);
   const int expert = __builtin_amdgcn_readlane(id, at);
   const int first = __builtin_amdgcn_readlane(rank, at);
-  const bool mine = routed && id == expert && rank >= first && rank < first + 16;
+  const bool mine = routed && id == expert && rank >= first && rank < first + ROWS;
   if (mine) slots[rank - first] = lane;  // every wave writes the same
   return Entry{expert, (int)__builtin_popcountll(__ballot(mine))};
 }
 
 }  // namespace
 
-// RL: lanes whose sums are kept, 16 per four rows (an entry never has more than RL / 4 rows).
-template <bool GATED, bool BF16, int RL>
+// RB: blocks of 16 rows.  RL: lanes whose sums are kept, 16 per four rows (an entry of one block
+// never has more than RL / 4 rows).
+template <bool GATED, bool BF16, int RB, int RL>
 __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const ExpertProduct p, int entries, int tiles,
                                                                     int splits, int steps,
                                                                     const int32_t* __restrict__ sorted,
@@ -133,7 +151,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
     floatx4 red[kWaves][16][RL];  // [wave][column entry][lane]
     float ys[RL / 4][GATED ? 2 : 1][kYld];
   } sh;
-  __shared__ int32_t slots[16];
+  __shared__ int32_t slots[16 * RB];
 
   // Block order: splits fastest, then column tiles, then entries.
   const int split = blockIdx.x % splits;
@@ -146,7 +164,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   const int q = lane >> 4, c = lane & 15;
   Entry en;
   if (table == nullptr) {
-    en = rank_entry(p.ids, p.S, p.E, entry, lane, slots);
+    en = rank_entry<16 * RB>(p.ids, p.S, p.E, entry, lane, slots);
   } else {
     en.expert = table[4 * entry];
     en.rows = en.expert < 0 ? 0 : table[4 * entry + 2];
@@ -167,8 +185,13 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   // Columns past N read the tile's first ones and are not stored.
   const int wc_in = tile * (kExpertStreamCols / 8) + 2 * c;
   const int wc = (wc_in < (N >> 3) ? wc_in : tile * (kExpertStreamCols / 8)) + half * (N >> 3);
-  const int xrow = slots[c < en.rows ? c : 0] / p.row_div;
-  const uint32_t x_off = ((uint32_t)xrow * (uint32_t)K + 8u * q) * 2u;
+  uint32_t x_off[RB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int r = 16 * rb + c;
+    const int xrow = slots[r < en.rows ? r : 0] / p.row_div;
+    x_off[rb] = ((uint32_t)xrow * (uint32_t)K + 8u * q) * 2u;
+  }
   const uint32_t row_bytes = (uint32_t)NW * 4u;
   const uint32_t w_off = (uint32_t)(8 * q) * row_bytes + (uint32_t)wc * 4u;
   const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
@@ -178,163 +201,183 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   const int s0 = split * PARTS * steps;
   const int kb = min(T, s0 + part_of * steps), ke = min(T, kb + steps);
 
-  // Groups of the k-step loaded next and of the one multiplied next, and where they end.
-  const int g0 = kb / gsteps;
-  int load_group = g0 - 1, load_end = kb, use_end = kb;
-  auto issue = [&](Step& st, int ks) {
-    if (ks == load_end) {
-      ++load_group;
-      load_end = (load_group + 1) * gsteps;
-      const int64_t at = (int64_t)load_group * NW + wc;
-      st.z = *reinterpret_cast<const u32x2*>(qzeros + at);
-      st.s0 = *reinterpret_cast<const half8v*>(scales + 8 * at);
-      st.s1 = *reinterpret_cast<const half8v*>(scales + 8 * at + 8);
-    }
+  // Group data: one set for each k-step in flight, or one in all.
+  constexpr bool kOneSet = BF16 && RB == 2;
+  GroupData data[kOneSet ? 1 : kPF];
+  // The group loaded next and entered next, and the k-steps they begin with.
+  int load_group = kb / gsteps, load_at = kb, enter_at = kb;
+  const int first_end = (load_group + 1) * gsteps;
+  auto fetch = [&](GroupData& d) {
+    const int64_t at = (int64_t)load_group * NW + wc;
+    d.z = *reinterpret_cast<const u32x2*>(qzeros + at);
+    d.s[0] = *reinterpret_cast<const half8v*>(scales + 8 * at);
+    d.s[1] = *reinterpret_cast<const half8v*>(scales + 8 * at + 8);
+    load_at = ++load_group * gsteps;
+  };
+  // Loads of k-step ks.  Group data goes first: a wait for the weights counts back from the
+  // newest load, and must not have to allow for loads that may not have been made.
+  auto issue = [&](Step<RB>& st, int slot, int ks) {
+    if (!kOneSet && ks == load_at) fetch(data[kOneSet ? 0 : slot]);
     const uint32_t r0 = (uint32_t)ks * 32u;
 #pragma unroll
     for (int r = 0; r < 8; ++r)
       st.w[r] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wrs, w_off, (r0 + r) * row_bytes, 2));
-    st.x = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(p.x) + (uint64_t)x_off + r0 * 2u);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      st.x[rb] = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(p.x) + (uint64_t)x_off[rb] + r0 * 2u);
   };
 
-  floatx4 part[16];
-  floatx4 sx = {0.f, 0.f, 0.f, 0.f};
+  const UnpackConsts uk = unpack_consts();
+  floatx4 part[RB][16], sx[RB];
   uint32_t zs[16];
-  half8v unit[2];    // the columns' current units
-  uint32_t nil = 0;  // columns whose scale is zero in the current group
+  half8v unit[2];          // the columns' current units
+  u32x2 zw = {0u, 0u};     // the current group's zero codes
+  u32x2 nil = {0u, 0u};    // nibbles of columns whose scale is zero in the current group
   bool any_nil = false;
 #pragma unroll
   for (int v = 0; v < 16; ++v) {
-    part[v] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) part[rb][v] = floatx4{0.f, 0.f, 0.f, 0.f};
     zs[v] = 0;
     unit[v >> 3][v & 7] = (_Float16)1.f;
   }
-  // A group ends: sums of columns without a scale are those from before it.
-  auto leave = [&] {
 #pragma unroll
-    for (int v = 0; v < 16; ++v)
-      if constexpr (BF16) part[v] -= __builtin_bit_cast(float, zs[v]) * sx;
-    if (any_nil) {
+  for (int rb = 0; rb < RB; ++rb) sx[rb] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // A group ends: bfloat16 sums lose their zeros' share.
+  auto leave = [&] {
+    if constexpr (BF16) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const floatx4 kept = sh.red[wave][v][lane % RL];
-        if ((nil >> v) & 1) part[v] = kept;
+        const float z = zs[v] == 0u ? 0.f : 128.0f + (float)zero_code(zw[v >> 3], col_of(v));
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) part[rb][v] -= z * sx[rb];
       }
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) sx[rb] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
   };
   // A group begins: the sums so far change units (there are none when the run begins).
-  auto enter = [&](const Step& st, bool begin) {
-    nil = 0;
+  auto enter = [&](const GroupData& d, bool begin) {
+    nil = u32x2{0u, 0u};
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
-      const _Float16 s = v < 8 ? st.s0[col_of(v)] : st.s1[col_of(v)];
+      const _Float16 s = d.s[v >> 3][col_of(v)];
       const _Float16 old = unit[v >> 3][v & 7];
       const bool none = s == (_Float16)0.f;
       const _Float16 now = none ? old : s;
       if (!begin) {
-        part[v] *= (float)old * __builtin_amdgcn_rcpf((float)now);
+        const float ratio = (float)old * __builtin_amdgcn_rcpf((float)now);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) part[rb][v] *= ratio;
       }
       unit[v >> 3][v & 7] = now;
-      nil |= none ? 1u << v : 0u;
-      const uint32_t z = zero_code(st.z[v >> 3], col_of(v));
+      nil[v >> 3] |= none ? 0xFu << (4 * (v & 7)) : 0u;  // entry v is nibble v % 8 of its word
       if constexpr (BF16) {
-        zs[v] = __builtin_bit_cast(uint32_t, 128.0f + (float)z);
+        zs[v] = none ? 0u : uk.bmagic;
       } else {
+        const uint32_t z = zero_code(d.z[v >> 3], col_of(v));
         const uint32_t h = (v & 1) ? (0xD400u | (z << 4)) : (0xE400u | z);  // -(64 + z), -(1024 + z)
         zs[v] = h | (h << 16);
       }
     }
-    sx = floatx4{0.f, 0.f, 0.f, 0.f};
-    any_nil = __builtin_amdgcn_ballot_w64(nil != 0) != 0;
-    if (any_nil && lane < RL) {
-#pragma unroll
-      for (int v = 0; v < 16; ++v) sh.red[wave][v][lane] = part[v];
-    }
+    zw = d.z;
+    enter_at = begin ? first_end : enter_at + gsteps;
+    any_nil = __builtin_amdgcn_ballot_w64((nil[0] | nil[1]) != 0) != 0;
   };
-  const UnpackConsts uk = unpack_consts();
-  Step ring[kPF];
+  Step<RB> ring[kPF];
+  if (kOneSet && kb < ke) fetch(data[0]);
 #pragma unroll
   for (int j = 0; j < kPF; ++j)
-    if (kb + j < ke) issue(ring[j], kb + j);
+    if (kb + j < ke) issue(ring[j], j, kb + j);
   for (int base = kb; base < ke; base += kPF) {
 #pragma unroll
     for (int j = 0; j < kPF; ++j) {
       const int ks = base + j;
       if (ks < ke) {
-        if (ks == use_end) {
+        const bool begins = ks == enter_at;
+        if (begins) {
           if (ks != kb) leave();
-          enter(ring[j], ks == kb);
-          use_end = ks == kb ? (g0 + 1) * gsteps : use_end + gsteps;
+          enter(data[kOneSet ? 0 : j], ks == kb);
         }
-        multiply<BF16>(ring[j], zs, uk, part, sx);
-        if (ks + kPF < ke) issue(ring[j], ks + kPF);
+        if (any_nil) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) ring[j].w[r] = (ring[j].w[r] & ~nil) | (BF16 ? u32x2{0u, 0u} : zw & nil);
+        }
+        multiply<BF16, RB>(ring[j], zs, uk, part, sx);
+        if (kOneSet && begins && load_at < ke) fetch(data[0]);
+        if (ks + kPF < ke) issue(ring[j], j, ks + kPF);
       }
     }
   }
   if (kb < ke) leave();
-#pragma unroll
-  for (int v = 0; v < 16; ++v) part[v] *= (float)unit[v >> 3][v & 7];
 
-  // Waves -> LDS, then one thread per (column entry, lane of rows): four rows of one column.
-  if (lane < RL) {
-#pragma unroll
-    for (int v = 0; v < 16; ++v) sh.red[wave][v][lane] = part[v];
-  }
-  __syncthreads();
+  // Per block of 16 rows: waves -> LDS, then one thread per (column entry, lane of rows) sums
+  // four rows of one column, and the rows leave in order.
   constexpr int SLOTS = 16 * RL / kThreads;  // sums per thread: 1, 2 or 4
-  floatx4 sum[SLOTS][GATED ? 2 : 1];
-#pragma unroll
-  for (int k = 0; k < SLOTS; ++k) {
-    const int i = tid + k * kThreads;
-    const int v = (i >> 4) & 15, ln = (i >> 8) * 16 + (i & 15);
-#pragma unroll
-    for (int hf = 0; hf < (GATED ? 2 : 1); ++hf) {
-      floatx4 a = sh.red[hf][v][ln];
-#pragma unroll
-      for (int w = 1; w < PARTS; ++w) a += sh.red[GATED ? 2 * w + hf : w][v][ln];
-      sum[k][hf] = a;
-    }
-  }
-  __syncthreads();  // the sums are in registers: their LDS takes the output rows
+  constexpr int HALVES = GATED ? 2 : 1;
   const bool finish = GATED && splits == 1;
-#pragma unroll
-  for (int k = 0; k < SLOTS; ++k) {
-    const int i = tid + k * kThreads;
-    const int v = (i >> 4) & 15, cc = i & 15;
-    const int col = 8 * (2 * cc + (v >> 3)) + col_of(v);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * (i >> 8) + r;
-      if constexpr (GATED) {
-        sh.ys[row][0][col] = finish ? gated(sum[k][0][r], sum[k][1][r]) : sum[k][0][r];
-        sh.ys[row][1][col] = sum[k][1][r];
-      } else {
-        sh.ys[row][0][col] = sum[k][0][r];
-      }
-    }
-  }
-  __syncthreads();
   const int n0 = tile * kExpertStreamCols;
-  if (finish) {
-    for (int i = tid; i < en.rows * (kExpertStreamCols / 8); i += kThreads) {
-      const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
-      if (n0 + cp < N) {
-        const float* y = &sh.ys[row][0][cp];
-        *reinterpret_cast<u32x4*>(p.h + (int64_t)slots[row] * N + n0 + cp) =
-            u32x4{pack_act2<BF16>(y[0], y[1]), pack_act2<BF16>(y[2], y[3]), pack_act2<BF16>(y[4], y[5]),
-                  pack_act2<BF16>(y[6], y[7])};
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int rows = min(en.rows - 16 * rb, 16);
+    if (rows <= 0) break;  // the same in every wave
+    if (rb > 0) __syncthreads();  // the last block's rows have left
+    if (lane < RL) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) sh.red[wave][v][lane] = part[rb][v] * (float)unit[v >> 3][v & 7];
+    }
+    __syncthreads();
+    floatx4 sum[SLOTS][HALVES];
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int i = tid + k * kThreads;
+      const int v = (i >> 4) & 15, ln = (i >> 8) * 16 + (i & 15);
+#pragma unroll
+      for (int hf = 0; hf < HALVES; ++hf) {
+        floatx4 a = sh.red[hf][v][ln];
+#pragma unroll
+        for (int w = 1; w < PARTS; ++w) a += sh.red[GATED ? 2 * w + hf : w][v][ln];
+        sum[k][hf] = a;
       }
     }
-  } else {
-    constexpr int HALVES = GATED ? 2 : 1;
-    float* out = p.sums + (int64_t)split * p.S * (HALVES * N);
-    for (int i = tid; i < en.rows * HALVES * (kExpertStreamCols / 4); i += kThreads) {
-      const int row = i / (HALVES * kExpertStreamCols / 4);
-      const int r = i - row * (HALVES * kExpertStreamCols / 4);
-      const int hf = r / (kExpertStreamCols / 4), cp = 4 * (r % (kExpertStreamCols / 4));
-      if (n0 + cp < N)
-        *reinterpret_cast<floatx4*>(out + ((int64_t)slots[row] * HALVES + hf) * N + n0 + cp) =
-            *reinterpret_cast<const floatx4*>(&sh.ys[row][hf][cp]);
+    __syncthreads();  // the sums are in registers: their LDS takes the output rows
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int i = tid + k * kThreads;
+      const int v = (i >> 4) & 15, cc = i & 15;
+      const int col = 8 * (2 * cc + (v >> 3)) + col_of(v);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 4 * (i >> 8) + r;
+        if constexpr (GATED) {
+          sh.ys[row][0][col] = finish ? gated(sum[k][0][r], sum[k][1][r]) : sum[k][0][r];
+          sh.ys[row][1][col] = sum[k][1][r];
+        } else {
+          sh.ys[row][0][col] = sum[k][0][r];
+        }
+      }
+    }
+    __syncthreads();
+    if (finish) {
+      for (int i = tid; i < rows * (kExpertStreamCols / 8); i += kThreads) {
+        const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
+        if (n0 + cp < N) {
+          const float* y = &sh.ys[row][0][cp];
+          *reinterpret_cast<u32x4*>(p.h + (int64_t)slots[16 * rb + row] * N + n0 + cp) =
+              u32x4{pack_act2<BF16>(y[0], y[1]), pack_act2<BF16>(y[2], y[3]), pack_act2<BF16>(y[4], y[5]),
+                    pack_act2<BF16>(y[6], y[7])};
+        }
+      }
+    } else {
+      float* out = p.sums + (int64_t)split * p.S * (HALVES * N);
+      for (int i = tid; i < rows * HALVES * (kExpertStreamCols / 4); i += kThreads) {
+        const int row = i / (HALVES * kExpertStreamCols / 4);
+        const int r = i - row * (HALVES * kExpertStreamCols / 4);
+        const int hf = r / (kExpertStreamCols / 4), cp = 4 * (r % (kExpertStreamCols / 4));
+        if (n0 + cp < N)
+          *reinterpret_cast<floatx4*>(out + ((int64_t)slots[16 * rb + row] * HALVES + hf) * N + n0 + cp) =
+              *reinterpret_cast<const floatx4*>(&sh.ys[row][hf][cp]);
+      }
     }
   }
 }
@@ -347,9 +390,10 @@ hipError_t launch_expert_stream(const ExpertProduct& p, const ExpertPlan& ep, co
   };
 #define AWQ_STREAM(GATED, BF16)                                            \
   do {                                                                     \
-    if (ep.rows == 4) go(expert_stream_kernel<GATED, BF16, 16>);           \
-    else if (ep.rows == 8) go(expert_stream_kernel<GATED, BF16, 32>);      \
-    else go(expert_stream_kernel<GATED, BF16, 64>);                        \
+    if (ep.rows == 4) go(expert_stream_kernel<GATED, BF16, 1, 16>);        \
+    else if (ep.rows == 8) go(expert_stream_kernel<GATED, BF16, 1, 32>);   \
+    else if (ep.rows == 16) go(expert_stream_kernel<GATED, BF16, 1, 64>);  \
+    else go(expert_stream_kernel<GATED, BF16, 2, 64>);                     \
   } while (0)
   if (p.gated) {
     if (p.bf16) AWQ_STREAM(true, true);
@@ -372,10 +416,10 @@ __global__ __launch_bounds__(256) void expert_gate_kernel(const float* __restric
   const int64_t s = i / (N / 4);
   const int n = 4 * (int)(i - s * (N / 4));
   const int e = ids[s];
-  if (e < 0 || e >= E) return;
   const float* at = sums + s * 2 * N + n;
   const int64_t stride = (int64_t)S * 2 * N;
   const floatx4 g = sum_splits<8>(at, stride, splits), u = sum_splits<8>(at + N, stride, splits);
+  if (e < 0 || e >= E) return;  // behind the loads, which need not wait for it
   *reinterpret_cast<u32x2*>(h + s * N + n) = u32x2{pack_act2<BF16>(gated(g[0], u[0]), gated(g[1], u[1])),
                                                   pack_act2<BF16>(gated(g[2], u[2]), gated(g[3], u[3]))};
 }

@@ -504,23 +504,25 @@ int plan_expert(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int cu
   p = ExpertPlan{};
   const int64_t S = T * topk;
   const int64_t wide = gated ? 2 * N : N;
-  // 32-bit byte offsets into one expert's weight.
-  p.stream = S <= 16 * E && K * (wide / 2) < k2p32 - 4096;
+  // Few rows per expert, or too few row tiles to fill half of the card.  (Streaming: 32-bit byte
+  // offsets into one expert's weight.)
+  const int64_t tile_cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
+  const int64_t row_tiles = (S + kExpertTileRows - 1) / kExpertTileRows * ((N + tile_cols - 1) / tile_cols);
+  p.stream = (S <= kExpertStreamRows * E || 2 * row_tiles <= cus) && K * (wide / 2) < k2p32 - 4096;
   if (p.stream) {
     p.ranked = S <= kExpertRankSlots;
-    p.rows = S <= 4 ? 4 : S <= 8 ? 8 : 16;
-    p.block_rows = 16;
+    p.rows = S <= 4 ? 4 : S <= 8 ? 8 : S < kExpertWideRows * E ? 16 : 32;
+    p.block_rows = p.rows == 32 ? 32 : 16;
     p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
-    p.tiles = p.ranked ? entry_bound(S, E, 16) : moe_tiles(S, E, 16);
+    p.tiles = p.ranked ? entry_bound(S, E, p.block_rows) : moe_tiles(S, E, p.block_rows);
     choose_splits(T, topk, E, K, wide, cus, gated, p);
     p.grid = p.tiles * p.col_tiles * p.splits;
     p.sums_bytes = gated && p.splits == 1 ? 0 : round_up(p.splits * S * wide * 4, 256);
     if (!p.ranked) p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
   } else {
-    const int64_t cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
     p.rows = p.block_rows = kExpertTileRows;
     p.tiles = moe_tiles(S, E, p.block_rows);
-    p.col_tiles = (int)((N + cols - 1) / cols);
+    p.col_tiles = (int)((N + tile_cols - 1) / tile_cols);
     p.grid = 2 * p.tiles * p.col_tiles;  // long entries, then short ones
     p.table_bytes = round_up(p.tiles * 16 + (E + 1 + S) * 4, 256);
     p.sums_bytes = gated ? 0 : round_up(S * N * 4, 256);

@@ -182,7 +182,7 @@ int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t
 
 // One product of routed rows with their experts' weights (gated: N pairs of columns of a
 // 2 N wide weight).  Entries are up to `rows` routed rows of one expert:
-//   stream   few rows per expert: 4, 8 or 16 rows kept, workgroups over (entry, column tile
+//   stream   few rows per expert: 4, 8, 16 or 32 rows kept, workgroups over (entry, column tile
 //            of 256 columns, K split); each wave of a workgroup takes `steps` k-steps of 32
 //   tiles    otherwise: row tiles of up to 256 x 256 over the sorted slots, one split
 struct ExpertPlan {
@@ -200,6 +200,15 @@ struct ExpertPlan {
 constexpr int kExpertTileRows = 256;
 constexpr int kExpertTileCols = 256;    // weight columns of a workgroup
 constexpr int kExpertStreamCols = 256;  // columns of a workgroup (gated: of each half)
+// Most slots per expert, on average, to stream.  Measured, us per call, streamed / tiles: mlp
+// 64 x 2048 -> 1408, 32, 64, 96, 128 slots per expert 150 / 197, 222 / 251, 307 / 290, 380 / 313;
+// 8 x 4096 -> 14336, 64, 96, 128: 527 / 650, 640 / 703, 806 / 764; one expert 4096 -> 4096 (64
+// and 32 tiles' workgroups), 512 rows 119 / 252.
+constexpr int64_t kExpertStreamRows = 80;
+// Slots per expert from which entries take 32 rows: 16 / 32 rows, mlp 64 x 2048 -> 1408, 4, 8,
+// 16, 32 slots per expert 87 / 92, 101 / 98, 128 / 115, 186 / 150; 8 x 4096 -> 14336, 8, 12, 16:
+// 159 / 192, 199 / 202, 237 / 209.
+constexpr int64_t kExpertWideRows = 12;
 constexpr int64_t kExpertMaxSplits = 32;
 constexpr int64_t kExpertRankSlots = 64;  // slots a wave can rank, one per lane
 // The gated MLP of routed experts and its two halves: which products it makes, and the
