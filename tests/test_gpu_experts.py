@@ -175,24 +175,105 @@ def test_long_axes(T, E, topk, K, inner, N, g, dtype):
     assert torch.equal(awq.awq_moe_mlp(x, up.dev, down.dev, ids, w, g), y)
 
 
+# Row tiles: more than 80 slots per expert, and enough columns that the tiles fill half of the
+# card.  Rows per expert around every height of a tile (64, 128, 192, 256), one more than one,
+# none, a few.
+COUNTS = [(300, 190, 0, 130, 100, 64, 20, 1), (512, 257, 193, 129, 65), (256, 192, 128, 64)]
+
+
+def routed_by_counts(counts, seed):
+    """topk 1: counts[e] tokens of expert e, shuffled."""
+    ids = np.random.default_rng(seed).permutation(np.repeat(np.arange(len(counts)), counts)).astype(np.int32)
+    w = np.random.default_rng(seed + 1).uniform(0.1, 1.0, (ids.size, 1)).astype(np.float32)
+    return torch.from_numpy(ids[:, None]).cuda(), torch.from_numpy(w).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("counts", COUNTS, ids=["eight", "five", "four"])
+@pytest.mark.parametrize("K,g", [(32, 32), (96, 32), (160, 160), (320, 64), (256, 128), (288, 96), (384, 128), (480, -1)])
+def test_row_tiles(K, g, counts, dtype):
+    E, T = len(counts), sum(counts)
+    print(f"row tiles K={K} g={g} counts={counts} {dtype}", flush=True)
+    ids, w = routed_by_counts(counts, K)
+    x = activations((T, K), dtype, K + 1)
+    up = Layer(E, K, 2 * 4512, g, 3)
+    close(awq.awq_moe_gate_up(x, *up.dev, ids, g), *gate_up_ref(x, up, ids, dtype), "gate_up")
+    down = Layer(E, K, 8736, g, 4)
+    close(awq.awq_moe_down(x, *down.dev, ids, w, g), *down_ref(x, down, ids, w, dtype), "down")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+def test_row_tiles_odd_scales_and_slots(dtype):
+    """Zero and negative scales, unrouted slots and a token's repeated expert on row tiles."""
+    T, E, topk, K, g, N = 420, 4, 2, 160, 32, 9120
+    up, down = Layer(E, K, 2 * 4544, g, 5, odd_scales), Layer(E, K, N, g, 6, odd_scales)
+    ids, w = routing(T, E, topk, 7)
+    ids[3], ids[5, 1], ids[9] = torch.tensor([-1, E]), E + 3, torch.tensor([2, 2])
+    w[3] = float("nan")
+    x, h = activations((T, K), dtype, 8), activations((T * topk, K), dtype, 9)
+    live = ((ids >= 0) & (ids < E)).flatten()
+    out = torch.full((T * topk, 4544), 7.0, dtype=dtype, device="cuda")
+    awq.awq_moe_gate_up(x, *up.dev, ids, g, out=out)
+    assert (out[~live] == 7.0).all() and torch.equal(out[18], out[19])
+    ref, tol = gate_up_ref(x, up, ids, dtype)
+    m = live.cpu().numpy()
+    close(out[live], ref[m], tol[m], "gate_up")
+    y = awq.awq_moe_down(h, *down.dev, ids, w, g)
+    assert (y[3] == 0).all()
+    close(y, *down_ref(h, down, ids, w, dtype), "down")
+
+
+@pytest.mark.parametrize("T,E,topk,K,inner,N", [(9000, 4, 2, 64, 32, 64), (700, 3, 25, 32, 32, 32)])
+def test_more_slots_than_the_alignment_holds(T, E, topk, K, inner, N):
+    """Over 16384 slots: the alignment counts those beyond in a second pass."""
+    up, down = Layer(E, K, 2 * inner, 32, 8), Layer(E, inner, N, 32, 9)
+    x = activations((T, K), torch.float16, 10)
+    ids, w = routing(T, E, topk, 11)
+    h = awq.awq_moe_gate_up(x, *up.dev, ids, 32)
+    close(h, *gate_up_ref(x, up, ids, torch.float16), "gate_up")
+    close(awq.awq_moe_down(h, *down.dev, ids, w, 32), *down_ref(h, down, ids, w, torch.float16), "down")
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn(seed):
+    """Sizes, types, routing and group sizes drawn at random."""
+    rng = np.random.default_rng(500 + seed)
+    g = int(rng.choice([32, 64, 96, 128, -1]))
+    step = 32 if g == -1 else g
+    E = int(rng.choice([1, 2, 7, 16, 33]))
+    topk = int(rng.integers(1, min(E, 6) + 1))
+    T = int(np.exp(rng.uniform(0, np.log(400))))
+    K, inner = step * int(rng.integers(1, max(2, 640 // step))), step * int(rng.integers(1, max(2, 512 // step)))
+    N = 32 * int(rng.integers(1, 24))
+    dtype = torch.float16 if seed % 2 else torch.bfloat16
+    print(f"drawn T={T} E={E} topk={topk} K={K} inner={inner} N={N} g={g} {dtype}", flush=True)
+    up, down, x, ids, w = big(T, E, topk, K, inner, N, g, dtype, seed)
+    h = awq.awq_moe_gate_up(x, *up.dev, ids, g)
+    close(h, *gate_up_ref(x, up, ids, dtype), "gate_up")
+    y = awq.awq_moe_down(h, *down.dev, ids, w, g)
+    close(y, *down_ref(h, down, ids, w, dtype), "down")
+    assert torch.equal(awq.awq_moe_mlp(x, up.dev, down.dev, ids, w, g), y)
+
+
+def odd_scales(layer):
+    """Scales of zero (single groups, both signs, whole columns), negative ones, and neighbours
+    at both ends of fp16's range within one column."""
+    s, G = layer.sc, layer.sc.shape[1]
+    s[:, 0, ::7] = 0.0
+    s[:, 3 % G, 1::5] = -0.0
+    s[:, -1, 2::9] = 0.0
+    s[1, :, 4::11] = 0.0
+    s[:, 2 % G] *= -1
+    s[:, 4 % G, 6::13] = 6e-8
+    s[:, 1 % G, 6::13] = 0.01
+    s[:, 2 % G, 6::13] = 6e-8
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
 @pytest.mark.parametrize("T", [2, 40, 300])
 def test_odd_scales(T, dtype):
-    """Scales of zero (single groups, both signs, whole columns), negative ones, and neighbours
-    at both ends of fp16's range within one column."""
     K, inner, N, g, E = 256, 64, 96, 32, 3
-
-    def edit(layer):
-        s = layer.sc
-        s[:, 0, ::7] = 0.0
-        s[:, 3, 1::5] = -0.0
-        s[:, -1, 2::9] = 0.0
-        s[1, :, 4::11] = 0.0
-        s[:, 2] *= -1
-        s[:, 4, 6::13] = 6e-8
-        s[:, 5, 6::13] = 3.0 / K
-        s[:, 6, 6::13] = 6e-8
-    up, down = Layer(E, K, 2 * inner, g, 31, edit), Layer(E, K, N, g, 32, edit)
+    up, down = Layer(E, K, 2 * inner, g, 31, odd_scales), Layer(E, K, N, g, 32, odd_scales)
     x, h = activations((T, K), dtype, 5), activations((T * 2, K), dtype, 6)
     ids, w = routing(T, E, 2, 7)
     close(awq.awq_moe_gate_up(x, *up.dev, ids, g), *gate_up_ref(x, up, ids, dtype), "gate_up")

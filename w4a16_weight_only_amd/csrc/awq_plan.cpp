@@ -539,6 +539,8 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
   if (inner < 1 || inner > kMaxDim) return inner < 1 ? AWQ_ERR_SHAPE : AWQ_ERR_UNSUPPORTED;
   if (T > kMaxDim || topk > kMaxDim || E > 1024) return AWQ_ERR_UNSUPPORTED;
   const int64_t S = T * topk;
+  // h: read with 32-bit offsets, written by one thread per four values.
+  if (S <= kMaxDim && S * inner * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;
   if (up) {
     const int st = limits_check(S, K, 2 * inner, group_size);
     if (st != AWQ_OK) return st;
@@ -548,7 +550,6 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
   if (down) {
     const int st = limits_check(S, inner, N, group_size);
     if (st != AWQ_OK) return st;
-    if (S * inner * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;
     if (T * (N / 4) + 256 >= k2p32) return AWQ_ERR_UNSUPPORTED;  // one thread per four outputs
   }
   if (T == 0) return AWQ_OK;
