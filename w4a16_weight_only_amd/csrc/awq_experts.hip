@@ -61,9 +61,10 @@ __device__ __forceinline__ int b_addr(int c, int chunk) {
 
 // 16 bytes per lane from a buffer (bounds-checked: past its end nothing is read) straight into
 // LDS: lane l's data lands at lds + 16 l.  Not tracked by the compiler: the kernel waits itself.
-__device__ __forceinline__ void load_lds16_buffer(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
-               "s"(soff), "s"(lds)
+// The whole offset is the lane's: a scalar one is not sure to count in the bounds check.
+__device__ __forceinline__ void load_lds16_buffer(u32x4 rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc),
+               "s"(lds)
                : "memory", "m0");
 }
 // Raw buffer descriptor of `bytes` bytes at a uniform address.
@@ -100,7 +101,7 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
   // x rows: wave w stages rows 8 FM w .. 8 FM w + 8 FM - 1, 8 rows a load; lane l fetches chunk
   // (l % 8) ^ ((row / 2) % 8) of row l / 8 of the eight (rows past the entry repeat its last).
   // The upper chunks of a last k-tile of 32 are the next row's, or past the end of x, and are
-  // not multiplied; so are k-tiles past the last.
+  // not multiplied.  Loads past the last k-tile re-read it (clamped) and are not multiplied.
   const u32x4 xrs = buffer_of(p.x, (uint32_t)p.S / (uint32_t)p.row_div * (uint32_t)K * 2u);
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds);
   uint32_t a_off[FM];
@@ -113,12 +114,14 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
   auto load_a = [&](int buf, int kt) {
     const uint32_t at = lds0 + (uint32_t)(buf * kATile + FM * wave * 1024);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) load_lds16_buffer(xrs, a_off[j], (uint32_t)kt * (kBK * 2u), at + 1024u * j);
+    for (int j = 0; j < FM; ++j)
+      load_lds16_buffer(xrs, a_off[j] + (uint32_t)min(kt, KT - 1) * (kBK * 2u), at + 1024u * j);
   };
 
   // This thread's share of the weights: rows 4 o .. 4 o + 3 of a k-tile, packed column pw.  A
   // wave has 8 rows, one chunk; its lanes' halves of the chunk alternate with the column so
-  // that 32 lanes' 8-byte writes fill all banks.  Rows past K read as zeros.
+  // that 32 lanes' 8-byte writes fill all banks.  Rows past K (of a last k-tile of 32, and of
+  // k-tiles past the last) are read from rows in range instead and not multiplied.
   const int w = lane & 31;
   const int o_half = (lane >> 5) ^ ((w >> 4) & 1);
   const int half_words = N >> 3;
@@ -128,11 +131,12 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
   const uint32_t row_bytes = (uint32_t)NW * 4u;
   const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint32_t*>(qweight), (short)0, (int)(row_bytes * (uint32_t)K), 0x00020000);
-  const uint32_t w_off = (uint32_t)(8 * wave + 4 * o_half) * row_bytes + (uint32_t)pw * 4u;
+  const uint32_t w_off = (uint32_t)min(8 * wave + 4 * o_half, K - 4) * row_bytes + (uint32_t)pw * 4u;
+  const int w_last = wave < 4 ? K - 32 : max(K - kBK, 0);  // where this wave's last rows' k-tile begins
   auto load_words = [&](uint32_t (&words)[4], int kt) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      words[r] = __builtin_amdgcn_raw_buffer_load_b32(wrs, w_off, (uint32_t)(kt * kBK + r) * row_bytes, 0);
+      words[r] = __builtin_amdgcn_raw_buffer_load_b32(wrs, w_off, (uint32_t)(min(kt * kBK, w_last) + r) * row_bytes, 0);
   };
   uint32_t zword;
   u32x4 sraw;
