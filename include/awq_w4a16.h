@@ -319,7 +319,8 @@ int awq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int
  * The result is deterministic.  A NaN or infinity in a row of x or h reaches only that row's
  * token.
  * Limits: those of awq_gemm for each product with M = T * topk (inner % 32 == 0 as well),
- * 1 <= E <= 1024, topk >= 1, x and h below 4 GiB.  T == 0 enqueues nothing.
+ * 1 <= E <= 1024, topk >= 1, x, h and the qweight of one expert below 4 GiB.  T == 0 enqueues
+ * nothing.
  *
  * awq_moe_workspace: bytes for gate_up (N = 0), down (K = 0, inner = its K) or mlp; the
  * negative status that the call would return for these sizes.  Host-only.

@@ -122,6 +122,16 @@ def test_workspace_sizes():
     assert ws(16, 2, 8, 4096, BIG, 4096, 128) == UNSUP
 
 
+@pytest.mark.parametrize("T", [1, 4096])
+def test_one_experts_weight_below_4_gib(T):
+    """32-bit offsets into one expert's weight, in either kernel."""
+    ws = _lib.load().awq_moe_workspace
+    assert ws(T, 1, 1, 1 << 16, 1 << 16, 0, 128) == UNSUP
+    assert ws(T, 1, 1, 0, 1 << 16, 1 << 17, 128) == UNSUP
+    assert ws(T, 1, 1, 1 << 16, 1 << 15, 0, 128) > 0
+    assert ws(T, 1, 1, 0, 1 << 16, 1 << 16, 128) > 0
+
+
 def gate_up(x=P, act=_lib.AWQ_F16, qw=P, qz=P, sc=P, ids=P, T=4, topk=2, E=8, K=256, inner=64, g=64, h=P, ws=P, nb=BIG):
     return _lib.load().awq_moe_gate_up(x, act, qw, qz, sc, ids, T, topk, E, K, inner, g, h, ws, nb, None)
 

@@ -504,11 +504,11 @@ int plan_expert(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int cu
   p = ExpertPlan{};
   const int64_t S = T * topk;
   const int64_t wide = gated ? 2 * N : N;
-  // Few rows per expert, or too few row tiles to fill half of the card.  (Streaming: 32-bit byte
-  // offsets into one expert's weight.)
+  if (K * (wide / 2) >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into one expert's weight
+  // Few rows per expert, or too few row tiles to fill half of the card.
   const int64_t tile_cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
   const int64_t row_tiles = (S + kExpertTileRows - 1) / kExpertTileRows * ((N + tile_cols - 1) / tile_cols);
-  p.stream = (S <= kExpertStreamRows * E || 2 * row_tiles <= cus) && K * (wide / 2) < k2p32 - 4096;
+  p.stream = S <= kExpertStreamRows * E || 2 * row_tiles <= cus;
   if (p.stream) {
     p.ranked = S <= kExpertRankSlots;
     p.rows = S <= 4 ? 4 : S <= 8 ? 8 : S < kExpertWideRows * E ? 16 : 32;
