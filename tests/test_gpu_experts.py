@@ -396,6 +396,43 @@ def test_two_streams_at_once(T):
     assert all(torch.equal(v, want) for v in got)
 
 
+def test_row_tiles_in_graphs_and_on_streams():
+    """Row tiles: graphs replayed side by side on two streams while a third works eagerly, each
+    replay the eager bits."""
+    T, E, topk, K, inner, N, g = 400, 2, 2, 64, 4352, 8704, 64
+    gen = torch.Generator(device="cuda").manual_seed(95)
+
+    def packed(rows, cols):
+        words = lambda *shape: torch.randint(-2 ** 31, 2 ** 31, shape, generator=gen, device="cuda").int()  # noqa: E731
+        sc = (torch.rand(E, rows // g, cols, generator=gen, device="cuda") + 0.5) / (6.5 * rows ** 0.5)
+        return words(E, rows, cols // 8), words(E, rows // g, cols // 8), sc.half()
+
+    up, down = packed(K, 2 * inner), packed(inner, N)
+    ids, w = routing(T, E, topk, 96)
+    xs = [activations((T, K), torch.bfloat16, 97 + i) for i in range(2)]
+    ys = [torch.empty(T, N, dtype=torch.bfloat16, device="cuda") for _ in xs]
+    graphs = []
+    for x, y in zip(xs, ys):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            awq.awq_moe_mlp(x, up, down, ids, w, g, out=y)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(4):
+        for x in xs:
+            x.mul_(0.75)
+        want = [awq.awq_moe_mlp(x, up, down, ids, w, g) for x in xs]
+        assert all(v.float().std() > 0 for v in want)
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = awq.awq_moe_mlp(xs[1], up, down, ids, w, g)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ys + [eager], want + want[1:]))
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
 @pytest.mark.parametrize("T", [1, 33])
 def test_layer_module(T, dtype):
