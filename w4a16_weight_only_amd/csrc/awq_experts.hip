@@ -22,6 +22,19 @@
 // without it makes the compiler move accumulators about).  A barrier ends each turn, and the
 // second four waves are one turn behind.
 // x is loaded two k-tiles ahead (three LDS buffers), words three (registers).
+// Entries of up to 128 rows have the registers for the operands of a whole k-tile, and take one
+// pair of turns for it instead of two: what such a turn costs is its reads and its barrier.  The
+// integers are then staged two k-tiles ahead (three LDS buffers) and x loaded three (four).  Half
+// k-tiles / whole ones, us: gate_up of 128 tokens, one expert 4096 -> 32768, fp16 101 / 95; mlp
+// 64 x 2048 -> 1408, 700 and 1000 tokens top 8, 291 / 281 and 338 / 321; 8 x 4096 -> 14336, 512 and
+// 1500 tokens top 2, 666 / 650 and 1520 / 1465.
+//
+// Bound by the matrix cores and what does not hide behind them.  2048 rows of 4096 -> 2 x 4096,
+// g 128, take 127 us: 1.08 PFLOP/s (a large dense product 1.19; the MFMAs alone 79 us), 13 us of
+// it the launch, the first k-tiles and the epilogue.  Groups of 32 take 175: the rescaling, 128
+// vector multiplications per 16 MFMAs of a wave, no longer hides.  A tile of 64, 128, 192 rows
+// takes 0.60, 0.70, 0.83 of a tile of 256: unpacking and staging the weights is the same for all,
+// so experts' last, short entries cost 13 to 36% of a prompt's products.
 #include <type_traits>
 
 #include "awq_device.h"
@@ -41,7 +54,7 @@ constexpr int kFN = 2;  // 32 x 32 column blocks of a wave
 constexpr int kWM = 2, kWN = 4;
 static_assert(kWN * kFN * 32 == kCols && kWM * 4 * 32 == kRows, "8 waves cover the tile");
 
-// LDS: three k-tiles of x, then two of the staged integers.
+// LDS: three (or four) k-tiles of x, then two (or three) of the staged integers.
 //   x         row r: 128 bytes (64 k), 16-byte chunk c at position c ^ ((r / 2) % 8)
 //   integers  column c: 128 bytes at row c ^ ((c / 8) % 2), chunk o at position o ^ swz(c),
 //             swz(c) = (c ^ (c / 16)) % 8
@@ -50,10 +63,8 @@ static_assert(kWN * kFN * 32 == kCols && kWM * 4 * 32 == kRows, "8 waves cover t
 // for 16 consecutive w.  Chunks and columns differ in address bits that rows do not reach, so a
 // thread keeps one address each and flips bits of it: chunk c + 2 s is address ^ (32 s), column
 // 8 w + j of a writer's word is address ^ (144 j).
-constexpr int kATile = kRows * kBK * 2;
 constexpr int kBTile = kCols * kBK * 2;
-constexpr int kBBase = 3 * kATile;
-constexpr int kLdsBytes = kBBase + 2 * kBTile;
+constexpr int kLdsBytes = 3 * kRows * kBK * 2 + 2 * kBTile;
 static_assert(kLdsBytes <= 160 * 1024, "the compute unit's LDS");
 __device__ __forceinline__ int b_addr(int c, int chunk) {
   return (c ^ ((c >> 3) & 1)) * (2 * kBK) + 16 * (chunk ^ ((c ^ (c >> 4)) & 7));
@@ -79,11 +90,18 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
 
 // FM: 32-row blocks of a wave; the entry has at most 64 FM rows.  BEGINS: groups
 // begin at even k-tiles only (2: g is a multiple of 128, or there is one group), at any k-tile
-// (1: a multiple of 64), or also in the middle of one (0).
-template <int FM, bool GATED, bool BF16, int BEGINS>
+// (1: a multiple of 64), or also in the middle of one (0).  WHOLE: turns of whole k-tiles (K is
+// a multiple of 64 and BEGINS is not 0).
+template <int FM, bool GATED, bool BF16, int BEGINS, bool WHOLE>
 __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, int e, int first, int rows, int tile,
                                             const int32_t* __restrict__ sorted) {
+  static_assert(!WHOLE || BEGINS > 0, "a whole k-tile's turn has one place to change units");
   constexpr int kWaveRows = 32 * FM;
+  constexpr int kXBufs = WHOLE ? 4 : 3, kBBufs = WHOLE ? 3 : 2;
+  constexpr int kATile = (WHOLE ? 64 * FM : kRows) * kBK * 2;
+  constexpr int kBBase = kXBufs * kATile;
+  static_assert(kBBase + kBBufs * kBTile <= kLdsBytes, "LDS");
+  constexpr int kSteps = WHOLE ? 4 : 2;  // k16 steps of a turn
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -223,8 +241,8 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   }
 
-  // Operands of half a k-tile: two k16 steps.
-  half8v fa[2][FM], fb[2][kFN];
+  // Operands of a turn: half a k-tile or a whole one.
+  half8v fa[kSteps][FM], fb[kSteps][kFN];
   const int r0 = wm * kWaveRows + lc;
   const int a_read = r0 * (2 * kBK) + 16 * ((lane >> 5) ^ ((r0 >> 1) & 7));
   int b_read[kFN];
@@ -232,7 +250,7 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
   for (int j = 0; j < kFN; ++j) b_read[j] = kBBase + b_addr(tcol(j) + lc, lane >> 5);
   auto read = [&](int abuf, int bbuf, int hf) {
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
+    for (int st = 0; st < kSteps; ++st) {
       const int flip = 32 * (2 * hf + st);
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
@@ -262,7 +280,7 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio[j];
   };
-  // The 4 FM MFMAs of half a k-tile.  SCALE: the second column block's sums still await their
+  // The 2 FM MFMAs of each step.  SCALE: the second column block's sums still await their
   // factor; the first block's MFMAs go first.  STAGE: with the unpacking of the next k-tile, 8 LDS
   // writes and about 40 vector instructions (88 with the conversions to bfloat16).  The matrix
   // core works on one MFMA while the next share of vector instructions issues.
@@ -270,7 +288,7 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
     constexpr bool SCALE = decltype(scale)::value, STAGE = decltype(stages)::value;
     if constexpr (SCALE) rescale(1);
 #pragma unroll
-    for (int st = 0; st < 2; ++st)
+    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
 #pragma unroll
@@ -289,7 +307,7 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
       }
     }
     if constexpr (STAGE) {
-      constexpr int kLeft = SCALE ? kHalf : 2 * kHalf;
+      constexpr int kLeft = (SCALE ? kSteps - 1 : kSteps) * kHalf;
 #pragma unroll
       for (int i = 0; i < kLeft; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -330,62 +348,111 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
   }
   load_words(words[0], 2);
   load_a(1, 1);
+  if constexpr (WHOLE) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) stage(words[1], 1, t);
+    if (any_nil) stage_nil(1);
+    load_words(words[1], 3);
+    load_a(2, 2);
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (wave >= 4) turn();  // one turn behind
 
+  using yes = std::true_type;
+  using no = std::false_type;
+  using even = std::integral_constant<int, 0>;
+  using odd = std::integral_constant<int, 1>;
   int ab = 0;  // LDS buffer of this k-tile's x
-  auto body = [&](int kt, auto parity, uint32_t (&next)[4]) {
-    constexpr int buf = decltype(parity)::value;  // kt % 2
-    const int k0 = kt * kBK;
-    const bool full = k0 + 32 < K;  // the last k-tile may hold 32 rows
-    using yes = std::true_type;
-    using no = std::false_type;
-    read(ab, buf, 0);
-    constexpr bool kBegin = BEGINS < 2 || buf == 0;
-    if constexpr (kBegin) {
-      ratio[1] = 1.f;
-      if (k0 == boundary) {
-        change_units();
-        rescale(0);
-      }
-    }
-    turn();
-    multiply(std::integral_constant<bool, kBegin>{}, yes{}, next, buf ^ 1);
-    if (any_nil) stage_nil(buf ^ 1);
-    turn();
-    if (full) read(ab, buf, 1);
-    if constexpr (BEGINS == 0) {
-      ratio[1] = 1.f;
-      if (full && k0 + 32 == boundary) {
-        change_units();
-        rescale(0);
-      }
-    }
-    if (k0 + 2 * kBK + row_half >= pend) {  // the zeros of k-tile kt + 2, which is staged next
+  // The zeros of k-tile kt + 2, which is staged next.
+  auto next_zeros = [&](int k0) {
+    if (k0 + 2 * kBK + row_half >= pend) {
       enter_group();  // loaded when the last group began
       pg += stride;
       pend += stride * p.g;
       load_group(min(pg + stride, G - 1));
     }
-    // Behind this turn's waits for scales and zeros: they count back from the newest load the
-    // compiler knows, would take these in, and wait for memory (12288 slots of 1408 -> 2048,
-    // g32: 266 -> 219 us).
-    load_a(ab == 0 ? 2 : ab - 1, kt + 2);
-    // x of k-tile kt + 1 has landed: the words of kt + 2 and FM loads of kt + 2 are younger.
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FM + 4) : "memory");
-    turn();
-    if (full) multiply(std::integral_constant<bool, BEGINS == 0>{}, no{}, next, 0);
-    load_words(next, kt + 3);
-    turn();
-    ab = ab == 2 ? 0 : ab + 1;
   };
-  int kt = 0;
-  for (; kt + 1 < KT; kt += 2) {
-    body(kt, std::integral_constant<int, 0>{}, words[1]);
-    body(kt + 1, std::integral_constant<int, 1>{}, words[0]);
+  if constexpr (WHOLE) {
+    int bb = 0;  // and of its integers
+    auto body = [&](int kt, auto parity, uint32_t (&next)[4]) {
+      const int k0 = kt * kBK;
+      constexpr bool kBegin = BEGINS < 2 || decltype(parity)::value == 0;
+      read(ab, bb, 0);
+      if constexpr (kBegin) {
+        ratio[1] = 1.f;
+        if (k0 == boundary) {
+          change_units();
+          rescale(0);
+        }
+      }
+      next_zeros(k0);
+      load_a((ab + 3) & 3, kt + 3);
+      // x of k-tile kt + 1 has landed: 2 FM loads of kt + 2 and kt + 3 and the words of kt + 3
+      // are younger.  (Its buffer's last readers, of k-tile kt - 1, ended a turn ago at least, and
+      // so did those of the integers that kt + 2's replace below.)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * FM + 4) : "memory");
+      turn();
+      const int to = bb == 0 ? 2 : bb - 1;
+      multiply(std::integral_constant<bool, kBegin>{}, yes{}, next, to);
+      if (any_nil) stage_nil(to);
+      load_words(next, kt + 4);
+      turn();
+      ab = (ab + 1) & 3;
+      bb = bb == 2 ? 0 : bb + 1;
+    };
+    int kt = 0;
+    for (; kt + 1 < KT; kt += 2) {
+      body(kt, even{}, words[0]);
+      body(kt + 1, odd{}, words[1]);
+    }
+    if (kt < KT) body(kt, even{}, words[0]);
+  } else {
+    auto body = [&](int kt, auto parity, uint32_t (&next)[4]) {
+      constexpr int buf = decltype(parity)::value;  // kt % 2
+      const int k0 = kt * kBK;
+      const bool full = k0 + 32 < K;  // the last k-tile may hold 32 rows
+      read(ab, buf, 0);
+      constexpr bool kBegin = BEGINS < 2 || buf == 0;
+      if constexpr (kBegin) {
+        ratio[1] = 1.f;
+        if (k0 == boundary) {
+          change_units();
+          rescale(0);
+        }
+      }
+      turn();
+      multiply(std::integral_constant<bool, kBegin>{}, yes{}, next, buf ^ 1);
+      if (any_nil) stage_nil(buf ^ 1);
+      turn();
+      if (full) read(ab, buf, 1);
+      if constexpr (BEGINS == 0) {
+        ratio[1] = 1.f;
+        if (full && k0 + 32 == boundary) {
+          change_units();
+          rescale(0);
+        }
+      }
+      next_zeros(k0);
+      // Behind this turn's waits for scales and zeros: they count back from the newest load the
+      // compiler knows, would take these in, and wait for memory (12288 slots of 1408 -> 2048,
+      // g32: 266 -> 219 us).
+      load_a(ab == 0 ? 2 : ab - 1, kt + 2);
+      // x of k-tile kt + 1 has landed: the words of kt + 2 and FM loads of kt + 2 are younger.
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FM + 4) : "memory");
+      turn();
+      if (full) multiply(std::integral_constant<bool, BEGINS == 0>{}, no{}, next, 0);
+      load_words(next, kt + 3);
+      turn();
+      ab = ab == 2 ? 0 : ab + 1;
+    };
+    int kt = 0;
+    for (; kt + 1 < KT; kt += 2) {
+      body(kt, even{}, words[1]);
+      body(kt + 1, odd{}, words[0]);
+    }
+    if (kt < KT) body(kt, even{}, words[1]);
   }
-  if (kt < KT) body(kt, std::integral_constant<int, 0>{}, words[1]);
   if (wave < 4) turn();
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last k-tile have landed
   __syncthreads();
@@ -446,10 +513,16 @@ __global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(const ExpertPr
   const int first = table[4 * entry + 1];
   const int rows = table[4 * entry + 2];
   if (e < 0 || (rows > 128) == small) return;  // the whole workgroup, before any barrier
-  if (rows > 192) expert_tile<4, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
-  else if (rows > 128) expert_tile<3, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
-  else if (rows > 64) expert_tile<2, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
-  else expert_tile<1, GATED, BF16, BEGINS>(p, lds, e, first, rows, tile, sorted);
+  if (rows > 192) return expert_tile<4, GATED, BF16, BEGINS, false>(p, lds, e, first, rows, tile, sorted);
+  if (rows > 128) return expert_tile<3, GATED, BF16, BEGINS, false>(p, lds, e, first, rows, tile, sorted);
+  if constexpr (BEGINS > 0) {
+    if (p.K % kBK == 0) {
+      if (rows > 64) return expert_tile<2, GATED, BF16, BEGINS, true>(p, lds, e, first, rows, tile, sorted);
+      return expert_tile<1, GATED, BF16, BEGINS, true>(p, lds, e, first, rows, tile, sorted);
+    }
+  }
+  if (rows > 64) return expert_tile<2, GATED, BF16, BEGINS, false>(p, lds, e, first, rows, tile, sorted);
+  expert_tile<1, GATED, BF16, BEGINS, false>(p, lds, e, first, rows, tile, sorted);
 }
 
 hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertPlan& tp, const int32_t* sorted,
