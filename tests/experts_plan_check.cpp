@@ -105,6 +105,7 @@ void check(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t
     CHECK(p.sorted_bytes >= (up ? p.up.table_bytes : 0) && p.sorted_bytes >= (down ? p.down.table_bytes : 0));
     CHECK(p.sums_bytes >= (up ? p.up.sums_bytes : 0) && p.sums_bytes >= (down ? p.down.sums_bytes : 0));
     CHECK(p.h_bytes >= (up && down ? S * inner * 2 : 0) && p.h_bytes % 256 == 0);
+    if (p.two_terms) CHECK(S <= 64 && p.down.rows <= 16 && p.h_bytes % 512 == 0 && p.h_bytes >= 4 * S * inner);
     CHECK(p.workspace_bytes() == p.sorted_bytes + p.h_bytes + p.sums_bytes);
   }
 }

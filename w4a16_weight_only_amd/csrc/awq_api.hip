@@ -514,12 +514,15 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
     q.g = eff_group(K, group_size);
     q.gated = true;
     q.h = down ? h : static_cast<uint16_t*>(out);
+    if (p.two_terms) q.h_rest = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(h) + p.h_bytes / 2);
     e = product(*up, p.up);
     if (e == hipSuccess && p.up.splits > 1)
-      e = awq::launch_expert_gate(sums, ids, (int)S, (int)E, (int)inner, p.up.splits, q.bf16, q.h, stream);
+      e = awq::launch_expert_gate(sums, ids, (int)S, (int)E, (int)inner, p.up.splits, q.bf16, q.h, q.h_rest,
+                                  stream);
   }
   if (e == hipSuccess && down) {
     q.x = up ? h : static_cast<const uint16_t*>(x);
+    q.x_rest = q.h_rest;
     q.row_div = 1;
     q.K = (int)inner;
     q.N = (int)N;

@@ -59,6 +59,13 @@ __device__ __forceinline__ uint32_t pack_act2(float a, float b) {
   else return __builtin_bit_cast(uint32_t, half2v{(_Float16)a, (_Float16)b});
 }
 
+// What the rounding of f to an activation leaves out (nothing, of one that is not finite).
+template <bool BF16>
+__device__ __forceinline__ float rest_of(float f) {
+  const float r = act_to_float<BF16>(float_to_act<BF16>(f));
+  return fabsf(r) < __builtin_inff() ? f - r : 0.f;
+}
+
 // Column held by the low / high nibble of byte t (see the table above).
 __host__ __device__ constexpr int lo_col(int t) { return ((t & 1) << 2) | (t >> 1); }
 __host__ __device__ constexpr int hi_col(int t) { return lo_col(t) + 2; }

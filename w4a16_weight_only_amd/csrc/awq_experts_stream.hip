@@ -20,6 +20,9 @@
 // bfloat16 sums of 32 rows leave no registers for two sets of those: there the next group's are
 // asked for when a group begins (both ways: 64 tokens through 8 x 4096 -> 14336 209 -> 187 us in
 // bfloat16, which had spilled; one token through 64 x 2048 -> 1408 25.0 -> 27.0 in fp16).
+// A decoding step's h may be two terms, h rounded and what that left out (REST): a second MFMA
+// on the same operand, whose result's error is y's rounding alone (with one term 1.3 to 1.5 times
+// that).
 // The waves meet in LDS.  With one split a gated workgroup writes h; otherwise fp32 sums
 // [split][slot][column] leave for the next kernel, which adds the splits in order.
 //
@@ -42,24 +45,33 @@ constexpr int kYld = kExpertStreamCols + 4;  // floats of a staged output row
 // Entry v of a lane's 16 columns: word v / 8, byte (v / 2) % 4, nibble v % 2.
 __device__ constexpr int col_of(int v) { return (v & 1) ? hi_col((v >> 1) & 3) : lo_col((v >> 1) & 3); }
 
-template <int RB>
+template <int RB, bool REST>
 struct Step {
   u32x2 w[8];        // rows 8 q .. 8 q + 7
   half8v x[RB];      // x[row][8 q ..], a row of each block
+  half8v rest[REST ? RB : 1];
 };
 
 // The 16 RB MFMAs of a k-step.  zs: per column, fp16: -(1024 + z) or -(64 + z) twice (low or high
 // nibble); bfloat16: 128 twice, or zeros for a column without a scale.
-template <bool BF16, int RB>
-__device__ __forceinline__ void multiply(const Step<RB>& st, const uint32_t (&zs)[16], const UnpackConsts& uk,
+template <bool BF16, int RB, bool REST>
+__device__ __forceinline__ void multiply(const Step<RB, REST>& st, const uint32_t (&zs)[16], const UnpackConsts& uk,
                                          floatx4 (&part)[RB][16], floatx4 (&sx)[RB]) {
+  auto mfma = [](const half8v& x, const u32x4& w, const floatx4& c) {
+    if constexpr (BF16)
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0,
+                                                     0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, __builtin_bit_cast(half8v, w), c, 0, 0, 0);
+  };
   if constexpr (BF16) {
     const uint32_t one2 = 0x3F803F80u;  // bfloat16 pair (1, 1)
+    const u32x4 ones = {one2, one2, one2, one2};
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-      sx[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.x[rb]),
-                                                       __builtin_bit_cast(bf16x8, u32x4{one2, one2, one2, one2}),
-                                                       sx[rb], 0, 0, 0);
+    for (int rb = 0; rb < RB; ++rb) {
+      sx[rb] = mfma(st.x[rb], ones, sx[rb]);
+      if constexpr (REST) sx[rb] = mfma(st.rest[rb], ones, sx[rb]);
+    }
   }
 #pragma unroll
   for (int w = 0; w < 2; ++w)
@@ -80,14 +92,11 @@ __device__ __forceinline__ void multiply(const Step<RB>& st, const uint32_t (&zs
       }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        if constexpr (BF16) {
-          const bf16x8 x = __builtin_bit_cast(bf16x8, st.x[rb]);
-          part[rb][il] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, lo), part[rb][il], 0, 0, 0);
-          part[rb][ih] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, hi), part[rb][ih], 0, 0, 0);
-        } else {
-          const half8v x = st.x[rb];
-          part[rb][il] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, __builtin_bit_cast(half8v, lo), part[rb][il], 0, 0, 0);
-          part[rb][ih] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, __builtin_bit_cast(half8v, hi), part[rb][ih], 0, 0, 0);
+        part[rb][il] = mfma(st.x[rb], lo, part[rb][il]);
+        part[rb][ih] = mfma(st.x[rb], hi, part[rb][ih]);
+        if constexpr (REST) {
+          part[rb][il] = mfma(st.rest[rb], lo, part[rb][il]);
+          part[rb][ih] = mfma(st.rest[rb], hi, part[rb][ih]);
         }
       }
     }
@@ -140,8 +149,8 @@ __device__ __forceinline__ Entry rank_entry(const int32_t* ids, int S, int E, in
 }  // namespace
 
 // RB: blocks of 16 rows.  RL: lanes whose sums are kept, 16 per four rows (an entry of one block
-// never has more than RL / 4 rows).
-template <bool GATED, bool BF16, int RB, int RL>
+// never has more than RL / 4 rows).  REST: rows of two terms, x and x_rest.
+template <bool GATED, bool BF16, int RB, int RL, bool REST>
 __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const ExpertProduct p, int entries, int tiles,
                                                                     int splits, int steps,
                                                                     const int32_t* __restrict__ sorted,
@@ -216,15 +225,18 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   };
   // Loads of k-step ks.  Group data goes first: a wait for the weights counts back from the
   // newest load, and must not have to allow for loads that may not have been made.
-  auto issue = [&](Step<RB>& st, int slot, int ks) {
+  auto issue = [&](Step<RB, REST>& st, int slot, int ks) {
     if (!kOneSet && ks == load_at) fetch(data[kOneSet ? 0 : slot]);
     const uint32_t r0 = (uint32_t)ks * 32u;
 #pragma unroll
     for (int r = 0; r < 8; ++r)
       st.w[r] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wrs, w_off, (r0 + r) * row_bytes, 2));
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-      st.x[rb] = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(p.x) + (uint64_t)x_off[rb] + r0 * 2u);
+    for (int rb = 0; rb < RB; ++rb) {
+      const uint64_t at = (uint64_t)x_off[rb] + r0 * 2u;
+      st.x[rb] = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(p.x) + at);
+      if constexpr (REST) st.rest[rb] = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(p.x_rest) + at);
+    }
   };
 
   const UnpackConsts uk = unpack_consts();
@@ -284,7 +296,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
     enter_at = begin ? first_end : enter_at + gsteps;
     any_nil = __builtin_amdgcn_ballot_w64((nil[0] | nil[1]) != 0) != 0;
   };
-  Step<RB> ring[kPF];
+  Step<RB, REST> ring[kPF];
   if (kOneSet && kb < ke) fetch(data[0]);
 #pragma unroll
   for (int j = 0; j < kPF; ++j)
@@ -303,7 +315,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
 #pragma unroll
           for (int r = 0; r < 8; ++r) ring[j].w[r] = (ring[j].w[r] & ~nil) | (BF16 ? u32x2{0u, 0u} : zw & nil);
         }
-        multiply<BF16, RB>(ring[j], zs, uk, part, sx);
+        multiply<BF16>(ring[j], zs, uk, part, sx);
         if (kOneSet && begins && load_at < ke) fetch(data[0]);
         if (ks + kPF < ke) issue(ring[j], j, ks + kPF);
       }
@@ -363,9 +375,15 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
         const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
         if (n0 + cp < N) {
           const float* y = &sh.ys[row][0][cp];
-          *reinterpret_cast<u32x4*>(p.h + (int64_t)slots[16 * rb + row] * N + n0 + cp) =
-              u32x4{pack_act2<BF16>(y[0], y[1]), pack_act2<BF16>(y[2], y[3]), pack_act2<BF16>(y[4], y[5]),
-                    pack_act2<BF16>(y[6], y[7])};
+          const int64_t at = (int64_t)slots[16 * rb + row] * N + n0 + cp;
+          *reinterpret_cast<u32x4*>(p.h + at) = u32x4{pack_act2<BF16>(y[0], y[1]), pack_act2<BF16>(y[2], y[3]),
+                                                      pack_act2<BF16>(y[4], y[5]), pack_act2<BF16>(y[6], y[7])};
+          if (p.h_rest != nullptr) {
+            u32x4 rest;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rest[j] = pack_act2<BF16>(rest_of<BF16>(y[2 * j]), rest_of<BF16>(y[2 * j + 1]));
+            *reinterpret_cast<u32x4*>(p.h_rest + at) = rest;
+          }
         }
       }
     } else {
@@ -388,19 +406,22 @@ hipError_t launch_expert_stream(const ExpertProduct& p, const ExpertPlan& ep, co
     hipLaunchKernelGGL(kern, dim3((unsigned)ep.grid), dim3(kThreads), 0, stream, p, (int)ep.tiles, ep.col_tiles,
                        ep.splits, ep.steps, sorted, table);
   };
-#define AWQ_STREAM(GATED, BF16)                                            \
-  do {                                                                     \
-    if (ep.rows == 4) go(expert_stream_kernel<GATED, BF16, 1, 16>);        \
-    else if (ep.rows == 8) go(expert_stream_kernel<GATED, BF16, 1, 32>);   \
-    else if (ep.rows == 16) go(expert_stream_kernel<GATED, BF16, 1, 64>);  \
-    else go(expert_stream_kernel<GATED, BF16, 2, 64>);                     \
+#define AWQ_STREAM(GATED, BF16, REST)                                            \
+  do {                                                                           \
+    if (ep.rows == 4) go(expert_stream_kernel<GATED, BF16, 1, 16, REST>);        \
+    else if (ep.rows == 8) go(expert_stream_kernel<GATED, BF16, 1, 32, REST>);   \
+    else if (ep.rows == 16) go(expert_stream_kernel<GATED, BF16, 1, 64, REST>);  \
+    else go(expert_stream_kernel<GATED, BF16, 2, 64, false>);                    \
   } while (0)
   if (p.gated) {
-    if (p.bf16) AWQ_STREAM(true, true);
-    else AWQ_STREAM(true, false);
+    if (p.bf16) AWQ_STREAM(true, true, false);
+    else AWQ_STREAM(true, false, false);
+  } else if (p.x_rest != nullptr) {
+    if (p.bf16) AWQ_STREAM(false, true, true);
+    else AWQ_STREAM(false, false, true);
   } else {
-    if (p.bf16) AWQ_STREAM(false, true);
-    else AWQ_STREAM(false, false);
+    if (p.bf16) AWQ_STREAM(false, true, false);
+    else AWQ_STREAM(false, false, false);
   }
 #undef AWQ_STREAM
   return hipGetLastError();
@@ -410,7 +431,8 @@ hipError_t launch_expert_stream(const ExpertProduct& p, const ExpertPlan& ep, co
 template <bool BF16>
 __global__ __launch_bounds__(256) void expert_gate_kernel(const float* __restrict__ sums,
                                                           const int32_t* __restrict__ ids, int64_t quads, int S, int E,
-                                                          int N, int splits, uint16_t* __restrict__ h) {
+                                                          int N, int splits, uint16_t* __restrict__ h,
+                                                          uint16_t* __restrict__ h_rest) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= quads) return;
   const int64_t s = i / (N / 4);
@@ -420,16 +442,22 @@ __global__ __launch_bounds__(256) void expert_gate_kernel(const float* __restric
   const int64_t stride = (int64_t)S * 2 * N;
   const floatx4 g = sum_splits<8>(at, stride, splits), u = sum_splits<8>(at + N, stride, splits);
   if (e < 0 || e >= E) return;  // behind the loads, which need not wait for it
-  *reinterpret_cast<u32x2*>(h + s * N + n) = u32x2{pack_act2<BF16>(gated(g[0], u[0]), gated(g[1], u[1])),
-                                                  pack_act2<BF16>(gated(g[2], u[2]), gated(g[3], u[3]))};
+  float v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = gated(g[j], u[j]);
+  *reinterpret_cast<u32x2*>(h + s * N + n) = u32x2{pack_act2<BF16>(v[0], v[1]), pack_act2<BF16>(v[2], v[3])};
+  if (h_rest != nullptr)
+    *reinterpret_cast<u32x2*>(h_rest + s * N + n) =
+        u32x2{pack_act2<BF16>(rest_of<BF16>(v[0]), rest_of<BF16>(v[1])),
+              pack_act2<BF16>(rest_of<BF16>(v[2]), rest_of<BF16>(v[3]))};
 }
 
 hipError_t launch_expert_gate(const float* sums, const int32_t* ids, int S, int E, int N, int splits, bool bf16,
-                              uint16_t* h, hipStream_t stream) {
+                              uint16_t* h, uint16_t* h_rest, hipStream_t stream) {
   const int64_t quads = (int64_t)S * (N / 4);
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, sums, ids, quads, S, E, N,
-                       splits, h);
+                       splits, h, h_rest);
   };
   if (bf16) go(expert_gate_kernel<true>);
   else go(expert_gate_kernel<false>);

@@ -113,6 +113,8 @@ struct ExpertProduct {
   bool gated, bf16;
   uint16_t* h;
   float* sums;
+  const uint16_t* x_rest;  // or NULL: what x's rounding left out, a second term of the rows
+  uint16_t* h_rest;        // or NULL: takes what h's rounding leaves out
 };
 // Row tiles over slots sorted by expert (table and sorted as launch_moe_align gives them).
 hipError_t launch_expert_tiles(const ExpertProduct& p, const ExpertPlan& tp, const int32_t* sorted,
@@ -124,7 +126,7 @@ hipError_t launch_expert_stream(const ExpertProduct& p, const ExpertPlan& ep, co
                                 const int32_t* table, hipStream_t stream);
 // h[s] = silu(gate) * up of the splits' sums [splits][S][2 N], for slots with an id in [0, E).
 hipError_t launch_expert_gate(const float* sums, const int32_t* ids, int S, int E, int N, int splits, bool bf16,
-                              uint16_t* h, hipStream_t stream);
+                              uint16_t* h, uint16_t* h_rest, hipStream_t stream);
 // y[t, n] = sum over j of weights[t, j] * the splits' sum of sums[split][t topk + j, n], in a
 // fixed order, over the slots with an id in [0, E); rounded once to the activation type.
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,

@@ -566,6 +566,8 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
     if (st != AWQ_OK) return st;
     if (p.down.table_bytes > p.sorted_bytes) p.sorted_bytes = p.down.table_bytes;
     if (p.down.sums_bytes > p.sums_bytes) p.sums_bytes = p.down.sums_bytes;
+    p.two_terms = up && p.up.ranked && p.down.ranked && p.down.rows <= 16;
+    if (p.two_terms) p.h_bytes *= 2;
   }
   return AWQ_OK;
 }

@@ -216,6 +216,11 @@ constexpr int64_t kExpertRankSlots = 64;  // slots a wave can rank, one per lane
 // and the fp32 sums (the first product's are dead when the second's are written).
 struct ExpertsPlan {
   ExpertPlan up, down;
+  // h as two terms, rounded and what that leaves out: a decoding step's few slots, whose h's
+  // rounding no number of tokens averages out.  (To 64 slots.  One term / two, us: mlp of one
+  // token 64 x 2048 -> 1408 25.0 / 25.4, 8 x 4096 -> 14336 51.4 / 52.5, 16 tokens 153.4 / 157.8;
+  // 128 slots 77.5 / 80.0, 80 of the second 183.7 / 192.4.)
+  bool two_terms = false;
   int64_t sorted_bytes = 0, h_bytes = 0, sums_bytes = 0;
   int64_t workspace_bytes() const { return sorted_bytes + h_bytes + sums_bytes; }
 };

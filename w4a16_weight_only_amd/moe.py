@@ -208,7 +208,9 @@ def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.
                 group_size: int = 128, out: torch.Tensor | None = None) -> torch.Tensor:
     """The gated MLP of routed experts in one call: x [T, K], gate_up and down packed weights
     (qweight, qzeros, scales) of K -> 2 I and I -> N columns, expert_ids int32 and weights fp32
-    [T, topk] -> y [T, N] in x's type.  The same values as awq_moe_down of awq_moe_gate_up."""
+    [T, topk] -> y [T, N] in x's type.  The same values as awq_moe_down of awq_moe_gate_up, but
+    for a decoding step's few slots (up to 64, of which at most 8 or fewer than 12 per expert),
+    where h is not rounded on the way."""
     _check_act("x", x)
     dev = x.device
     T, K = x.shape
