@@ -53,6 +53,7 @@ void check_product(const ExpertPlan& p, int64_t S, int64_t E, int64_t K, int64_t
     CHECK(p.rows >= (S < p.block_rows ? S : p.block_rows));
     CHECK((int64_t)p.col_tiles * 256 >= N && (int64_t)(p.col_tiles - 1) * 256 < N);
     CHECK(p.grid == p.tiles * p.col_tiles * p.splits);
+    if (p.by_xcd) CHECK(p.tiles % 8 == 0);
     const int64_t run = (int64_t)p.steps * (gated ? 2 : 4), T = K / 32;
     CHECK(p.steps >= 1 && p.splits >= 1 && p.splits <= kExpertMaxSplits);
     CHECK(run * p.splits >= T && run * (p.splits - 1) < T);

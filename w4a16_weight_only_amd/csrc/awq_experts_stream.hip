@@ -151,7 +151,7 @@ __device__ __forceinline__ Entry rank_entry(const int32_t* ids, int S, int E, in
 // RB: blocks of 16 rows.  RL: lanes whose sums are kept, 16 per four rows (an entry of one block
 // never has more than RL / 4 rows).  REST: rows of two terms, x and x_rest.
 template <bool GATED, bool BF16, int RB, int RL, bool REST>
-__global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const ExpertProduct p, int entries, int tiles,
+__global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const ExpertProduct p, int by_xcd, int tiles,
                                                                     int splits, int steps,
                                                                     const int32_t* __restrict__ sorted,
                                                                     const int32_t* __restrict__ table) {
@@ -162,11 +162,15 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   } sh;
   __shared__ int32_t slots[16 * RB];
 
-  // Block order: splits fastest, then column tiles, then entries.
-  const int split = blockIdx.x % splits;
-  const int b = blockIdx.x / splits;
-  const int tile = b % tiles;
-  const int entry = b / tiles;
+  // Block order: splits fastest, then column tiles, then entries; by_xcd: eight entries
+  // abreast, so that an entry's blocks share an XCD.
+  const int of_entry = tiles * splits;
+  const int group = by_xcd ? blockIdx.x / (8 * of_entry) : 0;
+  const int in_group = blockIdx.x - group * 8 * of_entry;
+  const int at_entry = by_xcd ? in_group >> 3 : in_group % of_entry;
+  const int entry = by_xcd ? 8 * group + (in_group & 7) : in_group / of_entry;
+  const int split = at_entry % splits;
+  const int tile = at_entry / splits;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -403,7 +407,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
 hipError_t launch_expert_stream(const ExpertProduct& p, const ExpertPlan& ep, const int32_t* sorted,
                                 const int32_t* table, hipStream_t stream) {
   auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)ep.grid), dim3(kThreads), 0, stream, p, (int)ep.tiles, ep.col_tiles,
+    hipLaunchKernelGGL(kern, dim3((unsigned)ep.grid), dim3(kThreads), 0, stream, p, (int)ep.by_xcd, ep.col_tiles,
                        ep.splits, ep.steps, sorted, table);
   };
 #define AWQ_STREAM(GATED, BF16, REST)                                            \

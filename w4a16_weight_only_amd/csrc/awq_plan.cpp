@@ -515,6 +515,8 @@ int plan_expert(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int cu
     p.block_rows = p.rows == 32 ? 32 : 16;
     p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
     p.tiles = p.ranked ? entry_bound(S, E, p.block_rows) : moe_tiles(S, E, p.block_rows);
+    p.by_xcd = p.tiles >= kExpertXcdEntries;
+    if (p.by_xcd) p.tiles = round_up(p.tiles, 8);
     choose_splits(T, topk, E, K, wide, cus, gated, p);
     p.grid = p.tiles * p.col_tiles * p.splits;
     p.sums_bytes = gated && p.splits == 1 ? 0 : round_up(p.splits * S * wide * 4, 256);

@@ -193,6 +193,7 @@ struct ExpertPlan {
   int64_t tiles = 0;        // entries the grid covers
   int col_tiles = 0;
   int splits = 1, steps = 0;
+  bool by_xcd = false;      // stream: an entry's workgroups share an XCD (tiles % 8 == 0)
   int64_t grid = 0;         // workgroups
   int64_t table_bytes = 0;  // table, offsets and sorted slots
   int64_t sums_bytes = 0;   // fp32 sums of all splits
@@ -209,6 +210,13 @@ constexpr int64_t kExpertStreamRows = 80;
 // 16, 32 slots per expert 87 / 92, 101 / 98, 128 / 115, 186 / 150; 8 x 4096 -> 14336, 8, 12, 16:
 // 159 / 192, 199 / 202, 237 / 209.
 constexpr int64_t kExpertWideRows = 12;
+// Entries from which a streaming grid keeps each on one XCD: rows of a weight that are no whole
+// 128-byte lines (64 x 2048 -> 1408: the up projection's half starts inside one) make neighbouring
+// column tiles share lines, which two L2s would each fetch (gate_up of 45 tokens read 1.5 times
+// its bytes).  Spread over all XCDs / one each, us: gate_up of 45 tokens 66 / 61, mlp of 4, 16, 64,
+// 256 tokens 48.7 / 46, 78 / 73.5, 101 / 94, 149.7 / 149.  Fewer entries leave XCDs idle: from 8
+// entries on, 24 tokens of 20 experts 45 / 52.7, 5 of 8 x 4096 -> 14336 114 / 157.
+constexpr int64_t kExpertXcdEntries = 32;
 constexpr int64_t kExpertMaxSplits = 32;
 constexpr int64_t kExpertRankSlots = 64;  // slots a wave can rank, one per lane
 // The gated MLP of routed experts and its two halves: which products it makes, and the
