@@ -202,10 +202,10 @@ constexpr int kExpertTileRows = 256;
 constexpr int kExpertTileCols = 256;    // weight columns of a workgroup
 constexpr int kExpertStreamCols = 256;  // columns of a workgroup (gated: of each half)
 // Most slots per expert, on average, to stream.  Measured, us per call, streamed / tiles: mlp
-// 64 x 2048 -> 1408, 32, 64, 96, 128 slots per expert 150 / 197, 222 / 251, 307 / 290, 380 / 313;
-// 8 x 4096 -> 14336, 64, 96, 128: 527 / 650, 640 / 703, 806 / 764; one expert 4096 -> 4096 (64
-// and 32 tiles' workgroups), 512 rows 119 / 252.
-constexpr int64_t kExpertStreamRows = 80;
+// 64 x 2048 -> 1408, 48, 64, 80 slots per expert 188 / 189, 222 / 228, 266 / 263 (bfloat16, 64:
+// 231 / 249); 8 x 4096 -> 14336, 48, 64, 80: 353 / 417, 456 / 475, 493 / 468; one expert 4096 ->
+// 4096 (64 and 32 tiles' workgroups), 512 rows 119 / 252.
+constexpr int64_t kExpertStreamRows = 72;
 // Slots per expert from which entries take 32 rows: 16 / 32 rows, mlp 64 x 2048 -> 1408, 4, 8,
 // 16, 32 slots per expert 87 / 92, 101 / 98, 128 / 115, 186 / 150; 8 x 4096 -> 14336, 8, 12, 16:
 // 159 / 192, 199 / 202, 237 / 209.
