@@ -34,7 +34,7 @@
 // it the launch, the first k-tiles and the epilogue.  Groups of 32 take 175: the rescaling, 128
 // vector multiplications per 16 MFMAs of a wave, no longer hides.  A tile of 64, 128, 192 rows
 // takes 0.60, 0.70, 0.83 of a tile of 256: unpacking and staging the weights is the same for all,
-// so experts' last, short entries cost 13 to 36% of a prompt's products.
+// so experts' last, short entries add 24 to 36% to a prompt's products.
 #include <type_traits>
 
 #include "awq_device.h"
