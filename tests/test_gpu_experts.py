@@ -383,6 +383,26 @@ def test_unrouted_and_repeated_slots(T, dtype):
     close(y[:T], *down_ref(h, down, ids, w, dtype), "down")
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("T,E,topk", [(1, 4, 3), (7, 2, 5), (40, 4, 3), (64, 1, 1)])
+def test_mlp_of_unrouted_and_repeated_slots(T, E, topk, dtype):
+    """The whole MLP: zeros for a token without a routed slot, whatever its weights hold and the
+    workspace held; more slots per token than experts; every slot unrouted."""
+    K, inner, N, g = 64, 96, 64, 32
+    up, down = Layer(E, K, 2 * inner, g, 43), Layer(E, inner, N, g, 44)
+    x = activations((T, K), dtype, 45)
+    ids, w = routing(T, E, topk, 46)
+    ids[T - 1] = E
+    w[T - 1] = float("nan")
+    junk = torch.full((1 << 22,), float("nan"), device="cuda")  # what the allocator hands out next
+    del junk
+    steps = awq.awq_moe_down(awq.awq_moe_gate_up(x, *up.dev, ids, g), *down.dev, ids, w, g)
+    y = check_mlp(x, up, down, ids, w, g, steps, dtype)
+    assert (y[T - 1] == 0).all()
+    ids.fill_(-1)
+    assert (awq.awq_moe_mlp(x, up.dev, down.dev, ids, w, g) == 0).all()
+
+
 @pytest.mark.parametrize("T", [2, 20, 200])
 def test_all_slots_on_one_expert(T):
     E, K, inner, N, g = 6, 512, 160, 96, 32
