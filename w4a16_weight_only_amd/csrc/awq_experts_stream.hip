@@ -7,15 +7,12 @@
 // lanes: 128 contiguous bytes of a row) and unpacks them into operands of exact integers, 16
 // columns x 8 rows; its rows of x are rows l % 16 (and 16 + l % 16: an operand unpacked once
 // serves both blocks of 16 rows) of the entry.
-//   fp16       operand q - z
-//   bfloat16   (no packed bfloat16 addition on this chip) operand 128 + q, and one more MFMA
-//              against ones for the rows' sums of x:  x . (128 + q) - (128 + z) x . 1
+// q - z; in bfloat16, which has no packed addition on this chip, by way of fp32.
 // The running sums are in units of the current group's scale u: a group boundary multiplies
 // them by u / u' (a second set of 64 accumulator registers, scaled group by group, spills).
 // A scale of zero cannot be a unit: the unit stays, and the column's operands become zeros, by
-// its codes replaced with its zero code (fp16), or cleared together with its 128 (bfloat16: a
-// difference of rounded sums would not be zero).  That is rare, and outside the MFMAs' code: a
-// second copy of those makes the compiler move accumulators about.
+// its codes replaced with its zero code.  That is rare, and outside the MFMAs' code: a second copy
+// of those makes the compiler move accumulators about.
 // A ring of two k-steps is in flight, and with each a group's zeros and scales where one begins.
 // bfloat16 sums of 32 rows leave no registers for two sets of those: there the next group's are
 // asked for when a group begins (both ways: 64 tokens through 8 x 4096 -> 14336 209 -> 187 us in
@@ -57,11 +54,22 @@ struct Step {
   half8v rest[REST ? RB : 1];
 };
 
+// Codes to (code - zero) in bfloat16, exact, by way of fp32: the nibbles in bits 0-3 (or 4-7) of a
+// word's halves are the subnormal halves q 2^-24 (or q 2^-20), so that one mixed-precision fma
+// makes q - z of each; two rows' are then narrowed together.  2.1 vector instructions a weight,
+// where fp16's 1024 + q takes 1.25 with packed additions.  (A bfloat16 128 + q takes 1.0, but leaves
+// x . (128 + q) - (128 + z) x . 1 to be formed: partial sums with four to five bits fewer, and NaN
+// where an infinite x gives an infinity.  That / this, us: gate_up of 45 tokens 64 x 2048 -> 1408
+// 61 / 67, mlp of 16 tokens 8 x 4096 -> 14336 158 / 168, of 256 tokens 64 x 2048 -> 1408 170 / 171.)
+__device__ __forceinline__ uint32_t minus_zero_bf16(uint32_t a, uint32_t b, int half, float scale, float neg) {
+  return pack_bf16x2(fmaf((float)as_h2(a)[half], scale, neg), fmaf((float)as_h2(b)[half], scale, neg));
+}
+
 // The 16 RB MFMAs of a k-step.  zs: per column, fp16: -(1024 + z) or -(64 + z) twice (low or high
-// nibble); bfloat16: 128 twice, or zeros for a column without a scale.
+// nibble); bfloat16: -z as a float.
 template <bool BF16, int RB, bool REST>
 __device__ __forceinline__ void multiply(const Step<RB, REST>& st, const uint32_t (&zs)[16], const UnpackConsts& uk,
-                                         floatx4 (&part)[RB][16], floatx4 (&sx)[RB]) {
+                                         floatx4 (&part)[RB][16]) {
   auto mfma = [](const half8v& x, const u32x4& w, const floatx4& c) {
     if constexpr (BF16)
       return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0,
@@ -69,42 +77,54 @@ __device__ __forceinline__ void multiply(const Step<RB, REST>& st, const uint32_
     else
       return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, __builtin_bit_cast(half8v, w), c, 0, 0, 0);
   };
-  if constexpr (BF16) {
-    const uint32_t one2 = 0x3F803F80u;  // bfloat16 pair (1, 1)
-    const u32x4 ones = {one2, one2, one2, one2};
+  auto column = [&](int v, const u32x4& op) {
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-      sx[rb] = mfma(st.x[rb], ones, sx[rb]);
-      if constexpr (REST) sx[rb] = mfma(st.rest[rb], ones, sx[rb]);
+      part[rb][v] = mfma(st.x[rb], op, part[rb][v]);
+      if constexpr (REST) part[rb][v] = mfma(st.rest[rb], op, part[rb][v]);
+    }
+  };
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if constexpr (BF16) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {  // nibbles 2 s, 2 s + 1 and, in the upper half, 2 s + 4, 2 s + 5
+        u32x4 op[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t a = st.w[2 * p][w] >> (8 * s), b = st.w[2 * p + 1][w] >> (8 * s);
+          const uint32_t al = a & 0x000F000Fu, bl = b & 0x000F000Fu, ah = a & 0x00F000F0u, bh = b & 0x00F000F0u;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int v = 8 * w + 2 * s + 4 * half;
+            op[2 * half][p] = minus_zero_bf16(al, bl, half, 0x1p24f, __builtin_bit_cast(float, zs[v]));
+            op[2 * half + 1][p] = minus_zero_bf16(ah, bh, half, 0x1p20f, __builtin_bit_cast(float, zs[v + 1]));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) column(8 * w + 2 * s + 4 * (i >> 1) + (i & 1), op[i]);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        u32x4 lo, hi;
+        const int il = 8 * w + 2 * t, ih = il + 1;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t wa = st.w[2 * p][w], wb = st.w[2 * p + 1][w];
+          uint32_t pb;
+          if (t == 0) pb = pair_byte<0>(wa, wb);
+          else if (t == 1) pb = pair_byte<1>(wa, wb);
+          else if (t == 2) pb = pair_byte<2>(wa, wb);
+          else pb = pair_byte<3>(wa, wb);
+          lo[p] = as_u32(lo_minus_zero(pb, as_h2(zs[il]), uk));
+          hi[p] = as_u32(hi_minus_zero(pb, as_h2(zs[ih]), uk));
+        }
+        column(il, lo);
+        column(ih, hi);
+      }
     }
   }
-#pragma unroll
-  for (int w = 0; w < 2; ++w)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      u32x4 lo, hi;
-      const int il = 8 * w + 2 * t, ih = il + 1;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t wa = st.w[2 * p][w], wb = st.w[2 * p + 1][w];
-        uint32_t pb;
-        if (t == 0) pb = pair_byte<0>(wa, wb);
-        else if (t == 1) pb = pair_byte<1>(wa, wb);
-        else if (t == 2) pb = pair_byte<2>(wa, wb);
-        else pb = pair_byte<3>(wa, wb);
-        lo[p] = BF16 ? (pb & uk.mlo) | zs[il] : as_u32(lo_minus_zero(pb, as_h2(zs[il]), uk));
-        hi[p] = BF16 ? ((pb >> 4) & uk.mlo) | zs[ih] : as_u32(hi_minus_zero(pb, as_h2(zs[ih]), uk));
-      }
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        part[rb][il] = mfma(st.x[rb], lo, part[rb][il]);
-        part[rb][ih] = mfma(st.x[rb], hi, part[rb][ih]);
-        if constexpr (REST) {
-          part[rb][il] = mfma(st.rest[rb], lo, part[rb][il]);
-          part[rb][ih] = mfma(st.rest[rb], hi, part[rb][ih]);
-        }
-      }
-    }
 }
 
 // Zeros and scales of a group, for a lane's two words.
@@ -221,6 +241,11 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
 
   // Group data: one set for each k-step in flight, or one in all.
   constexpr bool kOneSet = BF16 && RB == 2;
+  // Loads of steps past a run's end are made as well, which lets a step's loads stay in flight
+  // during the one before (without / with: mlp of 256 tokens 64 x 2048 -> 1408, g 64, bfloat16 181 /
+  // 171 us, of 128 tokens 8 x 4096 -> 14336 304 / 283; one block of rows 86 / 88 us for 16 tokens of
+  // the first and fp16's two blocks 152 / 159 for 256: there the loads of short runs cost more).
+  constexpr bool kAlways = BF16 && RB == 2;
   GroupData data[kOneSet ? 1 : kPF];
   // The group loaded next and entered next, and the k-steps they begin with.
   int load_group = kb / gsteps, load_at = kb, enter_at = kb;
@@ -232,14 +257,18 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
     d.s[1] = *reinterpret_cast<const half8v*>(scales + 8 * at + 8);
     load_at = ++load_group * gsteps;
   };
-  // Loads of k-step ks.  Group data goes first: a wait for the weights counts back from the
-  // newest load, and must not have to allow for loads that may not have been made.
+  // Loads of a k-step.  Group data goes first: a wait for the weights counts back from the newest
+  // load, and must not have to allow for loads that may not have been made.  kAlways: for the same
+  // reason the loads of steps past the run are made too; the weights' offset is the buffer's end
+  // there, past which nothing is read, and x is read at k = 0 again.
   auto issue = [&](Step<RB, REST>& st, int slot, int ks) {
-    if (!kOneSet && ks == load_at) fetch(data[kOneSet ? 0 : slot]);
-    const uint32_t r0 = (uint32_t)ks * 32u;
+    const bool live = !kAlways || ks < ke;
+    if (!kOneSet && live && ks == load_at) fetch(data[kOneSet ? 0 : slot]);
+    const uint32_t r0 = live ? (uint32_t)ks * 32u : 0u;
+    const uint32_t at_w = live ? w_off : row_bytes * (uint32_t)K, row_step = live ? row_bytes : 0u;
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-      st.w[r] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wrs, w_off, (r0 + r) * row_bytes, 2));
+      st.w[r] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wrs, at_w, (r0 + r) * row_step, 2));
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       const uint64_t at = (uint64_t)x_off[rb] + r0 * 2u;
@@ -249,7 +278,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   };
 
   const UnpackConsts uk = unpack_consts();
-  floatx4 part[RB][16], sx[RB];
+  floatx4 part[RB][16];
   uint32_t zs[16];
   half8v unit[2];          // the columns' current units
   u32x2 zw = {0u, 0u};     // the current group's zero codes
@@ -262,21 +291,6 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
     zs[v] = 0;
     unit[v >> 3][v & 7] = (_Float16)1.f;
   }
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) sx[rb] = floatx4{0.f, 0.f, 0.f, 0.f};
-  // A group ends: bfloat16 sums lose their zeros' share.
-  auto leave = [&] {
-    if constexpr (BF16) {
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const float z = zs[v] == 0u ? 0.f : 128.0f + (float)zero_code(zw[v >> 3], col_of(v));
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) part[rb][v] -= z * sx[rb];
-      }
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) sx[rb] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-  };
   // A group begins: the sums so far change units (there are none when the run begins).
   auto enter = [&](const GroupData& d, bool begin) {
     nil = u32x2{0u, 0u};
@@ -293,10 +307,10 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
       }
       unit[v >> 3][v & 7] = now;
       nil[v >> 3] |= none ? 0xFu << (4 * (v & 7)) : 0u;  // entry v is nibble v % 8 of its word
+      const uint32_t z = zero_code(d.z[v >> 3], col_of(v));
       if constexpr (BF16) {
-        zs[v] = none ? 0u : uk.bmagic;
+        zs[v] = __builtin_bit_cast(uint32_t, -(float)z);
       } else {
-        const uint32_t z = zero_code(d.z[v >> 3], col_of(v));
         const uint32_t h = (v & 1) ? (0xD400u | (z << 4)) : (0xE400u | z);  // -(64 + z), -(1024 + z)
         zs[v] = h | (h << 16);
       }
@@ -308,29 +322,28 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   Step<RB, REST> ring[kPF];
   if (kOneSet && kb < ke) fetch(data[0]);
 #pragma unroll
-  for (int j = 0; j < kPF; ++j)
-    if (kb + j < ke) issue(ring[j], j, kb + j);
+  for (int j = 0; j < kPF; ++j) {
+    if (kAlways || kb + j < ke) issue(ring[j], j, kb + j);
+    if constexpr (kAlways) __builtin_amdgcn_sched_barrier(0);
+  }
   for (int base = kb; base < ke; base += kPF) {
 #pragma unroll
     for (int j = 0; j < kPF; ++j) {
       const int ks = base + j;
-      if (ks < ke) {
+      if ((kAlways && j == 0) || ks < ke) {
         const bool begins = ks == enter_at;
-        if (begins) {
-          if (ks != kb) leave();
-          enter(data[kOneSet ? 0 : j], ks == kb);
-        }
+        if (begins) enter(data[kOneSet ? 0 : j], ks == kb);
         if (any_nil) {
 #pragma unroll
-          for (int r = 0; r < 8; ++r) ring[j].w[r] = (ring[j].w[r] & ~nil) | (BF16 ? u32x2{0u, 0u} : zw & nil);
+          for (int r = 0; r < 8; ++r) ring[j].w[r] = (ring[j].w[r] & ~nil) | (zw & nil);
         }
-        multiply<BF16>(ring[j], zs, uk, part, sx);
+        multiply<BF16>(ring[j], zs, uk, part);
         if (kOneSet && begins && load_at < ke) fetch(data[0]);
-        if (ks + kPF < ke) issue(ring[j], j, ks + kPF);
+        if (!kAlways && ks + kPF < ke) issue(ring[j], j, ks + kPF);
       }
+      if (kAlways) issue(ring[j], j, ks + kPF);
     }
   }
-  if (kb < ke) leave();
 
   // Per block of 16 rows: waves -> LDS, then one thread per (column entry, lane of rows) sums
   // four rows of one column, and the rows leave in order.
