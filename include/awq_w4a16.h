@@ -55,6 +55,10 @@ enum awq_status {
 /* Element types of the entry points that take one (16-bit types as raw storage). */
 enum awq_type { AWQ_F16 = 0, AWQ_BF16 = 1, AWQ_F32 = 2 };
 
+/* Added to act of awq_moe_down and awq_moe_mlp: a NaN weight makes its token's y NaN also where
+ * the slot's id is not routed, as awq_moe_route leaves a row that has no scores. */
+enum { AWQ_NAN_WEIGHTS = 256 };
+
 /* Scores of awq_moe_route. */
 enum awq_score { AWQ_SOFTMAX = 0, AWQ_SIGMOID = 1 };
 
@@ -303,13 +307,15 @@ int awq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int
  *                     slots (with more than 8, fewer than 12 per expert) also what that
  *                     rounding leaves out, so that y is rounded once
  * with silu(v) = v / (1 + exp(-v)).
- *   act            AWQ_F16 or AWQ_BF16: the type of x, h and y (scales stay fp16)
+ *   act            AWQ_F16 or AWQ_BF16: the type of x, h and y (scales stay fp16); for down and
+ *                  mlp plus AWQ_NAN_WEIGHTS, if wanted
  *   x              device [T, K];  h device [T * topk, inner];  y device [T, N]
  *   gate_up weight qweight int32 [E, K, 2 inner / 8], qzeros [E, G, 2 inner / 8], scales fp16
  *                  [E, G, 2 inner]: the gate's columns first, then the up projection's
  *   down weight    qweight int32 [E, K, N / 8] and so on; K = inner for awq_moe_mlp
  *   expert_ids     device int32 [T * topk]; ids outside [0, E) are not routed: their h rows are
- *                  left as they are, and they add nothing to y (a token without any gets zeros)
+ *                  left as they are, and they add nothing to y (a token without any gets zeros),
+ *                  whatever their weight, unless act asks for AWQ_NAN_WEIGHTS
  *   weights        device fp32 [T, topk]
  *   workspace      device memory of at least awq_moe_workspace bytes, 16-byte aligned, for this
  *                  call alone until its work on the stream is done.  It needs no contents and

@@ -198,3 +198,13 @@ def test_synth_routing_inputs():
     """The generator's layers: as many distinct experts per token as asked for."""
     d = synth.make_moe_custom(6, 5, 3, 64, 32, 32, seed=3)
     assert all(len(set(r)) == 3 for r in d["expert_ids"].reshape(6, 3).tolist())
+
+
+def test_nan_weights_flag():
+    """A flag of act, for the products that have weights; nothing else is one."""
+    keep = _lib.AWQ_NAN_WEIGHTS
+    for act in (_lib.AWQ_F16, _lib.AWQ_BF16):
+        assert down(act=act | keep, h=None) == NULL and mlp(act=act | keep, x=None) == NULL
+        assert gate_up(act=act | keep) == UNSUP
+        assert down(act=act | 2 * keep) == UNSUP and mlp(act=act | keep | 2) == UNSUP
+    assert down(act=_lib.AWQ_F32 | keep) == UNSUP and down(act=-1) == UNSUP

@@ -54,3 +54,54 @@ def test_infinities_keep_their_sign(counts, N, dtype):
         np.testing.assert_array_equal(h[t], ref)
     keep = np.setdiff1d(np.arange(T), [0, 1, T - 1])
     assert torch.equal(y[keep], clean[keep])
+
+
+@DTYPES
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+def test_layer_module_keeps_nan(T, dtype):
+    """A token without scores (a NaN in x, router products that overflow to infinity) comes out as
+    NaN; every other token's bits are those of a clean call, a token without experts' zeros too."""
+    E, topk, K, inner, g = 16, 4, 256, 128, 64
+    up, down = Layer(E, K, 2 * inner, g, 21), Layer(E, inner, K, g, 22)
+    router = activations((E, K), dtype, 23) / 16
+    layer = awq.AwqMoe(router, up.dev, down.dev, topk, g)
+    x = activations((T, K), dtype, 24)
+    clean = layer(x)
+    assert torch.isfinite(clean).all()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        y = x.clone()
+        y[T // 2, 3] = bad
+        got = layer(y)
+        keep = torch.arange(T) != T // 2
+        assert torch.equal(got[keep], clean[keep])
+        assert torch.isnan(got[T // 2]).all()
+    none = awq.AwqMoe(router, up.dev, down.dev, topk, g, bias=torch.full((E,), -float("inf"), device="cuda"))
+    assert (none(x) == 0).all()
+    far = torch.finfo(dtype).max
+    big = torch.full((T, K), 0.0, dtype=dtype, device="cuda")
+    big[T // 2] = far  # finite: it is the logits that are not
+    router[:, 0] = far
+    assert torch.isnan(layer(big)[T // 2]).all()
+
+
+@DTYPES
+@pytest.mark.parametrize("T,topk", [(1, 2), (3, 5), (40, 3), (300, 2)])
+def test_nan_weights_on_request(T, topk, dtype):
+    """nan_weights: a token with a NaN weight is NaN also where that slot is not routed; nothing
+    else changes, an infinite weight of an unrouted slot adds nothing."""
+    E, K, inner, N, g = 4, 64, 96, 64, 32
+    up, down = Layer(E, K, 2 * inner, g, 25), Layer(E, inner, N, g, 26)
+    x, h = activations((T, K), dtype, 27), activations((T * topk, inner), dtype, 28)
+    rng = np.random.default_rng(29)
+    ids = torch.from_numpy(rng.integers(-1, E + 1, (T, topk)).astype(np.int32)).cuda()
+    w = torch.from_numpy(rng.uniform(0.1, 1, (T, topk)).astype(np.float32)).cuda()
+    off = (ids < 0) | (ids >= E)
+    w[off] = float("inf")
+    calls = [lambda **kw: awq.awq_moe_down(h, *down.dev, ids, w, g, **kw),
+             lambda **kw: awq.awq_moe_mlp(x, up.dev, down.dev, ids, w, g, **kw)]
+    for call in calls:
+        assert torch.equal(call(nan_weights=True), call())
+    ids[0, topk - 1], w[0, topk - 1] = E, float("nan")
+    for call in calls:
+        plain, kept = call(), call(nan_weights=True)
+        assert torch.isfinite(plain).all() and torch.isnan(kept[0]).all() and torch.equal(kept[1:], plain[1:])

@@ -20,6 +20,7 @@ AWQ_ERR_UNSUPPORTED = -5
 AWQ_ERR_HIP = -6
 
 AWQ_F16, AWQ_BF16, AWQ_F32 = 0, 1, 2  # enum awq_type
+AWQ_NAN_WEIGHTS = 256
 AWQ_SOFTMAX, AWQ_SIGMOID = 0, 1  # enum awq_score
 
 # Every function include/awq_w4a16.h declares, with its ctypes signature.

@@ -466,6 +466,8 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
   ExpertsPlan p;
   int st = plan_experts(T, topk, E, K, inner, N, group_size, query_cus(), up != nullptr, down != nullptr, p);
   if (st != AWQ_OK) return st;
+  const bool nan_weights = down && (act & AWQ_NAN_WEIGHTS) != 0;
+  if (nan_weights) act -= AWQ_NAN_WEIGHTS;
   if (act != AWQ_F16 && act != AWQ_BF16) return AWQ_ERR_UNSUPPORTED;
   if (T == 0) return AWQ_OK;
   if (!x || !ids || !out || !workspace || (down && !weights)) return AWQ_ERR_NULL;
@@ -531,7 +533,7 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
     e = product(*down, p.down);
     if (e == hipSuccess)
       e = awq::launch_expert_combine(sums, ids, weights, (int)T, (int)topk, (int)E, (int)N, p.down.splits, q.bf16,
-                                     static_cast<uint16_t*>(out), stream);
+                                     nan_weights, static_cast<uint16_t*>(out), stream);
   }
   return e == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
 }

@@ -564,7 +564,7 @@ template <bool BF16, int PARTS>
 __global__ __launch_bounds__(256) void expert_combine_kernel(const float* __restrict__ sums,
                                                              const int32_t* __restrict__ ids,
                                                              const float* __restrict__ weights, int64_t quads, int S,
-                                                             int topk, int E, int N, int splits,
+                                                             int topk, int E, int N, int splits, int nan_weights,
                                                              uint16_t* __restrict__ y) {
   __shared__ floatx4 meet[PARTS > 1 ? 256 : 1];
   const int part = threadIdx.x % PARTS;
@@ -588,8 +588,10 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const float* __rest
       v[u] = *reinterpret_cast<const floatx4*>(sums + ((int64_t)(i - j * splits) * S + s) * N + n);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u) {
       if (i0 + u * PARTS < terms && e[u] >= 0 && e[u] < E) a += w[u] * v[u];
+      else if (nan_weights && w[u] != w[u]) a += w[u];  // (a term read twice is the token's own)
+    }
   }
   if constexpr (PARTS > 1) {
     meet[threadIdx.x] = a;
@@ -608,12 +610,12 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const float* __rest
 constexpr int64_t kFewQuads = 32768;
 
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
-                                 int N, int splits, bool bf16, uint16_t* y, hipStream_t stream) {
+                                 int N, int splits, bool bf16, bool nan_weights, uint16_t* y, hipStream_t stream) {
   const int64_t quads = (int64_t)T * (N / 4);
   auto go = [&](auto kern, int parts) {
     const int64_t per = 256 / parts;
     hipLaunchKernelGGL(kern, dim3((unsigned)((quads + per - 1) / per)), dim3(256), 0, stream, sums, ids, weights,
-                       quads, T * topk, topk, E, N, splits, y);
+                       quads, T * topk, topk, E, N, splits, (int)nan_weights, y);
   };
   const bool few = quads <= kFewQuads && topk * splits > 2;
   if (bf16) {

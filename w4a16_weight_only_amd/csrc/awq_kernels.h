@@ -129,7 +129,8 @@ hipError_t launch_expert_gate(const float* sums, const int32_t* ids, int S, int 
                               uint16_t* h, uint16_t* h_rest, hipStream_t stream);
 // y[t, n] = sum over j of weights[t, j] * the splits' sum of sums[split][t topk + j, n], in a
 // fixed order, over the slots with an id in [0, E); rounded once to the activation type.
+// nan_weights: also NaN where another slot's weight is.
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
-                                 int N, int splits, bool bf16, uint16_t* y, hipStream_t stream);
+                                 int N, int splits, bool bf16, bool nan_weights, uint16_t* y, hipStream_t stream);
 
 }  // namespace awq

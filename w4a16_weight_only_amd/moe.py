@@ -88,6 +88,10 @@ def _output(out, shape, dtype, device):
     return out
 
 
+def _act(t, nan_weights):
+    return _TYPES[t.dtype] | (_lib.AWQ_NAN_WEIGHTS if nan_weights else 0)
+
+
 def _call(fn, name, device, *args):
     """fn(*args, stream) with the tensors' device current; the stream is that device's current one."""
     index = device.index
@@ -184,10 +188,11 @@ def awq_moe_gate_up(x: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor
 
 def awq_moe_down(h: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor, scales: torch.Tensor,
                  expert_ids: torch.Tensor, weights: torch.Tensor, group_size: int = 128,
-                 out: torch.Tensor | None = None) -> torch.Tensor:
+                 out: torch.Tensor | None = None, nan_weights: bool = False) -> torch.Tensor:
     """Second half: h [T * topk, K], expert_ids int32 and weights fp32 [T, topk] ->
     y [T, N] = sum over j of weights[t, j] * (h[t topk + j] . W[expert_ids[t, j]]) in h's
-    type.  Ids outside [0, E) add nothing."""
+    type.  Ids outside [0, E) add nothing, whatever their weight; with nan_weights a NaN weight
+    makes its token NaN there too, as awq_moe_route leaves a row that has no scores."""
     _check_act("h", h)
     dev = h.device
     S, K = h.shape
@@ -198,19 +203,19 @@ def awq_moe_down(h: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor, s
     _check_weights(weights, expert_ids.shape, dev)
     out = _output(out, (T, N), h.dtype, dev)
     ws, nbytes = _workspace(dev, T, topk, E, 0, K, N, group_size)
-    _call(_lib.load().awq_moe_down, "awq_moe_down", dev, h.data_ptr(), _TYPES[h.dtype], qweight.data_ptr(),
+    _call(_lib.load().awq_moe_down, "awq_moe_down", dev, h.data_ptr(), _act(h, nan_weights), qweight.data_ptr(),
           qzeros.data_ptr(), scales.data_ptr(), expert_ids.data_ptr(), weights.data_ptr(), T, topk, E, K, N,
           group_size, out.data_ptr(), ws.data_ptr(), nbytes)
     return out
 
 
 def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.Tensor, weights: torch.Tensor,
-                group_size: int = 128, out: torch.Tensor | None = None) -> torch.Tensor:
+                group_size: int = 128, out: torch.Tensor | None = None, nan_weights: bool = False) -> torch.Tensor:
     """The gated MLP of routed experts in one call: x [T, K], gate_up and down packed weights
     (qweight, qzeros, scales) of K -> 2 I and I -> N columns, expert_ids int32 and weights fp32
     [T, topk] -> y [T, N] in x's type.  The same values as awq_moe_down of awq_moe_gate_up, but
     for a decoding step's few slots (up to 64, of which at most 8 or fewer than 12 per expert),
-    where h is not rounded on the way."""
+    where h is not rounded on the way.  nan_weights as for awq_moe_down."""
     _check_act("x", x)
     dev = x.device
     T, K = x.shape
@@ -225,7 +230,7 @@ def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.
     _check_weights(weights, expert_ids.shape, dev)
     out = _output(out, (T, N), x.dtype, dev)
     ws, nbytes = _workspace(dev, T, topk, E, K, inner, N, group_size)
-    _call(_lib.load().awq_moe_mlp, "awq_moe_mlp", dev, x.data_ptr(), _TYPES[x.dtype],
+    _call(_lib.load().awq_moe_mlp, "awq_moe_mlp", dev, x.data_ptr(), _act(x, nan_weights),
           *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down], expert_ids.data_ptr(), weights.data_ptr(),
           T, topk, E, K, inner, N, group_size, out.data_ptr(), ws.data_ptr(), nbytes)
     return out
@@ -233,7 +238,8 @@ def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.
 
 class AwqMoe(torch.nn.Module):
     """Inference-only routed-expert layer: a dense router [E, K] in the activations' type and
-    the experts' packed gate_up and down weights.  Routing arguments are awq_moe_route's."""
+    the experts' packed gate_up and down weights.  Routing arguments are awq_moe_route's.  A token
+    whose logits hold a NaN (for the softmax, or +inf) comes out as NaN."""
 
     def __init__(self, router, gate_up, down, topk, group_size=128, bias=None, **routing):
         super().__init__()
@@ -251,5 +257,6 @@ class AwqMoe(torch.nn.Module):
         logits = torch.nn.functional.linear(rows, self.router)
         weights, ids = awq_moe_route(logits, self.topk, bias=self.bias, **self.routing)
         y = awq_moe_mlp(rows, (self.gate_up_qweight, self.gate_up_qzeros, self.gate_up_scales),
-                        (self.down_qweight, self.down_qzeros, self.down_scales), ids, weights, self.group_size)
+                        (self.down_qweight, self.down_qzeros, self.down_scales), ids, weights, self.group_size,
+                        nan_weights=True)
         return y.reshape(x.shape[:-1] + (y.shape[-1],))
