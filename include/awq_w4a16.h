@@ -285,8 +285,9 @@ int awq_moe_gemm(const void* x_f16, const int32_t* qweight, const int32_t* qzero
  *   scale        factor of the weights
  *   weights      device fp32 [T, topk]: s of the chosen experts (divided, scaled)
  *   expert_ids   device int32 [T, topk]
- * Equal s + bias (equal group worths) go to the lowest index; the comparison is that of the
- * exact values: without a bias of the logits themselves, otherwise of sums in fp64.  An
+ * Equal s + bias (equal group worths) go to the lowest index.  Without a bias experts are
+ * compared by their logits themselves, and so are groups worth their largest score; sums with a
+ * bias, and sums of two scores, are formed and compared in fp64.  An
  * expert whose logit (or s + bias) is -inf is never chosen; slots left without an expert
  * get id -1, which the products below do not route, and weight 0.  A row that holds a NaN,
  * or for the softmax +inf, gets ids -1 and NaN weights.

@@ -383,14 +383,15 @@ def route_ref(logits, topk: int, score: str = "softmax", bias=None, groups: int 
             else:
                 s = 1.0 / (1.0 + np.exp(-l))
         # Without a bias the order of the scores is that of the logits, also where scores of
-        # different logits round to the same float64.
-        choice = l if bias is None and (groups == 1 or group_top == 1) else s + (0.0 if bias is None else bias)
+        # different logits round to the same float64; sums of two are formed of the scores.
+        choice = l if bias is None else s + bias
+        value = choice if group_top == 1 or bias is not None else s
         ranked = [e for e in sorted(range(E), key=lambda e: (-choice[e], e)) if open_[e] and not np.isneginf(choice[e])]
         worth = {}
         for g in range(groups):
             mine = [e for e in ranked if e // per == g]
             if mine:
-                worth[g] = sum(choice[e] for e in mine[:group_top])
+                worth[g] = sum(value[e] for e in mine[:group_top])
         kept = sorted(worth, key=lambda g: (-worth[g], g))[:topk_groups]
         chosen = [e for e in ranked if e // per in kept][:topk]
         if not chosen:

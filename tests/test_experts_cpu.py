@@ -208,3 +208,13 @@ def test_nan_weights_flag():
         assert gate_up(act=act | keep) == UNSUP
         assert down(act=act | 2 * keep) == UNSUP and mlp(act=act | keep | 2) == UNSUP
     assert down(act=_lib.AWQ_F32 | keep) == UNSUP and down(act=-1) == UNSUP
+
+
+@pytest.mark.parametrize("score,l", [("sigmoid", [[40.0, 50.0, 0.0, 0.0]]), ("softmax", [[-900.0, -800.0, 0.0, -950.0]])])
+def test_route_ref_chooses_by_the_logits_without_a_bias(score, l):
+    """Scores that round to the same number (1.0, or 0.0) still have their logits' order, also where
+    groups are worth sums of two."""
+    l = np.array(l)
+    for top in (1, 2):
+        ids = oracle.route_ref(l, 2, score=score, groups=2, topk_groups=2, group_top=top)[1]
+        assert ids.tolist() == ([[1, 0]] if score == "sigmoid" else [[2, 1]])

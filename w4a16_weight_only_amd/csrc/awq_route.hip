@@ -9,11 +9,11 @@
 //           -1 where nothing is left to choose
 //   weight  s of the chosen (without the bias), divided by their sum on request, times scale
 //
-// Order.  Without a bias and with groups worth their best expert, every comparison is one
-// of scores, and s rises strictly with l: the logits themselves are the keys, exact in
-// fp32, and two experts tie exactly when their logits do.  A bias or a sum of two scores
-// has to be added up, and in fp32 the sum's rounding (2^-25 of a score near 1) would swap
-// experts that close together: those keys are formed in fp64.
+// Order.  Without a bias the comparison of experts is one of scores, and s rises strictly with l:
+// the logits themselves are the keys, exact in fp32, and two experts tie exactly when their
+// logits do.  A bias has to be added up, and in fp32 the sum's rounding (2^-25 of a score near 1)
+// would swap experts that close together: those keys are formed in fp64.  So are the sums of two
+// scores that groups may be worth, whose experts then still go by their logits without a bias.
 // Weights.  Renormalised scores are quotients, so a common factor is taken out first:
 // exp(l - max over the chosen) instead of the softmax, and exp(min(l, 0) - min(max, 0)) /
 // (1 + exp(-|l|)) for the sigmoid, so that scores too small for fp32 still divide.
@@ -122,16 +122,17 @@ struct Two {
 
 }  // namespace
 
-// Key: float (keys are the logits) or double (keys are choices).  GROUPS: expert groups.
-// TYPE of the logits: 0 fp16, 1 bfloat16, 2 fp32.
-template <typename Key, int LPT, int VPL, bool GROUPS, int TYPE>
+// Key: float (keys are the logits) or double (keys are choices).  Worth, of groups: float (their
+// best logit) or double (choices).  GROUPS: expert groups.  TYPE of the logits: 0 fp16, 1
+// bfloat16, 2 fp32.
+template <typename Key, typename Worth, int LPT, int VPL, bool GROUPS, int TYPE>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a) {
   constexpr int TOKENS = kRouteThreads / LPT;  // tokens per workgroup (one wave)
-  constexpr bool kChoice = sizeof(Key) == 8;
+  constexpr bool kChoice = sizeof(Key) == 8, kScores = sizeof(Worth) == 8;
   constexpr int kOut = 64 / LPT;  // experts a lane stores, LPT apart
   constexpr float kInf = __builtin_inff();
-  __shared__ Key keys_lds[GROUPS ? TOKENS * LPT * VPL : 1];
-  __shared__ Key worth[GROUPS ? TOKENS : 1][kRouteMaxGroups];
+  __shared__ Worth keys_lds[GROUPS ? TOKENS * LPT * VPL : 1];
+  __shared__ Worth worth[GROUPS ? TOKENS : 1][kRouteMaxGroups];
   __shared__ int chosen[TOKENS][kRouteMaxTopk];
   const Key kNone = -(Key)kInf;
   const int lane = threadIdx.x;
@@ -187,7 +188,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
   top = lanes_max<LPT>(top);
 
   Key key[VPL];
-  if constexpr (kChoice) {
+  Worth val[VPL];  // what groups are worth the largest of
+  if constexpr (kScores) {
     double z = 0.0, s[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -200,11 +202,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
     for (int i = 0; i < VPL; ++i) {
       const int e = p * VPL + i;
       const double c = s[i] * z + (a.bias != nullptr && e < a.E ? (double)a.bias[e] : 0.0);
-      key[i] = l[i] == -kInf || c != c ? kNone : c;
+      val[i] = l[i] == -kInf || c != c ? -(Worth)kInf : c;
     }
-  } else {
+  }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = lost ? kNone : l[i];
+  for (int i = 0; i < VPL; ++i) {
+    if constexpr (kChoice) key[i] = val[i];
+    else key[i] = lost ? kNone : l[i];
+    if constexpr (!kScores) val[i] = key[i];
   }
 
   if constexpr (GROUPS) {
@@ -213,14 +218,17 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
     const int per = a.E / a.groups;
     const int width = per / VPL;  // lanes of a group
     const bool whole = per % VPL == 0 && width <= 16 && (width & (width - 1)) == 0;
-    auto value = [&](const Two<Key>& b) { return a.group_top == 2 && b.second != kNone ? b.first + b.second : b.first; };
+    const Worth kNothing = -(Worth)kInf;
+    auto value = [&](const Two<Worth>& b) {
+      return a.group_top == 2 && b.second != kNothing ? b.first + b.second : b.first;
+    };
     if (whole) {
-      Two<Key> b{kNone, kNone};
+      Two<Worth> b{kNothing, kNothing};
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) b.add(key[i]);
+      for (int i = 0; i < VPL; ++i) b.add(val[i]);
       auto meet = [&](auto ctrl) {
         constexpr int C = decltype(ctrl)::value;
-        b.add(Two<Key>{rotated<C>(b.first), rotated<C>(b.second)});
+        b.add(Two<Worth>{rotated<C>(b.first), rotated<C>(b.second)});
       };
       if (width >= 2) meet(std::integral_constant<int, 0xB1>{});   // lane ^ 1
       if (width >= 4) meet(std::integral_constant<int, 0x4E>{});   // lane ^ 2
@@ -228,12 +236,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
       if (width >= 16) meet(std::integral_constant<int, 0x140>{});  // mirrored in 16: the other eight
       if (p % width == 0 && p / width < a.groups) worth[slot][p / width] = value(b);
     } else {
-      Key* mine = keys_lds + slot * LPT * VPL;
+      Worth* mine = keys_lds + slot * LPT * VPL;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) mine[p * VPL + i] = key[i];
+      for (int i = 0; i < VPL; ++i) mine[p * VPL + i] = val[i];
       __syncthreads();
       for (int g = p; g < a.groups; g += LPT) {
-        Two<Key> b{kNone, kNone};
+        Two<Worth> b{kNothing, kNothing};
 #pragma unroll 8
         for (int i = 0; i < per; ++i) b.add(mine[g * per + i]);
         worth[slot][g] = value(b);
@@ -244,10 +252,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
 #pragma unroll
     for (int r = 0; r < kOut; ++r) {
       const int g = r * LPT + p;
-      const Key mine = worth[slot][g < a.groups ? g : 0];
+      const Worth mine = worth[slot][g < a.groups ? g : 0];
       int better = 0;
       for (int o = 0; o < a.groups; ++o) {
-        const Key k = worth[slot][o];
+        const Worth k = worth[slot][o];
         better += k > mine || (k == mine && o < g) ? 1 : 0;
       }
       keep |= vote(g < a.groups && better < a.topk_groups) << (r * LPT);
@@ -328,8 +336,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
 }
 
 hipError_t launch_route(RouteArgs a, hipStream_t stream) {
-  // Keys need fp64 where scores are added to something (see the top of the file).
-  const bool choice = a.bias != nullptr || (a.groups > 1 && a.group_top == 2);
+  // Keys and worths need fp64 where scores are added to something (see the top of the file).
+  const bool choice = a.bias != nullptr, scores = choice || (a.groups > 1 && a.group_top == 2);
   auto go = [&](auto kern, int lpt, int vpl) {
     const int64_t tokens = kRouteThreads / lpt;
     // Wide loads: rows and lanes start on whole pieces, and E ends on one.
@@ -339,15 +347,16 @@ hipError_t launch_route(RouteArgs a, hipStream_t stream) {
              (a.T == 1 || a.row_stride * size % piece == 0);
     hipLaunchKernelGGL(kern, dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kRouteThreads), 0, stream, a);
   };
-  auto typed = [&](auto key, auto groups, auto lpt, auto vpl) {
+  auto typed = [&](auto key, auto worth_of, auto groups, auto lpt, auto vpl) {
     using Key = decltype(key);
+    using Worth = decltype(worth_of);
     constexpr bool G = decltype(groups)::value;
     constexpr int L = decltype(lpt)::value, V = decltype(vpl)::value;
-    if (a.type == 2) go(route_kernel<Key, L, V, G, 2>, L, V);
-    else if (a.type == 1) go(route_kernel<Key, L, V, G, 1>, L, V);
-    else go(route_kernel<Key, L, V, G, 0>, L, V);
+    if (a.type == 2) go(route_kernel<Key, Worth, L, V, G, 2>, L, V);
+    else if (a.type == 1) go(route_kernel<Key, Worth, L, V, G, 1>, L, V);
+    else go(route_kernel<Key, Worth, L, V, G, 0>, L, V);
   };
-  auto sized = [&](auto key, auto groups) {
+  auto sized = [&](auto key, auto worth, auto groups) {
     using I4 = std::integral_constant<int, 4>;
     using I8 = std::integral_constant<int, 8>;
     using I16 = std::integral_constant<int, 16>;
@@ -358,22 +367,25 @@ hipError_t launch_route(RouteArgs a, hipStream_t stream) {
     // instructions.  Measured, us, a wave each / four a wave: 512 tokens of 128 experts 4.5 / 5.2,
     // 4096 6.4 / 5.5, 16384 14.6 / 7.5 (a third of a copy's rate); 16 fp64 keys a lane do not
     // pay: 512 tokens of 256 experts in 8 groups 7.4 / 15.6, 16384 32.4 / 36.5.
-    if (a.T <= kRouteFewTokens || (sizeof(key) == 8 && a.E > 128)) {
-      if (a.E <= 64) typed(key, groups, I64{}, I1{});
-      else if (a.E <= 128) typed(key, groups, I64{}, I2{});
-      else if (a.E <= 256) typed(key, groups, I64{}, I4{});
-      else if (a.E <= 512) typed(key, groups, I64{}, I8{});
-      else typed(key, groups, I64{}, I16{});
+    if (a.T <= kRouteFewTokens || (sizeof(worth) == 8 && a.E > 128)) {
+      if (a.E <= 64) typed(key, worth, groups, I64{}, I1{});
+      else if (a.E <= 128) typed(key, worth, groups, I64{}, I2{});
+      else if (a.E <= 256) typed(key, worth, groups, I64{}, I4{});
+      else if (a.E <= 512) typed(key, worth, groups, I64{}, I8{});
+      else typed(key, worth, groups, I64{}, I16{});
     } else {
-      if (a.E <= 64) typed(key, groups, I16{}, I4{});
-      else if (a.E <= 128) typed(key, groups, I16{}, I8{});
-      else if (a.E <= 256) typed(key, groups, I16{}, I16{});
-      else if (a.E <= 512) typed(key, groups, I64{}, I8{});
-      else typed(key, groups, I64{}, I16{});
+      if (a.E <= 64) typed(key, worth, groups, I16{}, I4{});
+      else if (a.E <= 128) typed(key, worth, groups, I16{}, I8{});
+      else if (a.E <= 256) typed(key, worth, groups, I16{}, I16{});
+      else if (a.E <= 512) typed(key, worth, groups, I64{}, I8{});
+      else typed(key, worth, groups, I64{}, I16{});
     }
   };
-  if (choice) a.groups > 1 ? sized(double{}, std::true_type{}) : sized(double{}, std::false_type{});
-  else a.groups > 1 ? sized(float{}, std::true_type{}) : sized(float{}, std::false_type{});
+  using yes = std::true_type;
+  using no = std::false_type;
+  if (choice) a.groups > 1 ? sized(double{}, double{}, yes{}) : sized(double{}, double{}, no{});
+  else if (scores) sized(float{}, double{}, yes{});
+  else a.groups > 1 ? sized(float{}, float{}, yes{}) : sized(float{}, float{}, no{});
   return hipGetLastError();
 }
 
