@@ -105,3 +105,24 @@ def test_nan_weights_on_request(T, topk, dtype):
     for call in calls:
         plain, kept = call(), call(nan_weights=True)
         assert torch.isfinite(plain).all() and torch.isnan(kept[0]).all() and torch.equal(kept[1:], plain[1:])
+
+
+@DTYPES
+@pytest.mark.parametrize("T", [1, 33])
+def test_layer_module_of_a_32_bit_router(T, dtype):
+    """A router in fp32 gives fp32 logits: experts that 16-bit logits would tie keep their order."""
+    E, topk, K, inner, g = 16, 2, 256, 128, 64
+    up, down = Layer(E, K, 2 * inner, g, 31), Layer(E, inner, K, g, 32)
+    router = torch.zeros(E, K, device="cuda")
+    router[:, 0] = 1.0 + 2.0 ** -14 * torch.arange(E, device="cuda")  # one value in 16 bits
+    x = activations((T, K), dtype, 33)
+    x[:, 0] = 1.0
+    y = awq.AwqMoe(router, up.dev, down.dev, topk, g)(x)
+    assert y.dtype == dtype
+    w, ids = awq.awq_moe_route(router[:, 0].repeat(T, 1), topk)
+    assert ids.cpu().tolist() == [[E - 1, E - 2]] * T
+    assert torch.equal(y, awq.awq_moe_mlp(x, up.dev, down.dev, ids, w, g))
+    with pytest.raises(TypeError):
+        awq.AwqMoe(router.double(), up.dev, down.dev, topk, g)(x)
+    with pytest.raises(TypeError):
+        awq.AwqMoe(router.to(torch.float16 if dtype is torch.bfloat16 else torch.bfloat16), up.dev, down.dev, topk, g)(x)

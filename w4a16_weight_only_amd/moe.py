@@ -237,8 +237,9 @@ def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.
 
 
 class AwqMoe(torch.nn.Module):
-    """Inference-only routed-expert layer: a dense router [E, K] in the activations' type and
-    the experts' packed gate_up and down weights.  Routing arguments are awq_moe_route's.  A token
+    """Inference-only routed-expert layer: a dense router [E, K] and the experts' packed gate_up and
+    down weights.  A router in the activations' type gives logits rounded to it; one in fp32 gives
+    fp32 logits, which do not tie experts that are a 16-bit rounding apart.  Routing arguments are awq_moe_route's.  A token
     whose logits hold a NaN (for the softmax, or +inf) comes out as NaN."""
 
     def __init__(self, router, gate_up, down, topk, group_size=128, bias=None, **routing):
@@ -254,7 +255,9 @@ class AwqMoe(torch.nn.Module):
 
     def forward(self, x):
         rows = x.reshape(-1, x.shape[-1]).contiguous()
-        logits = torch.nn.functional.linear(rows, self.router)
+        if self.router.dtype is not rows.dtype and self.router.dtype is not torch.float32:
+            raise TypeError(f"router must be {rows.dtype} or float32, got {self.router.dtype}")
+        logits = torch.nn.functional.linear(rows.to(self.router.dtype), self.router)
         weights, ids = awq_moe_route(logits, self.topk, bias=self.bias, **self.routing)
         y = awq_moe_mlp(rows, (self.gate_up_qweight, self.gate_up_qzeros, self.gate_up_scales),
                         (self.down_qweight, self.down_qzeros, self.down_scales), ids, weights, self.group_size,
