@@ -126,3 +126,27 @@ def test_layer_module_of_a_32_bit_router(T, dtype):
         awq.AwqMoe(router.double(), up.dev, down.dev, topk, g)(x)
     with pytest.raises(TypeError):
         awq.AwqMoe(router.to(torch.float16 if dtype is torch.bfloat16 else torch.bfloat16), up.dev, down.dev, topk, g)(x)
+
+
+@DTYPES
+@pytest.mark.parametrize("counts,K,N", [((1,), 4096, 512), ((5, 3), 4096, 512), ((30, 34), 2048, 320),
+                                        ((100, 140), 4096, 512), ((300, 190, 100, 230), 1024, 8736)],
+                         ids=["1", "8", "64", "240", "tiles"])
+def test_equal_scales_in_all_groups_change_nothing(counts, K, N, dtype):
+    """Groups of 32 that all have a column's one scale and zero are one group of K: sums of whole
+    numbers below 2^24 are exact, and stay so at every boundary, so both give the same bits."""
+    E, T = len(counts), sum(counts)
+    assert 3 * 15 * K < 2 ** 24
+    print(f"equal scales counts={counts} K={K} N={N} {dtype}", flush=True)
+    ids, w = routed_by_counts(counts, 12)
+    w.fill_(1.0)
+    x = torch.from_numpy(np.random.default_rng(13).integers(-3, 4, (T, K)).astype(np.float64)).to(dtype).cuda()
+
+    def same(layer):
+        layer.qz[:], layer.sc[:] = layer.qz[:, :1], layer.sc[:, :1]
+
+    many = Layer(E, K, N, 32, 14, same)
+    one = (many.dev[0], many.dev[1][:, :1].contiguous(), many.dev[2][:, :1].contiguous())
+    assert torch.equal(awq.awq_moe_down(x, *many.dev, ids, w, 32), awq.awq_moe_down(x, *one, ids, w, -1))
+    assert torch.equal(awq.awq_moe_gate_up(x, *(t.contiguous() for t in many.dev), ids, 32),
+                       awq.awq_moe_gate_up(x, *one, ids, -1))

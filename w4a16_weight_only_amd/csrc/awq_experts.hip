@@ -5,7 +5,7 @@
 // integers (q - z) (exact in fp16 and bfloat16) and the scales stay outside, in fp32:
 //   sum_k x_k (q - z) s_g(k)  =  u * acc,   acc in units of the current group's scale u;
 // at a group boundary acc *= u / u', u = u' (one multiplication per sum and group, no second
-// set of accumulators and no rounding of weights).  A scale of zero cannot be a unit: the
+// set of accumulators and no rounding of weights; exactly 1 where the scale stays the same).  A scale of zero cannot be a unit: the
 // unit stays and that group's (q - z) of the column are staged as zeros.
 //
 // Workgroup: 8 waves as 2 (rows) x 4 (columns), 256 weight columns (gated: 128 of each half,
@@ -271,7 +271,7 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
     for (int j = 0; j < kFN; ++j) {
       const float s = act_to_float<false>(s_next[j]);
       const float u = s == 0.f ? unit[j] : s;
-      ratio[j] = unit[j] * __builtin_amdgcn_rcpf(u);
+      ratio[j] = u == unit[j] ? 1.f : unit[j] * __builtin_amdgcn_rcpf(u);
       unit[j] = u;
     }
     load_scales(++group);

@@ -9,7 +9,9 @@
 // serves both blocks of 16 rows) of the entry.
 // q - z; in bfloat16, which has no packed addition on this chip, by way of fp32.
 // The running sums are in units of the current group's scale u: a group boundary multiplies
-// them by u / u' (a second set of 64 accumulator registers, scaled group by group, spills).
+// them by u / u', exactly 1 where the scale stays the same (u times its reciprocal may be a step
+// off, always to one side, which equal groups would add up).  (A second set of 64 accumulator
+// registers, scaled group by group, spills.)
 // A scale of zero cannot be a unit: the unit stays, and the column's operands become zeros, by
 // its codes replaced with its zero code.  That is rare, and outside the MFMAs' code: a second copy
 // of those makes the compiler move accumulators about.
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
       const bool none = s == (_Float16)0.f;
       const _Float16 now = none ? old : s;
       if (!begin) {
-        const float ratio = (float)old * __builtin_amdgcn_rcpf((float)now);
+        const float ratio = now == old ? 1.f : (float)old * __builtin_amdgcn_rcpf((float)now);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) part[rb][v] *= ratio;
       }
