@@ -130,7 +130,7 @@ def test_layer_module_of_a_32_bit_router(T, dtype):
 
 @DTYPES
 @pytest.mark.parametrize("counts,K,N", [((1,), 4096, 512), ((5, 3), 4096, 512), ((30, 34), 2048, 320),
-                                        ((100, 140), 4096, 512), ((300, 190, 100, 230), 1024, 8736)],
+                                        ((100, 140), 4096, 512), ((300, 190, 100, 230), 1024, 8768)],
                          ids=["1", "8", "64", "240", "tiles"])
 def test_equal_scales_in_all_groups_change_nothing(counts, K, N, dtype):
     """Groups of 32 that all have a column's one scale and zero are one group of K: sums of whole
