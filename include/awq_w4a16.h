@@ -310,7 +310,8 @@ int awq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int
  * with silu(v) = v / (1 + exp(-v)).
  *   act            AWQ_F16 or AWQ_BF16: the type of x, h and y (scales stay fp16); for down and
  *                  mlp plus AWQ_NAN_WEIGHTS, if wanted
- *   x              device [T, K];  h device [T * topk, inner];  y device [T, N]
+ *   x              device [T, K];  h device [T * topk, inner];  y device [T, N].  The h of
+ *                  awq_moe_gate_up may not overlap x (AWQ_ERR_UNSUPPORTED); y may
  *   gate_up weight qweight int32 [E, K, 2 inner / 8], qzeros [E, G, 2 inner / 8], scales fp16
  *                  [E, G, 2 inner]: the gate's columns first, then the up projection's
  *   down weight    qweight int32 [E, K, N / 8] and so on; K = inner for awq_moe_mlp

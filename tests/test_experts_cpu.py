@@ -218,3 +218,11 @@ def test_route_ref_chooses_by_the_logits_without_a_bias(score, l):
     for top in (1, 2):
         ids = oracle.route_ref(l, 2, score=score, groups=2, topk_groups=2, group_top=top)[1]
         assert ids.tolist() == ([[1, 0]] if score == "sigmoid" else [[2, 1]])
+
+
+def test_gate_up_refuses_an_h_that_overlaps_x():
+    """h is written while other workgroups still read x.  Refused before any launch."""
+    x = 1 << 20
+    size_x, size_h = 4 * 256 * 2, 8 * 64 * 2  # T K, T topk inner
+    for at in (x, x + size_x - 16, x - size_h + 16):
+        assert gate_up(h=ctypes.c_void_p(at)) == UNSUP

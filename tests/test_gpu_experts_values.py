@@ -150,3 +150,19 @@ def test_equal_scales_in_all_groups_change_nothing(counts, K, N, dtype):
     assert torch.equal(awq.awq_moe_down(x, *many.dev, ids, w, 32), awq.awq_moe_down(x, *one, ids, w, -1))
     assert torch.equal(awq.awq_moe_gate_up(x, *(t.contiguous() for t in many.dev), ids, 32),
                        awq.awq_moe_gate_up(x, *one, ids, -1))
+
+
+@DTYPES
+@pytest.mark.parametrize("counts", [(3, 2), (100, 140)], ids=["5", "240"])
+def test_outputs_over_inputs(counts, dtype):
+    """y may lie where h or x was; h may not lie where x is."""
+    E, T, K, g = len(counts), sum(counts), 128, 32
+    ids, w = routed_by_counts(counts, 41)
+    up, down = Layer(E, K, 2 * K, g, 42), Layer(E, K, K, g, 43)
+    x = activations((T, K), dtype, 44)
+    with pytest.raises(ValueError):
+        awq.awq_moe_gate_up(x, *up.dev, ids, g, out=x)
+    for call in (lambda v, **kw: awq.awq_moe_down(v, *down.dev, ids, w, g, **kw),
+                 lambda v, **kw: awq.awq_moe_mlp(v, up.dev, down.dev, ids, w, g, **kw)):
+        want, over = call(x), x.clone()
+        assert torch.equal(call(over, out=over), want)

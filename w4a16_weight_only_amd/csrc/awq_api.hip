@@ -478,6 +478,10 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
   if (workspace_bytes < p.workspace_bytes()) return AWQ_ERR_UNSUPPORTED;
 
   const int64_t S = T * topk;
+  // The gated product alone writes h while other workgroups still read x; in the others nothing
+  // reads x or h any more when y is written.
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), h0 = reinterpret_cast<uintptr_t>(out);
+  if (!down && x0 < h0 + (uintptr_t)(S * inner * 2) && h0 < x0 + (uintptr_t)(T * K * 2)) return AWQ_ERR_UNSUPPORTED;
   char* ws = static_cast<char*>(workspace);
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.sorted_bytes);
   float* sums = reinterpret_cast<float*>(ws + p.sorted_bytes + p.h_bytes);

@@ -169,7 +169,7 @@ def awq_moe_gate_up(x: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor
     """First half of the gated MLP: x [T, K] (fp16 or bfloat16), weights of 2 I columns (the
     gate's first), expert_ids int32 [T, topk] -> h [T * topk, I] in x's type,
     h[t topk + j] = silu(x[t] . gate) * (x[t] . up) of expert expert_ids[t, j].  Rows of ids
-    outside [0, E) keep what `out` holds."""
+    outside [0, E) keep what `out` holds, which may not overlap x."""
     _check_act("x", x)
     dev = x.device
     T, K = x.shape
