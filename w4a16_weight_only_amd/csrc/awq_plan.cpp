@@ -475,7 +475,8 @@ int64_t entry_bound(int64_t S, int64_t E, int64_t rows) {
 // reads its fp32 sums once (4 TB/s), and splits of a gated product cost the kernel that joins
 // them.  Measured against forced split counts, us per call: one token through 8 x 4096 -> 14336,
 // gated: 1, 2, 3, 4, 9 splits 56, 35.6, 36.5, 32.5, 34.3 (4 chosen: 448 workgroups); 45 tokens
-// over 64 x 2048 -> 1408: 1, 2, 3, 9 splits 65.3, 67.4, 70.5, 71.3 (1 chosen).
+// over 64 x 2048 -> 1408: 1, 2, 3, 9 splits 65.3, 67.4, 70.5, 71.3 (1 chosen); one expert 4096 ->
+// 4096, 256 rows: 2, 3 splits 33.5, 37.3 (2), 1024 rows: 1, 2 splits 80, 88 (1).
 void choose_splits(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t wide, int64_t cus, bool gated, ExpertPlan& p) {
   // Experts with rows, about, where a token's are distinct: E (1 - (1 - topk / E)^T).
   const int64_t S = T * topk;
@@ -483,13 +484,18 @@ void choose_splits(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t wide, 
   for (int64_t t = 0; t < T && idle > 1e-3; ++t) idle *= topk < E ? 1.0 - (double)topk / (double)E : 0.0;
   int64_t active = (int64_t)((double)E * (1.0 - idle) + 0.5);
   if (active < 1) active = 1;
+  // Their entries: one each, or, of several, half an entry more than the rows fill (one expert's
+  // last is as full as its rows make it).
+  const int64_t rows = p.block_rows;
+  const int64_t full = (2 * S + (active - 1) * rows + 2 * rows - 1) / (2 * rows);
+  const int64_t entries = full > active ? full : active;
   const int64_t parts = gated ? 2 : 4;  // waves of a workgroup along K
   const int64_t ksteps = K / 32;
   int64_t best = -1;
   for (int64_t want = 1; want <= kExpertMaxSplits; ++want) {
     const int64_t steps = (ksteps + want * parts - 1) / (want * parts);
     const int64_t splits = (ksteps + steps * parts - 1) / (steps * parts);
-    const int64_t n = (active * p.col_tiles * splits + cus - 1) / cus;
+    const int64_t n = (entries * p.col_tiles * splits + cus - 1) / cus;
     int64_t cost = steps * (12 * (n / 2) + 7 * (n % 2)) + 30 * ((n + 1) / 2);
     if (!gated || splits > 1) cost += splits * S * wide / 50000;
     if (gated && splits > 1) cost += 45;
