@@ -60,3 +60,26 @@ def test_no_splits_where_entries_fill_the_card(plans):
             filled += 1
             assert d["splits"] == 1, (c, d)
     assert filled > 100
+
+
+def test_family_by_row_tiles(plans):
+    """Row tiles from a third of the card's workgroups on: the second product of prompts through
+    8 x 4096 -> 14336, one dense expert."""
+    got = plans([(T, 2, 8, 4096, 14336, 4096, 128, MLP) for T in (200, 320, 512, 768, 1024)])
+    assert [(p["up"]["stream"], p["down"]["stream"]) for p in got] == [(1, 1), (0, 1), (0, 1), (0, 0), (0, 0)]
+    got = plans([(T, 1, 1, 0, 4096, 4096, 128, DOWN) for T in (64, 1024, 2048)])
+    assert [p["down"]["stream"] for p in got] == [1, 1, 0]
+
+
+def test_families_of_the_gpu_tests(plans):
+    """The GPU tests of row tiles, and of both kernels in one call, run what they say."""
+    from tests import expert_sizes as sizes
+
+    for counts in sizes.HEIGHTS:
+        S, E = sum(counts), len(counts)
+        for K, g in sizes.HEIGHT_KS:
+            p, q = plans([(S, 1, E, K, sizes.HEIGHT_INNER, 0, g, GATE_UP), (S, 1, E, 0, K, sizes.HEIGHT_N, g, DOWN)])
+            assert not p["up"]["stream"] and not q["down"]["stream"], (counts, K)
+    for (T, E, topk, K, inner, N, g), up, down in sizes.FAMILIES:
+        p = plans([(T, topk, E, K, inner, N, g, MLP)])[0]
+        assert (p["up"]["stream"], p["down"]["stream"]) == (up, down) and not p["two_terms"], (T, E, inner, N)

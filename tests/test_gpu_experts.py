@@ -214,7 +214,7 @@ def test_long_axes(T, E, topk, K, inner, N, g, dtype):
     check_mlp(x, up, down, ids, w, g, y, dtype)
 
 
-# Row tiles: more than 80 slots per expert, and enough columns that the tiles fill half of the
+# Row tiles: more than 72 slots per expert, and enough columns that the tiles fill a third of the
 # card.  Rows per expert around every height of a tile (64, 128, 192, 256), one more than one,
 # none, a few.
 COUNTS = [(300, 190, 0, 130, 100, 64, 20, 1), (512, 257, 193, 129, 65), (256, 192, 128, 64)]

@@ -511,10 +511,13 @@ int plan_expert(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int cu
   const int64_t S = T * topk;
   const int64_t wide = gated ? 2 * N : N;
   if (K * (wide / 2) >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into one expert's weight
-  // Few rows per expert, or too few row tiles to fill half of the card.
+  // Few rows per expert, or too few row tiles to fill a third of the card.  Streamed / tiles, us:
+  // 8 x 14336 -> 4096, top 2, 512 tokens (64 tiles) 286 / 355, 768 (96) 398 / 373, 1024 (128) 514 /
+  // 374; one expert 4096 -> 4096, 1024 rows (64) 80 / 121, 2048 (128) 147 / 128; 80 tiles: 8 x 4096
+  // -> 2048, 1200 tokens 104 / 118, gate_up of 600 tokens 8 x 4096 -> 2048 127 / 114.
   const int64_t tile_cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
   const int64_t row_tiles = (S + kExpertTileRows - 1) / kExpertTileRows * ((N + tile_cols - 1) / tile_cols);
-  p.stream = S <= kExpertStreamRows * E || 2 * row_tiles <= cus;
+  p.stream = S <= kExpertStreamRows * E || 3 * row_tiles <= cus;
   if (p.stream) {
     p.ranked = S <= kExpertRankSlots;
     p.rows = S <= 4 ? 4 : S <= 8 ? 8 : S < kExpertWideRows * E ? 16 : 32;

@@ -203,8 +203,8 @@ constexpr int kExpertTileCols = 256;    // weight columns of a workgroup
 constexpr int kExpertStreamCols = 256;  // columns of a workgroup (gated: of each half)
 // Most slots per expert, on average, to stream.  Measured, us per call, streamed / tiles: mlp
 // 64 x 2048 -> 1408, 48, 64, 80 slots per expert 188 / 189, 222 / 228, 266 / 263 (bfloat16, 64:
-// 231 / 249); 8 x 4096 -> 14336, 48, 64, 80: 353 / 417, 456 / 475, 493 / 468; one expert 4096 ->
-// 4096 (64 and 32 tiles' workgroups), 512 rows 119 / 252.
+// 231 / 249); 8 x 4096 -> 14336, 48, 64, 80: 353 / 417, 456 / 475, 493 / 468.  (And where there
+// are too few row tiles: see plan_expert.)
 constexpr int64_t kExpertStreamRows = 72;
 // Slots per expert from which entries take 32 rows: 16 / 32 rows, mlp 64 x 2048 -> 1408, 4, 8,
 // 16, 32 slots per expert 87 / 92, 101 / 98, 128 / 115, 186 / 150; 8 x 4096 -> 14336, 8, 12, 16:
