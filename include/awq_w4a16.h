@@ -306,7 +306,8 @@ int awq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int
  *   awq_moe_down      y[t, :] = sum over j of weights[t, j] * (h[s] . W[e])
  *   awq_moe_mlp       both, h kept in the workspace, rounded to the activation type; up to 64
  *                     slots (with more than 8, fewer than 12 per expert) also what that
- *                     rounding leaves out, so that y is rounded once
+ *                     rounding leaves out, so that y is rounded once.  An h beyond the
+ *                     activation type's range is infinite, as awq_moe_gate_up gives it
  * with silu(v) = v / (1 + exp(-v)).
  *   act            AWQ_F16 or AWQ_BF16: the type of x, h and y (scales stay fp16); for down and
  *                  mlp plus AWQ_NAN_WEIGHTS, if wanted

@@ -511,8 +511,9 @@ __global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(const ExpertPr
   int block = blockIdx.x - small * tiles * n_tiles;
   if constexpr (GATED) {
     // A tile's 64 bytes of a half's row share a 128-byte line with its neighbour's: the two go to
-    // one XCD, whose L2 then fetches it once (gate_up of 1024 tokens 8 x 4096 -> 14336 604 -> 590
-    // us, mlp of 2048 tokens 64 x 2048 -> 1408 516 -> 505).
+    // one XCD, whose L2 then fetches it once.  Without / with, the same routing, us: gate_up 8 x 4096
+    // -> 14336, 700, 1024, 2048 tokens 447 / 441, 606 / 596, 1068 / 1051; 64 x 2048 -> 1408, 700, 1200,
+    // 2048 tokens 192 / 190, 237 / 220, 313 / 303.
     if (block < ((tiles * n_tiles) & ~15)) block = (block & ~15) | ((block & 7) << 1) | ((block >> 3) & 1);
   }
   const int entry = block / n_tiles;

@@ -16,7 +16,9 @@
 // scores that groups may be worth, whose experts then still go by their logits without a bias.
 // Weights.  Renormalised scores are quotients, so a common factor is taken out first:
 // exp(l - max over the chosen) instead of the softmax, and exp(min(l, 0) - min(max, 0)) /
-// (1 + exp(-|l|)) for the sigmoid, so that scores too small for fp32 still divide.
+// (1 + exp(-|l|)) for the sigmoid, so that scores too small for fp32 still divide.  They are formed
+// in fp32, their type: off by 6e-8 of their size on the measured cases, where one rounding is 3e-8
+// (in fp64, us fp32 / fp64: 16384 tokens of 128 experts 7.7 / 8.5, not divided 8.5 / 10.8).
 //
 // One token per LPT lanes (16: four tokens a wave, for many tokens; else 64), each lane
 // holding VPL consecutive experts in registers, lanes in index order, so a tie goes to the

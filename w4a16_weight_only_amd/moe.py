@@ -215,7 +215,8 @@ def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.
     (qweight, qzeros, scales) of K -> 2 I and I -> N columns, expert_ids int32 and weights fp32
     [T, topk] -> y [T, N] in x's type.  The same values as awq_moe_down of awq_moe_gate_up, but
     for a decoding step's few slots (up to 64, of which at most 8 or fewer than 12 per expert),
-    where h is not rounded on the way.  nan_weights as for awq_moe_down."""
+    where h is not rounded on the way (a larger batch in parts of so many slots has that too).  An h
+    beyond the type's range is infinite, as awq_moe_gate_up's is.  nan_weights as for awq_moe_down."""
     _check_act("x", x)
     dev = x.device
     T, K = x.shape
