@@ -62,13 +62,13 @@ struct Step {
 // where fp16's 1024 + q takes 1.25 with packed additions.  (A bfloat16 128 + q takes 1.0, but leaves
 // x . (128 + q) - (128 + z) x . 1 to be formed: partial sums with four to five bits fewer, and NaN
 // where an infinite x gives an infinity.  That / this, us: gate_up of 45 tokens 64 x 2048 -> 1408
-// 61 / 67, mlp of 16 tokens 8 x 4096 -> 14336 158 / 168, of 256 tokens 64 x 2048 -> 1408 170 / 171.)
-__device__ __forceinline__ uint32_t minus_zero_bf16(uint32_t a, uint32_t b, int half, float scale, float neg) {
-  return pack_bf16x2(fmaf((float)as_h2(a)[half], scale, neg), fmaf((float)as_h2(b)[half], scale, neg));
+// 61 / 64, mlp of 16 tokens 8 x 4096 -> 14336 157 / 163, of 256 tokens 64 x 2048 -> 1408 170 / 165.)
+__device__ __forceinline__ uint32_t minus_zero_bf16(uint32_t a, uint32_t b, int half, float scale, float z) {
+  return pack_bf16x2(fmaf((float)as_h2(a)[half], scale, -z), fmaf((float)as_h2(b)[half], scale, -z));
 }
 
 // The 16 RB MFMAs of a k-step.  zs: per column, fp16: -(1024 + z) or -(64 + z) twice (low or high
-// nibble); bfloat16: -z as a float.
+// nibble); bfloat16: z as a float.
 template <bool BF16, int RB, bool REST>
 __device__ __forceinline__ void multiply(const Step<RB, REST>& st, const uint32_t (&zs)[16], const UnpackConsts& uk,
                                          floatx4 (&part)[RB][16]) {
@@ -291,35 +291,55 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) part[rb][v] = floatx4{0.f, 0.f, 0.f, 0.f};
     zs[v] = 0;
-    unit[v >> 3][v & 7] = (_Float16)1.f;
+    unit[v >> 3][v & 7] = (_Float16)1.f;  // (columns in order)
   }
-  // A group begins: the sums so far change units (there are none when the run begins).
+  // A group begins: the sums so far change units (there are none when the run begins).  A scale of
+  // zero is looked for in pairs of halves, and dealt with column by column where there is one (every
+  // column asking for itself: gate_up of 45 tokens 64 x 2048 -> 1408, g 64, bfloat16 68 / 63.7 us).
   auto enter = [&](const GroupData& d, bool begin) {
+    half8v now[2] = {d.s[0], d.s[1]};
     nil = u32x2{0u, 0u};
+    uint32_t zero = 0;  // a half of zero, either sign: the halves' borrow trick
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const _Float16 s = d.s[v >> 3][col_of(v)];
-      const _Float16 old = unit[v >> 3][v & 7];
-      const bool none = s == (_Float16)0.f;
-      const _Float16 now = none ? old : s;
-      if (!begin) {
-        const float ratio = now == old ? 1.f : (float)old * __builtin_amdgcn_rcpf((float)now);
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t s = __builtin_bit_cast(u32x4, now[w])[i] & 0x7FFF7FFFu;
+        zero |= (s - 0x00010001u) & ~s & 0x80008000u;
+      }
+    any_nil = __builtin_amdgcn_ballot_w64(zero != 0) != 0;
+    if (any_nil) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const bool none = now[v >> 3][col_of(v)] == (_Float16)0.f;
+        now[v >> 3][col_of(v)] = none ? unit[v >> 3][col_of(v)] : now[v >> 3][col_of(v)];
+        nil[v >> 3] |= none ? 0xFu << (4 * (v & 7)) : 0u;  // entry v is nibble v % 8 of its word
+      }
+    }
+    if (!begin) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const float o = (float)unit[v >> 3][col_of(v)], n = (float)now[v >> 3][col_of(v)];
+        const float ratio = n == o ? 1.f : o * __builtin_amdgcn_rcpf(n);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) part[rb][v] *= ratio;
       }
-      unit[v >> 3][v & 7] = now;
-      nil[v >> 3] |= none ? 0xFu << (4 * (v & 7)) : 0u;  // entry v is nibble v % 8 of its word
-      const uint32_t z = zero_code(d.z[v >> 3], col_of(v));
+    }
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
       if constexpr (BF16) {
-        zs[v] = __builtin_bit_cast(uint32_t, -(float)z);
+        const uint32_t z = (v & 1 ? d.z[v >> 3] >> 4 : d.z[v >> 3]) & 0x0F0F0F0Fu;
+        zs[v] = __builtin_bit_cast(uint32_t, (float)((z >> (8 * ((v & 7) >> 1))) & 0xFFu));
       } else {
+        const uint32_t z = zero_code(d.z[v >> 3], col_of(v));
         const uint32_t h = (v & 1) ? (0xD400u | (z << 4)) : (0xE400u | z);  // -(64 + z), -(1024 + z)
         zs[v] = h | (h << 16);
       }
     }
+    unit[0] = now[0];
+    unit[1] = now[1];
     zw = d.z;
     enter_at = begin ? first_end : enter_at + gsteps;
-    any_nil = __builtin_amdgcn_ballot_w64((nil[0] | nil[1]) != 0) != 0;
   };
   Step<RB, REST> ring[kPF];
   if (kOneSet && kb < ke) fetch(data[0]);
@@ -360,7 +380,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
     if (rb > 0) __syncthreads();  // the last block's rows have left
     if (lane < RL) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) sh.red[wave][v][lane] = part[rb][v] * (float)unit[v >> 3][v & 7];
+      for (int v = 0; v < 16; ++v) sh.red[wave][v][lane] = part[rb][v] * (float)unit[v >> 3][col_of(v)];
     }
     __syncthreads();
     floatx4 sum[SLOTS][HALVES];
