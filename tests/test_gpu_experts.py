@@ -6,8 +6,8 @@ of the activation type (2^-11 fp16, 2^-8 bfloat16), tiny its smallest step's hal
   quotient of scales at each of the G group boundaries (three roundings, one of them a
   reciprocal good to two of u): at most (K + 4 G + 4) roundings of something no larger than
   A = sum |x| |W|, so it is off by dP = (K + 4 G + 4) u A.
-  Where sums are corrected for the zeros afterwards (x . (128 + q) - (128 + z) x . 1), A is
-  sum |x| (143 + 143) s instead.
+  For bfloat16 A is sum |x| (143 + 143) s, that of sums corrected for the zeros afterwards
+  (x . (128 + q) - (128 + z) x . 1): wider than products of q - z need, which these now are.
   h = silu(g) u: |silu'| <= 1.1, so dh = 1.1 dP_g |u| + |silu(g)| dP_u + dP_g dP_u + 8 u |h|
   (exp, quotient, product), then r |h| + tiny for the rounding.
   y = sum_j w_j v_j: sum |w_j| dP_j + (topk + 2) u sum |w_j| |v_j| + r |y| + tiny.

@@ -202,20 +202,22 @@ constexpr int kExpertTileRows = 256;
 constexpr int kExpertTileCols = 256;    // weight columns of a workgroup
 constexpr int kExpertStreamCols = 256;  // columns of a workgroup (gated: of each half)
 // Most slots per expert, on average, to stream.  Measured, us per call, streamed / tiles: mlp
-// 64 x 2048 -> 1408, 48, 64, 80 slots per expert 188 / 189, 222 / 228, 266 / 263 (bfloat16, 64:
-// 231 / 249); 8 x 4096 -> 14336, 48, 64, 80: 353 / 417, 456 / 475, 493 / 468.  (And where there
-// are too few row tiles: see plan_expert.)
+// 64 x 2048 -> 1408, g 128, 48, 64, 80 slots per expert 185 / 199, 219 / 241, 263 / 263 (bfloat16,
+// 64, 80: 226 / 260, 274 / 287), g 64 186 / 222, 227 / 263, 272 / 293; 8 x 4096 -> 14336, 48, 64, 80:
+// 345 / 399, 428 / 447, 488 / 475 (bfloat16 352 / 420, 443 / 472, 505 / 507).  (And where there are
+// too few row tiles: see plan_expert.)
 constexpr int64_t kExpertStreamRows = 72;
-// Slots per expert from which entries take 32 rows: 16 / 32 rows, mlp 64 x 2048 -> 1408, 4, 8,
-// 16, 32 slots per expert 87 / 92, 101 / 98, 128 / 115, 186 / 150; 8 x 4096 -> 14336, 8, 12, 16:
-// 159 / 192, 199 / 202, 237 / 209.
+// Slots per expert from which entries take 32 rows: 16 / 32 rows, us, mlp 64 x 2048 -> 1408, 4, 8,
+// 16, 32 slots per expert 84 / 93, 97 / 97, 127 / 112, 190 / 150 (bfloat16 93 / 106, 106 / 111, 137 /
+// 125, 200 / 166); 8 x 4096 -> 14336, 8, 12, 16: 164 / 165, 199 / 175, 232 / 183 (171 / 179, 206 /
+// 185, 246 / 191).
 constexpr int64_t kExpertWideRows = 12;
 // Entries from which a streaming grid keeps each on one XCD: rows of a weight that are no whole
 // 128-byte lines (64 x 2048 -> 1408: the up projection's half starts inside one) make neighbouring
 // column tiles share lines, which two L2s would each fetch (gate_up of 45 tokens read 1.5 times
-// its bytes).  Spread over all XCDs / one each, us: gate_up of 45 tokens 66 / 61, mlp of 4, 16, 64,
-// 256 tokens 48.7 / 46, 78 / 73.5, 101 / 94, 149.7 / 149.  Fewer entries leave XCDs idle: from 8
-// entries on, 24 tokens of 20 experts 45 / 52.7, 5 of 8 x 4096 -> 14336 114 / 157.
+// its bytes).  Spread over all XCDs / one each, us: gate_up of 45 tokens, fp16, 64 / 58, mlp of 4, 16,
+// 64, 256 tokens 51 / 48.7, 82 / 77, 104 / 97, 152 / 150.  Fewer entries leave XCDs idle: from 8
+// entries on, 24 tokens of 20 experts 30.3 / 34.2, 5 of 8 x 4096 -> 14336 115 / 154.
 constexpr int64_t kExpertXcdEntries = 32;
 constexpr int64_t kExpertMaxSplits = 32;
 constexpr int64_t kExpertRankSlots = 64;  // slots a wave can rank, one per lane
@@ -226,8 +228,10 @@ struct ExpertsPlan {
   ExpertPlan up, down;
   // h as two terms, rounded and what that leaves out: a decoding step's few slots, whose h's
   // rounding no number of tokens averages out.  (To 64 slots.  One term / two, us: mlp of one
-  // token 64 x 2048 -> 1408 25.0 / 25.4, 8 x 4096 -> 14336 51.4 / 52.5, 16 tokens 153.4 / 157.8;
-  // 128 slots 77.5 / 80.0, 80 of the second 183.7 / 192.4.)
+  // token 64 x 2048 -> 1408 24.9 / 25.4, 8 x 4096 -> 14336 51.4 / 52.6, 16 tokens 151 / 155 (bfloat16
+  // 158.5 / 164).  Row tiles, bound by their MFMAs, would take most of the second product's time
+  // again, 184 of 512 us for 2048 tokens 64 x 2048 -> 1408; beyond the limit h is what
+  // awq_moe_gate_up gives, bit for bit.)
   bool two_terms = false;
   int64_t sorted_bytes = 0, h_bytes = 0, sums_bytes = 0;
   int64_t workspace_bytes() const { return sorted_bytes + h_bytes + sums_bytes; }
