@@ -62,6 +62,9 @@ enum { AWQ_NAN_WEIGHTS = 256 };
 /* Scores of awq_moe_route. */
 enum awq_score { AWQ_SOFTMAX = 0, AWQ_SIGMOID = 1 };
 
+/* Norms of awq_add_norm. */
+enum awq_norm_kind { AWQ_RMS = 0, AWQ_LAYER = 1 };
+
 /* Human-readable name of a status code; never NULL, static storage. */
 const char* awq_status_string(int status);
 
@@ -352,6 +355,35 @@ int awq_moe_mlp(const void* x, int act, const int32_t* up_qweight, const int32_t
                 int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
                 int64_t group_size, void* y, void* workspace, int64_t workspace_bytes,
                 struct ihipStream_t* stream);
+
+/*
+ * Norms on the residual stream, before and after a block, in one pass over it:
+ *   z = x, or, with post_weight, norm(x) * post_weight + post_bias
+ *   r = residual + scale * gate * z
+ *   y = norm(r) * weight + bias, of r before its rounding
+ * with norm(v) = v / sqrt(mean(v^2) + eps) over a row (AWQ_RMS), or the same of v - mean(v)
+ * (AWQ_LAYER); unit_offset nonzero: 1 + weight and 1 + post_weight in place of the weights.
+ *   x            device [T, H] of act (AWQ_F16, AWQ_BF16), rows x_stride elements apart
+ *   residual     device [T, H] of residual_type (act, or AWQ_F32), rows residual_stride apart; or
+ *                NULL: nothing is added
+ *   gate         device [gates, H] of act, or NULL: 1.  Row i is that of T / gates consecutive
+ *                rows of x (1: all of them, T: each its own; T % gates == 0)
+ *   post_weight, post_bias, weight, bias   device [H] of act; all but weight may be NULL
+ *                (post_bias needs post_weight)
+ *   y            device [T, H] of act
+ *   r            device [T, H] of residual_type, or NULL: not written
+ * Pointers need their element's alignment only; rows that all begin on 16 bytes, with H % 8 == 0,
+ * are read and written 16 bytes at a time.  Sums, statistics and r are fp32; r and y are rounded
+ * once each.  A NaN or infinity reaches its own row only.  Values beyond 1e17 or so overflow the
+ * fp32 sum of squares, as they would in any fp32 norm.
+ * r may be residual itself and y may be x itself (rows H apart); any other overlap of an output is
+ * refused (AWQ_ERR_UNSUPPORTED).  Limits: H <= 32768, T <= 2^24.  T == 0 enqueues nothing.  No
+ * workspace.  The result is deterministic.
+ */
+int awq_add_norm(const void* x, int act, int64_t T, int64_t H, int64_t x_stride, const void* residual,
+                 int residual_type, int64_t residual_stride, const void* gate, int64_t gates, float scale,
+                 const void* post_weight, const void* post_bias, const void* weight, const void* bias, int kind,
+                 int unit_offset, float eps, void* y, void* r, struct ihipStream_t* stream);
 
 /*
  * Round-to-nearest writer of the GEMM pack: quantise an fp16 weight in groups of

@@ -265,3 +265,27 @@ def test_quantization_config():
                 {**cfg, "quant_method": "gptq"}):
         with pytest.raises(ValueError):
             awq.group_size_from_config(bad)
+
+
+def test_norm_argument_errors_touch_no_device(lib):
+    """awq_add_norm checks sizes, types, pointers and overlaps before any HIP call."""
+    base = 1 << 20
+    p = ctypes.c_void_p
+
+    def call(x=base, act=0, T=4, H=64, xs=64, res=base * 2, rt=0, rs=64, gate=None, gates=0, pw=None, pb=None,
+             w=base * 3, b=None, kind=0, y=base * 4, r=base * 5):
+        f = lambda v: None if v is None else p(v)  # noqa: E731
+        return lib.awq_add_norm(f(x), act, T, H, xs, f(res), rt, rs, f(gate), gates, 1.0, f(pw), f(pb), f(w), f(b),
+                                kind, 0, 1e-6, f(y), f(r), None)
+
+    assert call(T=0) == _lib.AWQ_OK
+    assert call(T=-1) == call(H=0, xs=0) == call(xs=63) == call(rs=32) == _lib.AWQ_ERR_SHAPE
+    assert call(gate=base * 6, gates=3) == call(gate=base * 6, gates=0) == _lib.AWQ_ERR_SHAPE
+    assert call(H=32769, xs=32769, rs=32769) == call(T=(1 << 24) + 1) == _lib.AWQ_ERR_UNSUPPORTED
+    assert call(act=2) == call(rt=1) == call(kind=2) == _lib.AWQ_ERR_UNSUPPORTED
+    assert call(x=None) == call(w=None) == call(y=None) == call(pb=base * 6) == _lib.AWQ_ERR_NULL
+    assert call(x=base + 1) == call(rt=2, res=base * 2 + 2) == call(rt=2, r=base * 5 + 2) == _lib.AWQ_ERR_ALIGN
+    # y in x's place or r in residual's would be taken; every other overlap is not.
+    assert call(y=base + 2) == call(y=base * 2) == call(r=base) == call(r=base * 4 + 510) == _lib.AWQ_ERR_UNSUPPORTED
+    assert call(y=base, xs=72) == call(r=base * 2, rs=72) == call(y=base * 3) == _lib.AWQ_ERR_UNSUPPORTED
+    assert call(rt=2, r=base * 2 + 4) == _lib.AWQ_ERR_UNSUPPORTED

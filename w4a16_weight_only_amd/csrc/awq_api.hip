@@ -439,6 +439,75 @@ int awq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int
   return awq::launch_route(a, stream) == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
 }
 
+namespace {
+
+// Whether two byte ranges share a byte.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && a0 < b0 + (uintptr_t)b_bytes && b0 < a0 + (uintptr_t)a_bytes;
+}
+
+}  // namespace
+
+int awq_add_norm(const void* x, int act, int64_t T, int64_t H, int64_t x_stride, const void* residual,
+                 int residual_type, int64_t residual_stride, const void* gate, int64_t gates, float scale,
+                 const void* post_weight, const void* post_bias, const void* weight, const void* bias, int kind,
+                 int unit_offset, float eps, void* y, void* r, struct ihipStream_t* stream) {
+  const int st = plan_norm(T, H, x_stride, residual ? residual_stride : H, gate ? gates : 0);
+  if (st != AWQ_OK) return st;
+  if (act != AWQ_F16 && act != AWQ_BF16) return AWQ_ERR_UNSUPPORTED;
+  const bool r32 = residual_type == AWQ_F32;
+  if ((residual || r) && !r32 && residual_type != act) return AWQ_ERR_UNSUPPORTED;
+  if (kind != AWQ_RMS && kind != AWQ_LAYER) return AWQ_ERR_UNSUPPORTED;
+  if (gate && gates == 0) return AWQ_ERR_SHAPE;
+  if (T == 0) return AWQ_OK;
+  if (!x || !weight || !y || (post_bias && !post_weight)) return AWQ_ERR_NULL;
+  const uintptr_t unit = r32 ? 4 : 2;
+  for (const void* p : {x, gate, post_weight, post_bias, weight, bias, (const void*)y})
+    if (reinterpret_cast<uintptr_t>(p) % 2 != 0) return AWQ_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(residual) % unit != 0 || reinterpret_cast<uintptr_t>(r) % unit != 0) return AWQ_ERR_ALIGN;
+  // A row is read whole before it is written, so r may take residual's place and y that of x, row
+  // for row; nothing else that is read or written may share memory with them.
+  const int64_t x_bytes = ((T - 1) * x_stride + H) * 2, y_bytes = T * H * 2, r_bytes = T * H * (int64_t)unit;
+  const int64_t res_bytes = ((T - 1) * residual_stride + H) * (int64_t)unit;
+  auto clash = [&](const void* out, int64_t bytes, const void* same, int64_t same_stride, int64_t same_unit,
+                   int64_t out_unit) {
+    auto meets = [&](const void* in, int64_t in_bytes, int64_t stride, int64_t in_unit) {
+      const bool in_place = in == same && in == out && stride == same_stride && (T == 1 || stride == H) &&
+                            in_unit == same_unit && in_unit == out_unit;
+      return !in_place && overlap(out, bytes, in, in_bytes);
+    };
+    return meets(x, x_bytes, x_stride, 2) || meets(residual, res_bytes, residual_stride, (int64_t)unit) ||
+           overlap(out, bytes, gate, gates * H * 2) || overlap(out, bytes, post_weight, H * 2) ||
+           overlap(out, bytes, post_bias, H * 2) || overlap(out, bytes, weight, H * 2) || overlap(out, bytes, bias, H * 2);
+  };
+  if (clash(y, y_bytes, x, x_stride, 2, 2) || clash(r, r_bytes, residual, residual_stride, (int64_t)unit, (int64_t)unit) ||
+      overlap(y, y_bytes, r, r_bytes))
+    return AWQ_ERR_UNSUPPORTED;
+  NormArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.post_weight = static_cast<const uint16_t*>(post_weight);
+  a.post_bias = static_cast<const uint16_t*>(post_bias);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.residual = residual;
+  a.y = static_cast<uint16_t*>(y);
+  a.r = r;
+  a.T = T;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.gate_rows = gate ? T / gates : 1;
+  a.H = (int)H;
+  a.scale = scale;
+  a.eps = eps;
+  a.bf16 = act == AWQ_BF16;
+  a.r32 = r32;
+  a.layer = kind == AWQ_LAYER;
+  a.unit_offset = unit_offset != 0;
+  return awq::launch_norm(a, stream) == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
+}
+
 int64_t awq_moe_workspace(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
                           int64_t group_size) {
   if (K < 0 || N < 0 || (K == 0 && N == 0)) return AWQ_ERR_SHAPE;

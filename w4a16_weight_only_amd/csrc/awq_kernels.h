@@ -133,4 +133,18 @@ hipError_t launch_expert_gate(const float* sums, const int32_t* ids, int S, int 
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
                                  int N, int splits, bool bf16, bool nan_weights, uint16_t* y, hipStream_t stream);
 
+// Norms on the residual stream (awq_add_norm).  x, gate, weights, biases and y are fp16 or (bf16)
+// bfloat16; residual and r too, or (r32) fp32.  Strides in elements; gate row t / gate_rows.
+struct NormArgs {
+  const uint16_t *x, *gate, *post_weight, *post_bias, *weight, *bias;
+  const void* residual;
+  uint16_t* y;
+  void* r;
+  int64_t T, x_stride, residual_stride, gate_rows;
+  int H;
+  float scale, eps;
+  bool bf16, r32, layer, unit_offset;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
 }  // namespace awq

@@ -456,6 +456,14 @@ int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t
   return AWQ_OK;
 }
 
+int plan_norm(int64_t T, int64_t H, int64_t x_stride, int64_t residual_stride, int64_t gates) {
+  if (T < 0 || H < 1 || x_stride < H || residual_stride < H || gates < 0) return AWQ_ERR_SHAPE;
+  if (gates > 0 && T % gates != 0) return AWQ_ERR_SHAPE;
+  if (H > kNormMaxH || T > kMaxDim) return AWQ_ERR_UNSUPPORTED;
+  if (x_stride > (int64_t(1) << 36) || residual_stride > (int64_t(1) << 36)) return AWQ_ERR_UNSUPPORTED;
+  return AWQ_OK;
+}
+
 namespace {
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }

@@ -180,6 +180,10 @@ constexpr int64_t kRouteMaxGroups = 64;
 int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t topk_groups, int group_top,
                int64_t topk);
 
+// awq_add_norm: the longest row that its kernels hold in registers.
+constexpr int64_t kNormMaxH = 32768;
+int plan_norm(int64_t T, int64_t H, int64_t x_stride, int64_t residual_stride, int64_t gates);
+
 // One product of routed rows with their experts' weights (gated: N pairs of columns of a
 // 2 N wide weight).  Entries are up to `rows` routed rows of one expert:
 //   stream   few rows per expert: 4, 8, 16 or 32 rows kept, workgroups over (entry, column tile
