@@ -62,6 +62,12 @@ enum { AWQ_NAN_WEIGHTS = 256 };
 /* Scores of awq_moe_route. */
 enum awq_score { AWQ_SOFTMAX = 0, AWQ_SIGMOID = 1 };
 
+/* Activations of awq_gemm_fused: v; max(v, 0); v / (1 + exp(-v)); v (1 + erf(v / sqrt 2)) / 2;
+ * v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2. */
+enum awq_activation {
+  AWQ_ACT_NONE = 0, AWQ_ACT_RELU = 1, AWQ_ACT_SILU = 2, AWQ_ACT_GELU = 3, AWQ_ACT_GELU_TANH = 4
+};
+
 /* Norms of awq_add_norm. */
 enum awq_norm_kind { AWQ_RMS = 0, AWQ_LAYER = 1 };
 
@@ -355,6 +361,36 @@ int awq_moe_mlp(const void* x, int act, const int32_t* up_qweight, const int32_t
                 int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
                 int64_t group_size, void* y, void* workspace, int64_t workspace_bytes,
                 struct ihipStream_t* stream);
+
+/*
+ * A dense product with its epilogue:
+ *   y[m, n] = residual[m, n] + scale * f(x[m] . W[:, n] + bias[n])
+ * or, gated, of a weight with the gate's N columns first, then the up projection's:
+ *   y[m, n] = residual[m, n] + scale * f(x[m] . W[:, n] + bias[n]) * (x[m] . W[:, N + n] + bias[N + n])
+ *   act            AWQ_F16 or AWQ_BF16: the type of x, bias, residual and y (scales stay fp16)
+ *   activation     f, one of enum awq_activation
+ *   x              device [M, K];  y device [M, N], written in full
+ *   weight         qweight int32 [K, C / 8], qzeros [G, C / 8], scales fp16 [G, C], C = N or, gated, 2 N
+ *   bias           device [C], or NULL;  residual device [M, N], or NULL.  y may be residual itself;
+ *                  it may not overlap x, or residual in part (AWQ_ERR_UNSUPPORTED)
+ *   workspace      device memory of workspace_bytes as awq_gemm_fused_plan gives them, 16-byte
+ *                  aligned, for this call alone until its work on the stream is done.  It needs no
+ *                  contents and keeps none
+ *   counters       device memory of counter_bytes, zero before the call and zero again after it, for
+ *                  this call alone until then.  (Calls in one stream's order may share both.)
+ * Either may be NULL where the plan's bytes are 0.
+ * The product is a sum of x times the integers (q - z), scaled per group in fp32; bias, activation
+ * and residual are applied in fp32 and y is rounded once.  The result is deterministic.  A NaN or
+ * infinity in a row of x reaches only that row.
+ * Limits: those of awq_gemm with the weight's C columns, N % 32 == 0, qweight below 4 GiB, K < 2^23
+ * (above 72 rows).  M == 0 enqueues nothing.
+ */
+int awq_gemm_fused_plan(int64_t M, int64_t K, int64_t N, int64_t group_size, int gated, int64_t* workspace_bytes,
+                        int64_t* counter_bytes);
+int awq_gemm_fused(const void* x, int act, const int32_t* qweight, const int32_t* qzeros, const void* scales_f16,
+                   const void* bias, int activation, int gated, const void* residual, float scale, int64_t M,
+                   int64_t K, int64_t N, int64_t group_size, void* y, void* workspace, int64_t workspace_bytes,
+                   void* counters, int64_t counter_bytes, struct ihipStream_t* stream);
 
 /*
  * Norms on the residual stream, before and after a block, in one pass over it:

@@ -289,3 +289,38 @@ def test_norm_argument_errors_touch_no_device(lib):
     assert call(y=base + 2) == call(y=base * 2) == call(r=base) == call(r=base * 4 + 510) == _lib.AWQ_ERR_UNSUPPORTED
     assert call(y=base, xs=72) == call(r=base * 2, rs=72) == call(y=base * 3) == _lib.AWQ_ERR_UNSUPPORTED
     assert call(rt=2, r=base * 2 + 4) == _lib.AWQ_ERR_UNSUPPORTED
+
+
+def test_fused_argument_errors_touch_no_device(lib):
+    """awq_gemm_fused checks sizes, types, pointers, workspace and overlaps before any HIP call."""
+    base = 1 << 24
+    p = ctypes.c_void_p
+
+    def plan(M, K, N, g, gated=0):
+        ws, count = ctypes.c_int64(-1), ctypes.c_int64(-1)
+        return lib.awq_gemm_fused_plan(M, K, N, g, gated, ctypes.byref(ws), ctypes.byref(count)), ws.value, count.value
+
+    assert plan(1, 4096, 4096, 128)[0] == _lib.AWQ_OK and plan(1, 4096, 4096, 128)[2] == 64  # 16 column tiles
+    assert plan(0, 4096, 4096, 128) == (_lib.AWQ_OK, 0, 0)
+    assert plan(2048, 4096, 11008, 128, 1) == (_lib.AWQ_OK, 0, 0)  # row tiles need neither
+    assert plan(1, 4096, 4100, 128)[0] == plan(-1, 4096, 4096, 128)[0] == plan(1, 4096, 0, 128)[0] == _lib.AWQ_ERR_SHAPE
+    assert plan(1, 4096, 4096, 100)[0] == _lib.AWQ_ERR_GROUP
+    assert plan(1, 4096, 4112, 128)[0] == plan(1, 4096, 16, 128, 1)[0] == _lib.AWQ_ERR_UNSUPPORTED
+    assert plan(1, 1 << 20, 1 << 13, 128)[0] == _lib.AWQ_ERR_UNSUPPORTED  # a weight of 4 GiB
+    assert plan(1, 1 << 20, 1 << 12, 128, 1)[0] == _lib.AWQ_ERR_UNSUPPORTED
+    assert plan(256, 1 << 23, 32 * 256, -1)[0] == _lib.AWQ_ERR_UNSUPPORTED
+
+    def call(x=base, act=0, w=base * 2, z=base * 3, s=base * 4, b=None, f=0, gated=0, r=None, M=1, K=4096, N=4096, g=128,
+             y=base * 5, ws=base * 6, wb=1 << 24, c=base * 7, cb=1 << 12):
+        v = lambda a: None if a is None else p(a)  # noqa: E731
+        return lib.awq_gemm_fused(v(x), act, v(w), v(z), v(s), v(b), f, gated, v(r), 1.0, M, K, N, g, v(y), v(ws), wb,
+                                  v(c), cb, None)
+
+    assert call(M=0) == _lib.AWQ_OK
+    assert call(N=4100) == _lib.AWQ_ERR_SHAPE
+    assert call(act=2) == call(f=5) == call(f=-1) == call(wb=0) == call(cb=0) == _lib.AWQ_ERR_UNSUPPORTED
+    assert call(x=None) == call(w=None) == call(z=None) == call(s=None) == call(y=None) == _lib.AWQ_ERR_NULL
+    assert call(ws=None) == call(c=None) == _lib.AWQ_ERR_NULL
+    assert call(x=base + 2) == call(b=base + 8) == call(r=base + 8) == call(y=base + 2) == _lib.AWQ_ERR_ALIGN
+    assert call(ws=base * 6 + 4) == call(c=base * 7 + 2) == _lib.AWQ_ERR_ALIGN
+    assert call(y=base) == call(y=base + 4096) == call(r=base * 5 + 16) == _lib.AWQ_ERR_UNSUPPORTED

@@ -449,6 +449,57 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
 
 }  // namespace
 
+int awq_gemm_fused_plan(int64_t M, int64_t K, int64_t N, int64_t group_size, int gated, int64_t* workspace_bytes,
+                        int64_t* counter_bytes) {
+  DensePlan p;
+  const int st = plan_dense(M, K, N, group_size, query_cus(), gated != 0, p);
+  if (st != AWQ_OK) return st;
+  if (workspace_bytes) *workspace_bytes = p.sums_bytes;
+  if (counter_bytes) *counter_bytes = p.counter_bytes;
+  return AWQ_OK;
+}
+
+int awq_gemm_fused(const void* x, int act, const int32_t* qweight, const int32_t* qzeros, const void* scales_f16,
+                   const void* bias, int activation, int gated, const void* residual, float scale, int64_t M,
+                   int64_t K, int64_t N, int64_t group_size, void* y, void* workspace, int64_t workspace_bytes,
+                   void* counters, int64_t counter_bytes, struct ihipStream_t* stream) {
+  DensePlan d;
+  const int st = plan_dense(M, K, N, group_size, query_cus(), gated != 0, d);
+  if (st != AWQ_OK) return st;
+  if (act != AWQ_F16 && act != AWQ_BF16) return AWQ_ERR_UNSUPPORTED;
+  if (activation < AWQ_ACT_NONE || activation > AWQ_ACT_GELU_TANH) return AWQ_ERR_UNSUPPORTED;
+  if (M == 0) return AWQ_OK;
+  if (!x || !qweight || !qzeros || !scales_f16 || !y) return AWQ_ERR_NULL;
+  if ((d.sums_bytes > 0 && !workspace) || (d.counter_bytes > 0 && !counters)) return AWQ_ERR_NULL;
+  for (const void* p : {x, (const void*)qweight, (const void*)qzeros, scales_f16, bias, residual, (const void*)y,
+                        (const void*)workspace})
+    if (!aligned16(p)) return AWQ_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(counters) % 4 != 0) return AWQ_ERR_ALIGN;
+  if (workspace_bytes < d.sums_bytes || counter_bytes < d.counter_bytes) return AWQ_ERR_UNSUPPORTED;
+  // Workgroups write y while others still read x.  The residual is read where y is written, by the
+  // same thread: y may be the residual.
+  const int64_t y_bytes = M * N * 2;
+  if (overlap(y, y_bytes, x, M * K * 2) || (y != residual && overlap(y, y_bytes, residual, y_bytes)))
+    return AWQ_ERR_UNSUPPORTED;
+  DenseProduct p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.qweight = reinterpret_cast<const uint32_t*>(qweight);
+  p.qzeros = reinterpret_cast<const uint32_t*>(qzeros);
+  p.scales = static_cast<const uint16_t*>(scales_f16);
+  p.M = (int)M;
+  p.K = (int)K;
+  p.N = (int)N;
+  p.g = eff_group(K, group_size);
+  p.gated = gated != 0;
+  p.bf16 = act == AWQ_BF16;
+  p.sums = static_cast<float*>(workspace);
+  p.counters = static_cast<uint32_t*>(counters);
+  const Epilogue e{static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(y),
+                   scale, activation};
+  const hipError_t err = d.stream ? awq::launch_fused_stream(p, e, d, stream) : awq::launch_fused_tiles(p, e, d, stream);
+  return err == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
+}
+
 int awq_add_norm(const void* x, int act, int64_t T, int64_t H, int64_t x_stride, const void* residual,
                  int residual_type, int64_t residual_stride, const void* gate, int64_t gates, float scale,
                  const void* post_weight, const void* post_bias, const void* weight, const void* bias, int kind,

@@ -97,6 +97,30 @@ struct RouteArgs {
 };
 hipError_t launch_route(RouteArgs a, hipStream_t stream);
 
+// A product's epilogue: y = residual + scale * f(v + bias), gated f(v + bias) * (u + bias of u).
+// kAct*: the values of enum awq_activation.
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
+struct Epilogue {
+  const uint16_t *bias, *residual;  // or NULL
+  uint16_t* y;
+  float scale;
+  int act;
+};
+// One dense packed weight (awq_gemm_fused): x [M, K], N output columns, gated of a 2 N wide weight.
+// sums and counters: the workspace of the streaming kernel's splits (see there).
+struct DenseProduct {
+  const uint16_t* x;
+  const uint32_t* qweight;
+  const uint32_t* qzeros;
+  const uint16_t* scales;
+  int M, K, N, g;
+  bool gated, bf16;
+  float* sums;
+  uint32_t* counters;
+};
+hipError_t launch_fused_stream(const DenseProduct& p, const Epilogue& e, const DensePlan& d, hipStream_t stream);
+hipError_t launch_fused_tiles(const DenseProduct& p, const Epilogue& e, const DensePlan& d, hipStream_t stream);
+
 // One product of routed rows with their experts' weights (awq_moe_gate_up, awq_moe_down).
 // Slot s of the S routed slots multiplies row s / row_div of x by the weight of expert
 // ids[s]: N output columns, or, gated, N pairs of columns (n, N + n) of a 2 N wide weight,
@@ -113,6 +137,7 @@ struct ExpertProduct {
   bool gated, bf16;
   uint16_t* h;
   float* sums;
+  int ldx;                 // x's row length (row tiles of one dense weight)
   const uint16_t* x_rest;  // or NULL: what x's rounding left out, a second term of the rows
   uint16_t* h_rest;        // or NULL: takes what h's rounding leaves out
 };

@@ -591,6 +591,56 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
   return AWQ_OK;
 }
 
+int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, bool gated, DensePlan& p) {
+  p = DensePlan{};
+  if (N < 1 || N > kMaxDim) return N < 1 ? AWQ_ERR_SHAPE : AWQ_ERR_UNSUPPORTED;
+  const int64_t wide = gated ? 2 * N : N;
+  const int st = limits_check(M, K, wide, group_size);
+  if (st != AWQ_OK) return st;
+  if (N % 32 != 0) return AWQ_ERR_UNSUPPORTED;                     // halves of whole 16-byte pieces
+  if (K * (wide / 2) >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into the weight
+  if (M == 0) return AWQ_OK;
+  if (cus < 1) cus = 1;
+  const int64_t tile_cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
+  const int64_t tiles_n = (N + tile_cols - 1) / tile_cols;
+  const int64_t row_tiles = (M + kExpertTileRows - 1) / kExpertTileRows * tiles_n;
+  p.stream = M <= kExpertStreamRows || 3 * row_tiles <= cus;
+  if (p.stream) {
+    if (M * K * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into x
+    ExpertPlan e;
+    p.rows = M <= 4 ? 4 : M <= 8 ? 8 : M <= 16 ? 16 : 32;
+    e.block_rows = p.rows == 32 ? 32 : 16;
+    e.col_tiles = p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
+    choose_splits(M, 1, 1, K, wide, cus, gated, e);
+    p.splits = e.splits;
+    p.steps = e.steps;
+    const int64_t tiles = (M + e.block_rows - 1) / e.block_rows * p.col_tiles;
+    p.grid = tiles * p.splits;
+    if (p.splits > 1) {
+      // Four rows of a column per thread and slot, in every half and block of 16 rows.
+      const int64_t slots = p.rows == 4 ? 1 : p.rows == 8 ? 2 : p.rows == 16 ? 4 : 8;
+      p.counter_bytes = tiles * 4;
+      p.sums_bytes = p.grid * slots * (gated ? 2 : 1) * 256 * 16;
+    }
+  } else {
+    // The height of the tiles: rounds of the card times what a tile takes (in hundredths of one of
+    // 256 rows).
+    if (int64_t(kExpertTileRows) * K * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into a tile's rows
+    const int heights[4] = {256, 192, 128, 64}, cost[4] = {100, 83, 70, 60};
+    int64_t best = -1;
+    for (int i = 0; i < 4; ++i) {
+      const int64_t tiles = (M + heights[i] - 1) / heights[i] * tiles_n;
+      const int64_t c = (tiles + cus - 1) / cus * cost[i];
+      if (best >= 0 && c >= best) continue;
+      best = c;
+      p.rows = heights[i];
+      p.grid = tiles;
+    }
+    p.col_tiles = (int)tiles_n;
+  }
+  return grid_fits(p.grid, 1, p.stream ? 256 : 512) && p.grid < (int64_t(1) << 31) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
+}
+
 int plan_rtn(int64_t K, int64_t N, int64_t group_size, int sym, RtnPlan& p) {
   p = RtnPlan{};
   const int st = format_check(K, N, group_size);

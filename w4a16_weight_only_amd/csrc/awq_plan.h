@@ -240,6 +240,21 @@ struct ExpertsPlan {
   int64_t sorted_bytes = 0, h_bytes = 0, sums_bytes = 0;
   int64_t workspace_bytes() const { return sorted_bytes + h_bytes + sums_bytes; }
 };
+// A dense product with its epilogue (awq_gemm_fused).
+//   stream   up to `rows` (4, 8, 16, 32) rows and 256 columns per workgroup, `steps` k-steps per
+//            wave, `splits` K splits that meet over the workspace
+//   else     row tiles of up to `rows` (64, 128, 192, 256) rows
+struct DensePlan {
+  bool stream = false;
+  int rows = 0;
+  int col_tiles = 0;
+  int splits = 1, steps = 0;
+  int64_t grid = 0;           // workgroups
+  int64_t counter_bytes = 0;  // zero between calls: one 32-bit count per row block and column tile
+  int64_t sums_bytes = 0;     // fp32 sums of all splits
+};
+int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, bool gated, DensePlan& p);
+
 // K -> I gated (up) and inner -> N (down) products.
 int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
                  int cus, bool up, bool down, ExpertsPlan& p);

@@ -1,0 +1,113 @@
+"""Dense products with their epilogue: torch tensors in, C ABI calls out.
+
+Work runs on the current stream of the tensors' device.  Where K is split, a call needs scratch
+memory, which comes from torch's allocator on that stream, and counters that are zero between
+calls: one zeroed tensor per stream, kept; under capture one of the graph's own, which the graph
+clears itself, so that graphs share none and need no call before.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from .linear import _check_tensor, validate
+from .moe import _TYPES, _call, _is, _output
+
+_ACTIVATIONS = {None: _lib.AWQ_ACT_NONE, "relu": _lib.AWQ_ACT_RELU, "silu": _lib.AWQ_ACT_SILU,
+                "gelu": _lib.AWQ_ACT_GELU, "gelu_tanh": _lib.AWQ_ACT_GELU_TANH}
+
+_plans = {}  # (workspace, counter) bytes by device and the call's sizes
+_counters = {}  # zeroed tensors by device and stream
+
+
+def _plan(device, *sizes):
+    key = (device.index, sizes)
+    need = _plans.get(key)
+    if need is None:
+        ws, count = ctypes.c_int64(), ctypes.c_int64()
+        with torch.cuda.device(device):
+            status = _lib.load().awq_gemm_fused_plan(*sizes, ctypes.byref(ws), ctypes.byref(count))
+        _lib.check(status, "awq_gemm_fused_plan")
+        if len(_plans) >= 4096:
+            _plans.clear()
+        _plans[key] = need = (ws.value, count.value)
+    return need
+
+
+def zeroed_counters(device, nbytes):
+    """Device memory of at least nbytes, zero when this stream's next kernel runs, for kernels that
+    leave it zero."""
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(nbytes // 4, dtype=torch.int32, device=device)
+        key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
+        got = _counters.get(key)
+        if got is None or got.numel() * 4 < nbytes:
+            _counters[key] = got = torch.zeros(max(nbytes // 4, 4096), dtype=torch.int32, device=device)
+        return got
+
+
+def awq_gemm_fused(x: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor, scales: torch.Tensor,
+                   bias: torch.Tensor | None = None, group_size: int = 128, *, activation: str | None = None,
+                   gated: bool = False, residual: torch.Tensor | None = None, scale: float = 1.0,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """A product with its epilogue, in x's type (fp16 or bfloat16), rounded once:
+
+        y = residual + scale * f(x . dequant(W) + bias)
+
+    f: None (the value itself), "relu", "silu", "gelu" or "gelu_tanh".  gated: the weight (and bias)
+    holds the gate's columns, then as many of the up projection's, and f(gate) * up stands in f's
+    place.  x may have leading dimensions, as for awq_gemm; residual has y's shape, and out may be
+    residual itself."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dtype, dev = x.dtype, x.device
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"x must be float16 or bfloat16, got {dtype}")
+    if dev.type != "cuda" or not x.is_contiguous():
+        _check_tensor("x", x, dtype)
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None, 'relu', 'silu', 'gelu' or 'gelu_tanh', got {activation!r}")
+    if not (_is(qweight, torch.int32, dev) and _is(qzeros, torch.int32, dev) and _is(scales, torch.float16, dev)):
+        _check_tensor("qweight", qweight, torch.int32, dev)
+        _check_tensor("qzeros", qzeros, torch.int32, dev)
+        _check_tensor("scales", scales, torch.float16, dev)
+    if x.dim() < 1 or qweight.dim() != 2 or qzeros.dim() != 2 or scales.dim() != 2:
+        raise ValueError("x must have rows; qweight, qzeros and scales must be 2-D")
+    K, words = qweight.shape
+    C = 8 * words
+    lead = x.shape[:-1]
+    if x.shape[-1] != K:
+        raise ValueError(f"x has {x.shape[-1]} input features, qweight has {K}")
+    G = 1 if group_size == -1 else K // group_size if group_size > 0 else 0
+    if K < 1 or qzeros.shape != (G, words) or scales.shape != (G, C):
+        validate(K, C, group_size, qweight, qzeros, scales)
+    N = C
+    if gated:
+        if C % 16 != 0:
+            raise ValueError("gated: the columns must be two equal halves of whole words")
+        N = C // 2
+    if bias is not None:
+        if not _is(bias, dtype, dev):
+            _check_tensor("bias", bias, dtype, dev)
+        if bias.shape != (C,):
+            raise ValueError(f"bias must be [{C}]")
+    shape = lead + (N,)
+    if residual is not None:
+        if not _is(residual, dtype, dev):
+            _check_tensor("residual", residual, dtype, dev)
+        if residual.shape != shape:
+            raise ValueError(f"residual must be {list(shape)}")
+    M = x.numel() // K
+    out = _output(out, shape, dtype, dev)
+    ws_bytes, count_bytes = _plan(dev, M, K, N, group_size, 1 if gated else 0)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    counters = zeroed_counters(dev, count_bytes) if count_bytes else None
+    _call(_lib.load().awq_gemm_fused, "awq_gemm_fused", dev, x.data_ptr(), _TYPES[dtype], qweight.data_ptr(),
+          qzeros.data_ptr(), scales.data_ptr(), None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation],
+          1 if gated else 0, None if residual is None else residual.data_ptr(), scale, M, K, N, group_size,
+          out.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes,
+          None if counters is None else counters.data_ptr(), count_bytes)
+    return out
