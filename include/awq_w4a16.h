@@ -363,6 +363,38 @@ int awq_moe_mlp(const void* x, int act, const int32_t* up_qweight, const int32_t
                 struct ihipStream_t* stream);
 
 /*
+ * A whole routed layer for a few tokens (T * topk <= 64), in two launches:
+ *   logits = x . router^T in fp32;  weights, ids = awq_moe_route of them
+ *   y[t] = residual[t] + sum over j of weights[t, j] * (h[s] . down[e]),
+ *   h[s] = silu(x[t] . gate[e]) * (x[t] . up[e]),  e = ids[t, j]
+ *   act, weights   as for awq_moe_mlp (gate_up weight K -> 2 inner, down weight inner -> N)
+ *   router         device [E, K] of router_type: act, or AWQ_F32
+ *   round_logits   nonzero: the logits are rounded to act before they are compared
+ *   bias ... scale as for awq_moe_route (topk of E experts, groups, renormalize, scale of the weights)
+ *   residual       device [T, N] of act, or NULL
+ *   y              device [T, N].  It may be residual itself, and may overlap x
+ *   workspace      as for awq_moe_mlp, awq_moe_layer_workspace bytes
+ *   counters       device memory of AWQ_MOE_LAYER_COUNTERS bytes, zero before the call and zero again
+ *                  after it, for this call alone until then.  (Calls in one stream's order may
+ *                  share it.)
+ * h is not rounded on the way (two terms, as for awq_moe_mlp): y is rounded once.  A token whose
+ * logits hold a NaN (for the softmax, or +inf) comes out as NaN, one without experts as its residual.
+ * The result is deterministic.  The second launch's workgroups wait for each other's parts of h;
+ * they need not all be resident, and calls may run side by side.
+ * Limits: those of awq_moe_route and awq_moe_mlp.  T == 0 enqueues nothing.
+ */
+enum { AWQ_MOE_LAYER_COUNTERS = 256 };
+int64_t awq_moe_layer_workspace(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
+                                int64_t group_size);
+int awq_moe_layer(const void* x, int act, const void* router, int router_type, int round_logits, const float* bias,
+                  int score, int64_t groups, int64_t topk_groups, int group_top, int64_t topk, int renormalize,
+                  float scale, const int32_t* up_qweight, const int32_t* up_qzeros, const void* up_scales_f16,
+                  const int32_t* down_qweight, const int32_t* down_qzeros, const void* down_scales_f16,
+                  const void* residual, int64_t T, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
+                  void* y, void* workspace, int64_t workspace_bytes, void* counters, int64_t counter_bytes,
+                  struct ihipStream_t* stream);
+
+/*
  * A dense product with its epilogue:
  *   y[m, n] = residual[m, n] + scale * f(x[m] . W[:, n] + bias[n])
  * or, gated, of a weight with the gate's N columns first, then the up projection's:

@@ -324,3 +324,30 @@ def test_fused_argument_errors_touch_no_device(lib):
     assert call(x=base + 2) == call(b=base + 8) == call(r=base + 8) == call(y=base + 2) == _lib.AWQ_ERR_ALIGN
     assert call(ws=base * 6 + 4) == call(c=base * 7 + 2) == _lib.AWQ_ERR_ALIGN
     assert call(y=base) == call(y=base + 4096) == call(r=base * 5 + 16) == _lib.AWQ_ERR_UNSUPPORTED
+
+
+def test_layer_argument_errors_touch_no_device(lib):
+    """awq_moe_layer checks sizes, types, pointers, workspace and overlaps before any HIP call."""
+    base = 1 << 24
+    p = ctypes.c_void_p
+    need = lib.awq_moe_layer_workspace(2, 8, 64, 2048, 1408, 2048, 128)
+    assert need > 2 * 64 * 4 + 2 * 16 * 1408 * 2
+    assert lib.awq_moe_layer_workspace(9, 8, 64, 2048, 1408, 2048, 128) == _lib.AWQ_ERR_UNSUPPORTED  # 72 slots
+    assert lib.awq_moe_layer_workspace(2, 8, 64, 2048, 1416, 2048, 8) == _lib.AWQ_ERR_UNSUPPORTED
+    assert lib.awq_moe_layer_workspace(2, 8, 64, 2048, 1408, 2048, 100) == _lib.AWQ_ERR_GROUP
+    assert lib.awq_moe_layer_workspace(0, 8, 64, 2048, 1408, 2048, 128) == 0
+
+    def call(x=base, act=0, router=base * 2, rt=2, bias=None, score=0, groups=1, tg=1, gt=1, topk=8, w=base * 3,
+             res=None, T=2, E=64, K=2048, g=128, y=base * 4, ws=base * 5, wb=need, c=base * 6, cb=256):
+        v = lambda a: None if a is None else p(a)  # noqa: E731
+        return lib.awq_moe_layer(v(x), act, v(router), rt, 0, v(bias), score, groups, tg, gt, topk, 1, 1.0, v(w), v(w),
+                                 v(w), v(w), v(w), v(w), v(res), T, E, K, 1408, 2048, g, v(y), v(ws), wb, v(c), cb, None)
+
+    assert call(T=0) == _lib.AWQ_OK
+    assert call(topk=65, E=80) == call(T=9) == call(E=1025) == _lib.AWQ_ERR_UNSUPPORTED
+    assert call(groups=3) == call(topk=0) == call(tg=2) == call(topk=65) == _lib.AWQ_ERR_SHAPE
+    assert call(act=2) == call(act=0, rt=1) == call(score=2) == call(wb=need - 1) == call(cb=0) == _lib.AWQ_ERR_UNSUPPORTED
+    assert call(x=None) == call(router=None) == call(w=None) == call(y=None) == call(ws=None) == call(c=None) == _lib.AWQ_ERR_NULL
+    assert call(x=base + 2) == call(router=base * 2 + 8) == call(w=base * 3 + 4) == call(res=base * 7 + 8) == _lib.AWQ_ERR_ALIGN
+    assert call(y=base * 4 + 2) == call(ws=base * 5 + 4) == call(c=base * 6 + 2) == call(bias=base * 7 + 2) == _lib.AWQ_ERR_ALIGN
+    assert call(res=base * 4 + 16) == _lib.AWQ_ERR_UNSUPPORTED

@@ -8,7 +8,7 @@ from ._lib import (  # noqa: F401
     AWQ_ERR_HIP, AwqError, LIB_PATH, load as load_library, status_string,
 )
 from .moe import (  # noqa: F401
-    AwqMoe, awq_moe_down, awq_moe_gate_up, awq_moe_mlp, awq_moe_route,
+    AwqMoe, awq_moe_down, awq_moe_gate_up, awq_moe_layer, awq_moe_mlp, awq_moe_route,
 )
 from .fused import awq_gemm_fused  # noqa: F401
 from .norm import awq_add_norm, awq_norm  # noqa: F401

@@ -22,6 +22,7 @@ AWQ_ERR_HIP = -6
 AWQ_F16, AWQ_BF16, AWQ_F32 = 0, 1, 2  # enum awq_type
 AWQ_NAN_WEIGHTS = 256
 AWQ_SOFTMAX, AWQ_SIGMOID = 0, 1  # enum awq_score
+AWQ_MOE_LAYER_COUNTERS = 256
 AWQ_RMS, AWQ_LAYER = 0, 1  # enum awq_norm_kind
 AWQ_ACT_NONE, AWQ_ACT_RELU, AWQ_ACT_SILU, AWQ_ACT_GELU, AWQ_ACT_GELU_TANH = range(5)  # enum awq_activation
 
@@ -46,6 +47,10 @@ SIGNATURES = {
     "awq_moe_gate_up": (ctypes.c_int, [_vp, ctypes.c_int] + [_vp] * 4 + [_i64] * 6 + [_vp, _vp, _i64, _vp]),
     "awq_moe_down": (ctypes.c_int, [_vp, ctypes.c_int] + [_vp] * 5 + [_i64] * 6 + [_vp, _vp, _i64, _vp]),
     "awq_moe_mlp": (ctypes.c_int, [_vp, ctypes.c_int] + [_vp] * 8 + [_i64] * 7 + [_vp, _vp, _i64, _vp]),
+    "awq_moe_layer_workspace": (ctypes.c_int64, [_i64] * 7),
+    "awq_moe_layer": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, ctypes.c_int, _vp, ctypes.c_int, _i64, _i64,
+                                     ctypes.c_int, _i64, ctypes.c_int, ctypes.c_float] + [_vp] * 7 + [_i64] * 6 +
+                      [_vp, _vp, _i64, _vp, _i64, _vp]),
     "awq_gemm_fused_plan": (ctypes.c_int, [_i64] * 4 + [ctypes.c_int, ctypes.POINTER(ctypes.c_int64),
                                                         ctypes.POINTER(ctypes.c_int64)]),
     "awq_gemm_fused": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_int, ctypes.c_int, _vp,

@@ -664,6 +664,97 @@ int experts_common(const void* x, int act, const Packed* up, const Packed* down,
 
 }  // namespace
 
+int64_t awq_moe_layer_workspace(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N,
+                                int64_t group_size) {
+  LayerPlan p;
+  const int st = plan_layer(T, topk, E, K, inner, N, group_size, query_cus(), p);
+  return st == AWQ_OK ? p.workspace_bytes() : st;
+}
+
+int awq_moe_layer(const void* x, int act, const void* router, int router_type, int round_logits, const float* bias,
+                  int score, int64_t groups, int64_t topk_groups, int group_top, int64_t topk, int renormalize,
+                  float scale, const int32_t* up_qweight, const int32_t* up_qzeros, const void* up_scales_f16,
+                  const int32_t* down_qweight, const int32_t* down_qzeros, const void* down_scales_f16,
+                  const void* residual, int64_t T, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
+                  void* y, void* workspace, int64_t workspace_bytes, void* counters, int64_t counter_bytes,
+                  struct ihipStream_t* stream) {
+  int st = plan_route(T, E, E, groups, topk_groups, group_top, topk);
+  if (st != AWQ_OK) return st;
+  LayerPlan p;
+  st = plan_layer(T, topk, E, K, inner, N, group_size, query_cus(), p);
+  if (st != AWQ_OK) return st;
+  if (act != AWQ_F16 && act != AWQ_BF16) return AWQ_ERR_UNSUPPORTED;
+  if (router_type != act && router_type != AWQ_F32) return AWQ_ERR_UNSUPPORTED;
+  if (score != AWQ_SOFTMAX && score != AWQ_SIGMOID) return AWQ_ERR_UNSUPPORTED;
+  if (T == 0) return AWQ_OK;
+  if (!x || !router || !y || !workspace || !counters) return AWQ_ERR_NULL;
+  const Packed up{up_qweight, up_qzeros, up_scales_f16}, down{down_qweight, down_qzeros, down_scales_f16};
+  for (const Packed* w : {&up, &down})
+    if ((st = w->check()) != AWQ_OK) return st;
+  if (!aligned16(x) || !aligned16(router) || !aligned16(y) || !aligned16(residual) || !aligned16(workspace))
+    return AWQ_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(bias) % 4 != 0 || reinterpret_cast<uintptr_t>(counters) % 4 != 0) return AWQ_ERR_ALIGN;
+  if (workspace_bytes < p.workspace_bytes() || counter_bytes < AWQ_MOE_LAYER_COUNTERS) return AWQ_ERR_UNSUPPORTED;
+  // Nobody reads x any more when y is written; the residual is read where y is, by the same thread.
+  if (y != residual && overlap(y, T * N * 2, residual, T * N * 2)) return AWQ_ERR_UNSUPPORTED;
+  LayerArgs a;
+  char* ws = static_cast<char*>(workspace);
+  auto part = [&](int64_t bytes) {
+    char* at = ws;
+    ws += bytes;
+    return static_cast<void*>(at);
+  };
+  a.counts = static_cast<uint32_t*>(part(p.counts_bytes));
+  a.logits = static_cast<float*>(part(p.logits_bytes));
+  a.ids = static_cast<int32_t*>(part(p.ids_bytes));
+  a.weights = static_cast<float*>(part(p.ids_bytes));
+  a.h = static_cast<uint16_t*>(part(p.h_bytes));
+  a.up_sums = static_cast<float*>(part(p.up_bytes));
+  a.down_sums = static_cast<float*>(part(p.down_bytes));
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.router = router;
+  a.y = static_cast<uint16_t*>(y);
+  a.up_qweight = reinterpret_cast<const uint32_t*>(up_qweight);
+  a.up_qzeros = reinterpret_cast<const uint32_t*>(up_qzeros);
+  a.up_scales = static_cast<const uint16_t*>(up_scales_f16);
+  a.down_qweight = reinterpret_cast<const uint32_t*>(down_qweight);
+  a.down_qzeros = reinterpret_cast<const uint32_t*>(down_qzeros);
+  a.down_scales = static_cast<const uint16_t*>(down_scales_f16);
+  a.arrivals = static_cast<uint32_t*>(counters);
+  a.n_counts = p.n_counts;
+  a.T = (int)T;
+  a.topk = (int)topk;
+  a.E = (int)E;
+  a.K = (int)K;
+  a.inner = (int)inner;
+  a.N = (int)N;
+  a.g_up = eff_group(K, group_size);
+  a.g_down = eff_group(inner, group_size);
+  a.router_waves = p.router_waves;
+  a.up_tiles = p.up_tiles;
+  a.up_splits = p.up_splits;
+  a.up_steps = p.up_steps;
+  a.down_tiles = p.down_tiles;
+  a.down_splits = p.down_splits;
+  a.down_steps = p.down_steps;
+  a.bf16 = act == AWQ_BF16;
+  a.router32 = router_type == AWQ_F32;
+  a.round_logits = round_logits != 0;
+  RouteArgs r{};
+  r.bias = bias;
+  r.T = T;
+  r.E = (int)E;
+  r.topk = (int)topk;
+  r.groups = (int)groups;
+  r.topk_groups = (int)topk_groups;
+  r.group_top = group_top;
+  r.softmax = score == AWQ_SOFTMAX;
+  r.renormalize = renormalize != 0;
+  r.scale = scale;
+  return awq::launch_layer(a, r, p, stream) == hipSuccess ? AWQ_OK : AWQ_ERR_HIP;
+}
+
 int awq_moe_gate_up(const void* x, int act, const int32_t* qweight, const int32_t* qzeros, const void* scales_f16,
                     const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner,
                     int64_t group_size, void* h, void* workspace, int64_t workspace_bytes,

@@ -50,7 +50,8 @@ __global__ __launch_bounds__(kThreads, 2) void expert_stream_kernel(const Expert
   const int q = lane >> 4, c = lane & 15;
   Entry en;
   if (table == nullptr) {
-    en = rank_entry<16 * RB>(p.ids, p.S, p.E, entry, lane, slots);
+    const int id = lane < p.S ? p.ids[lane] : -1;
+    en = entry_of<16 * RB>(rank_slots<16 * RB>(id, p.E), id, entry, lane, slots);
   } else {
     en.expert = table[4 * entry];
     en.rows = en.expert < 0 ? 0 : table[4 * entry + 2];

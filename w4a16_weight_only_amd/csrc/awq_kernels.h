@@ -158,6 +158,29 @@ hipError_t launch_expert_gate(const float* sums, const int32_t* ids, int S, int 
 hipError_t launch_expert_combine(const float* sums, const int32_t* ids, const float* weights, int T, int topk, int E,
                                  int N, int splits, bool bf16, bool nan_weights, uint16_t* y, hipStream_t stream);
 
+// A whole routed layer for few tokens (awq_moe_layer).  logits, ids and weights, h (two terms
+// [S, inner]), up_sums, down_sums and counts are parts of the workspace; counts are zeroed by the
+// first kernel, arrivals (a count per kLayerTokens tokens) are zero between calls.
+struct LayerArgs {
+  const uint16_t *x, *residual;
+  const void* router;
+  uint16_t* y;
+  const uint32_t *up_qweight, *up_qzeros, *down_qweight, *down_qzeros;
+  const uint16_t *up_scales, *down_scales;
+  float* logits;
+  int32_t* ids;
+  float* weights;
+  uint16_t* h;
+  float *up_sums, *down_sums;
+  uint32_t *counts, *arrivals;
+  int64_t n_counts;
+  int T, topk, E, K, inner, N, g_up, g_down;
+  int router_waves;  // waves per expert of the first kernel: 1 or 4
+  int up_tiles, up_splits, up_steps, down_tiles, down_splits, down_steps;
+  bool bf16, router32, round_logits;
+};
+hipError_t launch_layer(const LayerArgs& a, RouteArgs r, const LayerPlan& p, hipStream_t stream);
+
 // Norms on the residual stream (awq_add_norm).  x, gate, weights, biases and y are fp16 or (bf16)
 // bfloat16; residual and r too, or (r32) fp32.  Strides in elements; gate row t / gate_rows.
 struct NormArgs {

@@ -1,0 +1,444 @@
+// A whole routed layer for few tokens (at most 64 slots), in two kernels:
+//   y[t] = residual[t] + sum over j of weights[t, j] * down[e](silu(gate[e](x[t])) * up[e](x[t])),
+//   e and weights of slot (t, j) from the logits x . router^T
+//
+// layer_router_kernel: a wave per expert (four for few experts) forms the logits of eight tokens; the
+// workgroup that finishes last routes those tokens, a wave per token (awq_route.h).
+//
+// layer_kernel: both products, streamed (awq_stream.h) in items of (up to 16 slots of one expert, 256
+// columns, K split).  Workgroups take the items of the gated product first, then those of the
+// second, by tickets.  h is two terms, rounded and what that leaves out, as in awq_moe_mlp.
+//   - Splits of a gated tile meet in the workspace; the last to arrive adds them in order and writes h.
+//   - An item of the second product waits until h of its slots is whole, with its first weights already
+//     on their way.
+//   - The last item of a column tile of the second product adds the slots and splits of every token in a fixed
+//     order, and the residual, and writes y.
+// What workgroups hand to each other goes through to, and comes from, where every XCD's L2 sees the
+// same (kCpolDevice), and is counted in after it is complete.
+//
+// Every wait ends, whatever else runs on the card and however many workgroups are resident: a ticket
+// is taken by a workgroup that runs, a gated item waits for nothing, and a workgroup takes an item of
+// the second product only after it has seen that all gated items are taken.  So does a bound on the
+// polls, behind which y is NaN.  Tickets are eight lists, one per XCD as blocks go round them (one
+// list: 18 ns for each workgroup in turn); who finds his own empty takes from the others.
+#include "awq_route.h"
+#include "awq_stream.h"
+
+namespace awq {
+
+using namespace stream;
+
+namespace {
+
+constexpr uint32_t kMaxPolls = 1u << 18;  // a fifth of a second or more
+
+__device__ __forceinline__ uint32_t load_count(const uint32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t count_in(uint32_t* p) {
+  return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Stores of this wave are complete where every XCD sees them.
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <bool BF16, bool R32>
+__device__ __forceinline__ void dots(const LayerArgs& a, int e, int t0, int first, int step, float (&acc)[kLayerTokens]) {
+  const char* row = static_cast<const char*>(a.router) + (int64_t)e * a.K * (R32 ? 4 : 2);
+  const int nt = min(a.T - t0, kLayerTokens);
+#pragma unroll 2
+  for (int k = first; k < a.K; k += step) {
+    float w[8];
+    if constexpr (R32) {
+      const floatx4* p = reinterpret_cast<const floatx4*>(row + 4 * (int64_t)k);
+      const floatx4 lo = p[0], hi = p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = lo[i], w[4 + i] = hi[i];
+    } else {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(row + 2 * (int64_t)k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = act_to_float<BF16>((uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+    }
+#pragma unroll
+    for (int t = 0; t < kLayerTokens; ++t) {
+      if (t < nt) {  // the same in every lane
+        const u32x4 v = *reinterpret_cast<const u32x4*>(a.x + (int64_t)(t0 + t) * a.K + k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[t] = fmaf(act_to_float<BF16>((uint16_t)(v[i >> 1] >> (16 * (i & 1)))), w[i], acc[t]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+template <typename Key, typename Worth, int VPL, bool GROUPS>
+__global__ __launch_bounds__(256) void layer_router_kernel(const LayerArgs a, const RouteArgs r) {
+  constexpr float kInf = __builtin_inff();
+  __shared__ union {
+    float part[4][kLayerTokens];
+    struct {
+      float l[64 * VPL];
+      route::Scratch<Worth, 64, VPL, GROUPS> scratch;
+    } of[4];
+  } sh;
+  __shared__ uint32_t last_arrival;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int t0 = blockIdx.y * kLayerTokens;
+  const int nt = min(a.T - t0, kLayerTokens);
+  // The other kernel's counts.
+  for (int64_t i = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 256 + tid; i < a.n_counts;
+       i += (int64_t)gridDim.x * gridDim.y * 256)
+    a.counts[i] = 0;
+
+  const int per = 4 / a.router_waves;  // experts of a workgroup
+  const int e = blockIdx.x * per + wave / a.router_waves, part = wave % a.router_waves;
+  const int el = min(e, a.E - 1);
+  float acc[kLayerTokens];
+#pragma unroll
+  for (int t = 0; t < kLayerTokens; ++t) acc[t] = 0.f;
+  const int first = 8 * (part * 64 + lane), step = 512 * a.router_waves;
+  if (a.bf16) a.router32 ? dots<true, true>(a, el, t0, first, step, acc) : dots<true, false>(a, el, t0, first, step, acc);
+  else a.router32 ? dots<false, true>(a, el, t0, first, step, acc) : dots<false, false>(a, el, t0, first, step, acc);
+#pragma unroll
+  for (int t = 0; t < kLayerTokens; ++t) acc[t] = lanes_sum<64>(acc[t]);
+  if (lane == 0) {
+#pragma unroll
+    for (int t = 0; t < kLayerTokens; ++t) sh.part[wave][t] = acc[t];
+  }
+  __syncthreads();
+  if (part == 0 && lane < nt && e < a.E) {
+    float v = sh.part[wave][lane];
+    for (int w = 1; w < a.router_waves; ++w) v += sh.part[wave + w][lane];
+    if (a.round_logits) v = a.bf16 ? act_to_float<true>(float_to_act<true>(v)) : act_to_float<false>(float_to_act<false>(v));
+    __hip_atomic_store(a.logits + (int64_t)(t0 + lane) * a.E + e, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  stores_done();
+  __syncthreads();
+  if (tid == 0) {
+    const bool last = count_in(a.arrivals + blockIdx.y) == gridDim.x - 1;
+    if (last) __hip_atomic_store(a.arrivals + blockIdx.y, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last_arrival = last;
+  }
+  __syncthreads();
+  if (!last_arrival) return;
+
+  // The LDS accesses of a wave are its own and in order; the compiler keeps them so.
+  auto sync = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+  for (int i = wave; i < nt; i += 4) {
+    const int t = t0 + i;
+    float l[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int f = lane * VPL + j;
+      const float v = __hip_atomic_load(a.logits + (int64_t)t * a.E + min(f, a.E - 1), __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
+      l[j] = f < a.E ? v : -kInf;
+    }
+    sync();
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) sh.of[wave].l[lane * VPL + j] = l[j];
+    sync();
+    route::route_tokens<Key, Worth, 64, VPL, GROUPS>(
+        r, l, [&](int f) { return sh.of[wave].l[f]; }, sync, sh.of[wave].scratch, true, [&](int j, int id, float weight) {
+          a.ids[t * a.topk + j] = id;
+          a.weights[t * a.topk + j] = weight;
+        });
+  }
+}
+
+// RL: lanes whose rows are kept, 16 per four rows; no expert has more than RL / 4 slots.. (16: any).
+template <bool BF16, int RL>
+__global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
+  constexpr int SLOTS = 16 * RL / kThreads;
+  constexpr int kEntryRows = 16;
+  __shared__ union {
+    floatx4 red[kWaves][16][RL];
+    float ys[RL / 4][2][kYld];
+  } sh;
+  __shared__ int32_t slots[kEntryRows], ids[kExpertRankSlots];
+  __shared__ float weights[kExpertRankSlots];
+  __shared__ int taken;
+  __shared__ uint32_t last_arrival;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, c = lane & 15;
+  const int S = a.T * a.topk;
+
+  // Slots by expert, one per lane, in every wave: blocks of 16 slots of one expert are entries.
+  const int id = lane < S ? a.ids[lane] : -1;
+  if (wave == 0) {
+    ids[lane] = id;
+    weights[lane] = lane < S ? a.weights[lane] : 0.f;
+  }
+  const Ranks ranks = rank_slots<kEntryRows>(id, a.E);
+  const int entries = ranks.entries;
+  const int up_items = entries * a.up_tiles * a.up_splits, down_items = entries * a.down_tiles * a.down_splits;
+  __syncthreads();
+
+  // y of a column tile: every token's slots and splits, in order.  P threads share four columns.
+  auto combine = [&](int tile) {
+    const int P = a.T == 1 ? 4 : a.T == 2 ? 2 : 1;
+    const int part = tid & (P - 1), terms = entries > 0 ? a.topk * a.down_splits : 0;
+    const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
+        a.down_sums, (short)0, (int)((uint32_t)a.down_splits * (uint32_t)S * (uint32_t)a.N * 4u), 0x00020000);
+    for (int i = tid / P; i < a.T * (kExpertStreamCols / 4); i += kThreads / P) {
+      const int t = i / (kExpertStreamCols / 4);
+      const int n = tile * kExpertStreamCols + 4 * (i % (kExpertStreamCols / 4));
+      const bool live = n < a.N;
+      floatx4 sum = {0.f, 0.f, 0.f, 0.f};
+      // Eight terms' loads at a time, routed or not (what no one wrote is dropped).
+      for (int i0 = part; i0 < terms; i0 += 8 * P) {
+        floatx4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int term = min(i0 + u * P, terms - 1);
+          const int j = term / a.down_splits, sp = term - j * a.down_splits;
+          const uint32_t at = ((uint32_t)(sp * S + t * a.topk + j) * (uint32_t)a.N + (uint32_t)(live ? n : 0)) * 4u;
+          v[u] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(srs, at, 0, kCpolDevice));
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int term = i0 + u * P;
+          const int s = t * a.topk + min(term, terms - 1) / a.down_splits;
+          if (term < terms && ids[s] >= 0) sum += weights[s] * v[u];
+        }
+      }
+      for (int m = 1; m < P; m *= 2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], m);
+      // A token without scores has NaN weights and no experts.
+      const float lost = weights[t * a.topk] != weights[t * a.topk] ? weights[t * a.topk] : 0.f;
+      if (part != 0 || !live) continue;
+      const int64_t at = (int64_t)t * a.N + n;
+      if (a.residual != nullptr) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(a.residual + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += act_to_float<BF16>((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
+      }
+      *reinterpret_cast<u32x2*>(a.y + at) = u32x2{pack_act2<BF16>(sum[0] + lost, sum[1] + lost),
+                                                  pack_act2<BF16>(sum[2] + lost, sum[3] + lost)};
+    }
+  };
+  if (entries == 0) {  // nobody goes anywhere
+    for (int tile = blockIdx.x; tile < a.down_tiles; tile += gridDim.x) combine(tile);
+    return;
+  }
+
+  // The next item of a list, or -1 when all of it is taken.  Item i is in list i % 8.
+  auto take = [&](uint32_t* tickets, int total) {
+    if (wave == 0) {
+      const int home = blockIdx.x & 7;
+      int got = -1, list = home;
+      for (;;) {
+        const int n = (total - list + 7) >> 3;  // items of this list
+        uint32_t v = 0;
+        if (lane == 0 && n > 0) v = count_in(tickets + kLayerStride * list);
+        v = __builtin_amdgcn_readfirstlane(v);
+        if (n > 0 && v < (uint32_t)n) {
+          got = (int)v * 8 + list;
+          break;
+        }
+        const uint32_t seen = lane < 8 ? load_count(tickets + kLayerStride * lane) : 0u;
+        const uint64_t left = __ballot(lane < 8 && (int64_t)seen < (int64_t)((total - lane + 7) >> 3));
+        if (left == 0) break;
+        // The next list after one's own that has something left.
+        const uint32_t turned = (uint32_t)((left | left << 8) >> home) & 0xFFu;
+        list = (home + __builtin_ctz(turned)) & 7;
+      }
+      if (lane == 0) taken = got;
+    }
+    __syncthreads();
+    const int got = taken;
+    __syncthreads();  // before it is written again, and before the LDS of the last item is
+    return got;
+  };
+  // Last of n arrivals at a count (the same answer in every thread); the workgroup's stores precede.
+  auto last_of = [&](uint32_t* count, int n) {
+    stores_done();
+    __syncthreads();
+    if (tid == 0) last_arrival = count_in(count) == (uint32_t)n - 1u;
+    __syncthreads();
+    return last_arrival != 0;
+  };
+  uint32_t* const up_tickets = a.counts;
+  uint32_t* const down_tickets = up_tickets + 8 * kLayerStride;
+  uint32_t* const ready = down_tickets + 8 * kLayerStride;
+  uint32_t* const down_counts = ready + kExpertRankSlots * kLayerStride;
+  uint32_t* const up_counts = down_counts + a.down_tiles;
+  const __amdgpu_buffer_rsrc_t hrs = __builtin_amdgcn_make_buffer_rsrc(
+      a.h, (short)0, (int)(2u * (uint32_t)S * (uint32_t)a.inner * 2u), 0x00020000);
+  const uint32_t rest_at = (uint32_t)S * (uint32_t)a.inner * 2u;  // the second term's bytes
+
+  // ---- The gated product.
+  for (;;) {
+    const int item = take(up_tickets, up_items);
+    if (item < 0) break;
+    const int split = item % a.up_splits, tile = item / a.up_splits % a.up_tiles;
+    const int entry = item / a.up_splits / a.up_tiles;
+    const Entry en = entry_of<kEntryRows>(ranks, id, entry, lane, slots);
+    __syncthreads();
+    const int K = a.K, N = a.inner, half = wave & 1, NW = N >> 2, G = K / a.g_up;
+    const int wc_in = tile * (kExpertStreamCols / 8) + 2 * c;
+    const int wc = (wc_in < (N >> 3) ? wc_in : tile * (kExpertStreamCols / 8)) + half * (N >> 3);
+    Share<1> share{a.up_qweight + (int64_t)en.expert * K * NW, a.up_qzeros + (int64_t)en.expert * G * NW,
+                   a.up_scales + (int64_t)en.expert * G * NW * 8, NW, K, a.g_up, wc, a.x, nullptr, {}, 0, 0};
+    share.x_off[0] = ((uint32_t)(slots[c < en.rows ? c : 0] / a.topk) * (uint32_t)K + 8u * q) * 2u;
+    share.kb = min(K / 32, (split * kParts<true> + (wave >> 1)) * a.up_steps);
+    share.ke = min(K / 32, share.kb + a.up_steps);
+    floatx4 part[1][16];
+    half8v unit[2];
+    stream_sums<BF16, 1, false>(share, Now{}, part, unit);
+    floatx4 sum[SLOTS][2];
+    wave_sums<true, RL>(sh.red, part[0], unit, sum);
+    if (a.up_splits > 1) {
+      constexpr uint32_t kShare = 2u * SLOTS * kThreads * 16u;
+      const int64_t tile_at = (int64_t)entry * a.up_tiles + tile;
+      const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
+          a.up_sums + tile_at * a.up_splits * (kShare / 4), (short)0, (int)(kShare * (uint32_t)a.up_splits), 0x00020000);
+      auto at = [&](int sp, int k, int hf) { return (uint32_t)sp * kShare + (uint32_t)((2 * k + hf) * kThreads + tid) * 16u; };
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[k][hf]), prs, at(split, k, hf), 0, kCpolDevice);
+      if (!last_of(up_counts + tile_at, a.up_splits)) continue;
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          sum[k][hf] = floatx4{0.f, 0.f, 0.f, 0.f};
+          for (int s0 = 0; s0 < a.up_splits; s0 += 8) {
+            floatx4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              v[j] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     prs, at(min(s0 + j, a.up_splits - 1), k, hf), 0, kCpolDevice));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (s0 + j < a.up_splits) sum[k][hf] += v[j];
+          }
+        }
+    } else {
+      __syncthreads();  // the sums are in registers: their LDS takes h
+    }
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int s = tid + k * kThreads;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sh.ys[slot_row(s) + r][0][slot_col(s)] = gated(sum[k][0][r], sum[k][1][r]);
+    }
+    __syncthreads();
+    const int n0 = tile * kExpertStreamCols;
+    for (int i = tid; i < en.rows * (kExpertStreamCols / 8); i += kThreads) {
+      const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
+      if (n0 + cp >= N) continue;
+      const float* v = &sh.ys[row][0][cp];
+      u32x4 term, rest;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        term[j] = pack_act2<BF16>(v[2 * j], v[2 * j + 1]);
+        rest[j] = pack_act2<BF16>(rest_of<BF16>(v[2 * j]), rest_of<BF16>(v[2 * j + 1]));
+      }
+      const uint32_t at = ((uint32_t)slots[row] * (uint32_t)N + (uint32_t)(n0 + cp)) * 2u;
+      __builtin_amdgcn_raw_buffer_store_b128(term, hrs, at, 0, kCpolDevice);
+      __builtin_amdgcn_raw_buffer_store_b128(rest, hrs, at + rest_at, 0, kCpolDevice);
+    }
+    stores_done();
+    __syncthreads();
+    if (tid == 0) count_in(ready + kLayerStride * entry);
+  }
+
+  // ---- The second product.
+  for (;;) {
+    const int item = take(down_tickets, down_items);
+    if (item < 0) break;
+    const int split = item % a.down_splits, tile = item / a.down_splits % a.down_tiles;
+    const int entry = item / a.down_splits / a.down_tiles;
+    const Entry en = entry_of<kEntryRows>(ranks, id, entry, lane, slots);
+    __syncthreads();
+    const int K = a.inner, N = a.N, NW = N >> 3, G = K / a.g_down;
+    const int wc_in = tile * (kExpertStreamCols / 8) + 2 * c;
+    const int wc = wc_in < NW ? wc_in : tile * (kExpertStreamCols / 8);
+    Share<1> share{a.down_qweight + (int64_t)en.expert * K * NW, a.down_qzeros + (int64_t)en.expert * G * NW,
+                   a.down_scales + (int64_t)en.expert * G * NW * 8, NW, K, a.g_down, wc, a.h,
+                   a.h + (int64_t)S * a.inner, {}, 0, 0};
+    share.x_off[0] = ((uint32_t)slots[c < en.rows ? c : 0] * (uint32_t)K + 8u * q) * 2u;
+    share.kb = min(K / 32, (split * kParts<false> + wave) * a.down_steps);
+    share.ke = min(K / 32, share.kb + a.down_steps);
+    bool whole = true;
+    auto wait = [&] {
+      uint32_t polls = 0;
+      while (load_count(ready + kLayerStride * entry) < (uint32_t)a.up_tiles) {
+        if (++polls == kMaxPolls) {
+          whole = false;
+          break;
+        }
+        __builtin_amdgcn_s_sleep(1);
+      }
+      asm volatile("" ::: "memory");  // nothing of h is read before
+    };
+    floatx4 part[1][16];
+    half8v unit[2];
+    stream_sums<BF16, 1, true>(share, wait, part, unit);
+    if (!whole) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) part[0][v] = floatx4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+    }
+    floatx4 sum[SLOTS][1];
+    wave_sums<false, RL>(sh.red, part[0], unit, sum);
+    __syncthreads();  // the sums are in registers: their LDS takes the output rows
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int s = tid + k * kThreads;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sh.ys[slot_row(s) + r][0][slot_col(s)] = sum[k][0][r];
+    }
+    __syncthreads();
+    const int n0 = tile * kExpertStreamCols;
+    const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
+        a.down_sums, (short)0, (int)((uint32_t)a.down_splits * (uint32_t)S * (uint32_t)N * 4u), 0x00020000);
+    for (int i = tid; i < en.rows * (kExpertStreamCols / 4); i += kThreads) {
+      const int row = i / (kExpertStreamCols / 4), cp = 4 * (i % (kExpertStreamCols / 4));
+      if (n0 + cp >= N) continue;
+      __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(&sh.ys[row][0][cp]), srs,
+                                             ((uint32_t)(split * S + slots[row]) * (uint32_t)N + (uint32_t)(n0 + cp)) * 4u,
+                                             0, kCpolDevice);
+    }
+    if (last_of(down_counts + tile, entries * a.down_splits)) combine(tile);
+  }
+}
+
+hipError_t launch_layer(const LayerArgs& a, RouteArgs r, const LayerPlan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.E * a.router_waves + 3) / 4), (unsigned)((a.T + kLayerTokens - 1) / kLayerTokens));
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, a, r); };
+  auto sized = [&](auto key, auto worth, auto groups) {
+    using Key = decltype(key);
+    using Worth = decltype(worth);
+    constexpr bool G = decltype(groups)::value;
+    if (a.E <= 64) go(layer_router_kernel<Key, Worth, 1, G>);
+    else if (a.E <= 256) go(layer_router_kernel<Key, Worth, 4, G>);
+    else go(layer_router_kernel<Key, Worth, 16, G>);
+  };
+  using yes = std::true_type;
+  using no = std::false_type;
+  // Which keys need fp64: awq_route.h.
+  if (r.bias != nullptr) r.groups > 1 ? sized(double{}, double{}, yes{}) : sized(double{}, double{}, no{});
+  else if (r.groups > 1 && r.group_top == 2) sized(float{}, double{}, yes{});
+  else r.groups > 1 ? sized(float{}, float{}, yes{}) : sized(float{}, float{}, no{});
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  auto main_kernel = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)p.workgroups), dim3(kThreads), 0, stream, a);
+  };
+  auto by_rows = [&](auto bf16) {
+    constexpr bool B = decltype(bf16)::value;
+    if (p.rows == 4) main_kernel(layer_kernel<B, 16>);
+    else if (p.rows == 8) main_kernel(layer_kernel<B, 32>);
+    else main_kernel(layer_kernel<B, 64>);
+  };
+  a.bf16 ? by_rows(yes{}) : by_rows(no{});
+  return hipGetLastError();
+}
+
+}  // namespace awq

@@ -591,6 +591,44 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
   return AWQ_OK;
 }
 
+int plan_layer(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size, int cus,
+               LayerPlan& p) {
+  p = LayerPlan{};
+  ExpertsPlan sizes;  // every check of the products
+  int st = plan_experts(T, topk, E, K, inner, N, group_size, cus, true, true, sizes);
+  if (st != AWQ_OK || T == 0) return st;
+  const int64_t S = T * topk;
+  if (S > kExpertRankSlots) return AWQ_ERR_UNSUPPORTED;
+  if (cus < 1) cus = 1;
+  p.rows = T <= 4 ? 4 : T <= 8 ? 8 : 16;  // a token goes to an expert once
+  p.router_waves = E <= 32 ? 4 : 1;
+  ExpertPlan up, down;
+  up.block_rows = down.block_rows = 16;
+  up.col_tiles = p.up_tiles = (int)((inner + kExpertStreamCols - 1) / kExpertStreamCols);
+  down.col_tiles = p.down_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
+  choose_splits(T, topk, E, K, 2 * inner, cus, true, up);
+  choose_splits(T, topk, E, inner, N, cus, false, down);
+  p.up_splits = up.splits;
+  p.up_steps = up.steps;
+  p.down_splits = down.splits;
+  p.down_steps = down.steps;
+  const int64_t entries = entry_bound(S, E, 16);
+  const int64_t up_items = entries * p.up_tiles * p.up_splits, down_items = entries * p.down_tiles * p.down_splits;
+  const int64_t items = up_items > down_items ? up_items : down_items;
+  if (up_items >= (int64_t(1) << 30) || down_items >= (int64_t(1) << 30)) return AWQ_ERR_UNSUPPORTED;
+  p.workgroups = items < 2 * (int64_t)cus ? items : 2 * (int64_t)cus;
+  p.n_counts = (16 + kExpertRankSlots) * kLayerStride + p.down_tiles + (p.up_splits > 1 ? entries * p.up_tiles : 0);
+  p.counts_bytes = round_up(p.n_counts * 4, 256);
+  p.logits_bytes = round_up(T * E * 4, 256);
+  p.ids_bytes = round_up(S * 4, 256);
+  p.h_bytes = round_up(2 * S * inner * 2, 256);
+  if (p.up_splits > 1) p.up_bytes = entries * p.up_tiles * p.up_splits * 2 * (p.rows / 4) * 256 * 16;
+  p.down_bytes = round_up(p.down_splits * S * N * 4, 256);
+  // 32-bit offsets into h and the sums.
+  if (2 * S * inner * 2 >= k2p32 || p.down_splits * S * N * 4 >= k2p32) return AWQ_ERR_UNSUPPORTED;
+  return AWQ_OK;
+}
+
 int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, bool gated, DensePlan& p) {
   p = DensePlan{};
   if (N < 1 || N > kMaxDim) return N < 1 ? AWQ_ERR_SHAPE : AWQ_ERR_UNSUPPORTED;

@@ -255,6 +255,24 @@ struct DensePlan {
 };
 int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, bool gated, DensePlan& p);
 
+// A whole routed layer of at most kExpertRankSlots slots (awq_moe_layer), and its workspace, in this
+// order: counts, logits, ids, weights, h, and the sums of both products' splits.
+constexpr int kLayerTokens = 8;    // tokens a workgroup of the router kernel takes
+constexpr int kLayerStride = 32;   // 32-bit counts that many workgroups touch: a 128-byte line each
+struct LayerPlan {
+  int rows = 0;          // rows kept per entry: 4, 8 or 16
+  int router_waves = 1;  // waves per expert
+  int up_tiles = 0, up_splits = 1, up_steps = 0, down_tiles = 0, down_splits = 1, down_steps = 0;
+  int64_t workgroups = 0;
+  int64_t n_counts = 0;
+  int64_t counts_bytes = 0, logits_bytes = 0, ids_bytes = 0, h_bytes = 0, up_bytes = 0, down_bytes = 0;
+  int64_t workspace_bytes() const {
+    return counts_bytes + logits_bytes + 2 * ids_bytes + h_bytes + up_bytes + down_bytes;
+  }
+};
+int plan_layer(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size, int cus,
+               LayerPlan& p);
+
 // K -> I gated (up) and inner -> N (down) products.
 int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
                  int cus, bool up, bool down, ExpertsPlan& p);

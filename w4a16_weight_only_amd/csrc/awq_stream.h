@@ -136,30 +136,38 @@ __device__ __forceinline__ int bits_below(uint64_t mask) {
 }
 
 // Entries of at most 64 slots, ranked by each wave (lane l: slot l): the slots of an expert,
-// in order, in blocks of ROWS; entries in the order of their first slot.  rows 0: no such entry.
+// in order, in blocks of ROWS; entries in the order of their first slot.
 // A lane's mask of slots with its expert comes from one ballot per bit of the id (a loop over
 // the slots took 5 us of 64 slots' 20).
+struct Ranks {
+  int rank;        // among the lower slots of the same expert
+  uint64_t leads;  // slots that begin an entry
+  int entries;
+  bool routed;
+};
 template <int ROWS>
-__device__ __forceinline__ Entry rank_entry(const int32_t* ids, int S, int E, int entry, int lane, int32_t* slots) {
-  const int id = lane < S ? ids[lane] : -1;
+__device__ __forceinline__ Ranks rank_slots(int id, int E) {
   const bool routed = id >= 0 && id < E;
-  const uint64_t live = __ballot(routed);
-  uint64_t same = live;
+  uint64_t same = __ballot(routed);
 #pragma unroll
   for (int b = 0; b < 10; ++b) {  // E <= 1024
     const uint64_t set = __ballot((id >> b) & 1);
     same &= ((id >> b) & 1) ? set : ~set;
   }
-  const int rank = bits_below(same);  // among the lower slots of the same expert
-  const bool lead = routed && rank % ROWS == 0;
-  const uint64_t leads = __ballot(lead);
-  const uint64_t found = __ballot(lead && bits_below(leads) == entry);
+  const int rank = bits_below(same);
+  const uint64_t leads = __ballot(routed && rank % ROWS == 0);
+  return Ranks{rank, leads, (int)__builtin_popcountll(leads), routed};
+}
+// The entry's expert and rows, its slots to LDS (every wave writes the same); rows 0: no such entry.
+template <int ROWS>
+__device__ __forceinline__ Entry entry_of(const Ranks& k, int id, int entry, int lane, int32_t* slots) {
+  const uint64_t found = __ballot(((k.leads >> lane) & 1) != 0 && bits_below(k.leads) == entry);
   if (found == 0) return Entry{0, 0};
   const int at = __builtin_ctzll(found);
   const int expert = __builtin_amdgcn_readlane(id, at);
-  const int first = __builtin_amdgcn_readlane(rank, at);
-  const bool mine = routed && id == expert && rank >= first && rank < first + ROWS;
-  if (mine) slots[rank - first] = lane;  // every wave writes the same
+  const int first = __builtin_amdgcn_readlane(k.rank, at);
+  const bool mine = k.routed && id == expert && k.rank >= first && k.rank < first + ROWS;
+  if (mine) slots[k.rank - first] = lane;
   return Entry{expert, (int)__builtin_popcountll(__ballot(mine))};
 }
 
@@ -178,6 +186,13 @@ struct Share {
 struct Now {
   __device__ void operator()() const {}
 };
+
+// 16 bytes as every XCD sees them alike.
+__device__ __forceinline__ half8v device_load(const uint16_t* base, uint64_t at) {
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), (short)0, -1, 0x00020000);
+  return __builtin_bit_cast(half8v, __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)at, 0, kCpolDevice));
+}
 
 // part[rb][v] * unit: sums of entry v's column and four rows (4 (lane / 16) ..) of block rb.
 // ready(): called before anything of x is read, behind the first loads of the weights.
@@ -230,6 +245,11 @@ __device__ __forceinline__ void stream_sums(const Share<RB>& s, Ready ready, flo
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       const uint64_t at = (uint64_t)s.x_off[rb] + r0 * 2u;
+      if constexpr (kWaits) {  // written by this kernel's other workgroups
+        st.x[rb] = device_load(s.x, at);
+        if constexpr (REST) st.rest[rb] = device_load(s.x_rest, at);
+        continue;
+      }
       st.x[rb] = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(s.x) + at);
       if constexpr (REST) st.rest[rb] = *reinterpret_cast<const half8v*>(reinterpret_cast<const char*>(s.x_rest) + at);
     }

@@ -2,8 +2,7 @@
 
 Work runs on the current stream of the tensors' device.  Where K is split, a call needs scratch
 memory, which comes from torch's allocator on that stream, and counters that are zero between
-calls: one zeroed tensor per stream, kept; under capture one of the graph's own, which the graph
-clears itself, so that graphs share none and need no call before.
+calls (counters.py), so calls may be captured into graphs without a call before.
 """
 from __future__ import annotations
 
@@ -12,6 +11,7 @@ import ctypes
 import torch
 
 from . import _lib
+from .counters import zeroed_counters
 from .linear import _check_tensor, validate
 from .moe import _TYPES, _call, _is, _output
 
@@ -19,7 +19,6 @@ _ACTIVATIONS = {None: _lib.AWQ_ACT_NONE, "relu": _lib.AWQ_ACT_RELU, "silu": _lib
                 "gelu": _lib.AWQ_ACT_GELU, "gelu_tanh": _lib.AWQ_ACT_GELU_TANH}
 
 _plans = {}  # (workspace, counter) bytes by device and the call's sizes
-_counters = {}  # zeroed tensors by device and stream
 
 
 def _plan(device, *sizes):
@@ -34,19 +33,6 @@ def _plan(device, *sizes):
             _plans.clear()
         _plans[key] = need = (ws.value, count.value)
     return need
-
-
-def zeroed_counters(device, nbytes):
-    """Device memory of at least nbytes, zero when this stream's next kernel runs, for kernels that
-    leave it zero."""
-    with torch.cuda.device(device):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(nbytes // 4, dtype=torch.int32, device=device)
-        key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
-        got = _counters.get(key)
-        if got is None or got.numel() * 4 < nbytes:
-            _counters[key] = got = torch.zeros(max(nbytes // 4, 4096), dtype=torch.int32, device=device)
-        return got
 
 
 def awq_gemm_fused(x: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor, scales: torch.Tensor,

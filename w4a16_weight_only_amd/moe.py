@@ -11,6 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
+from .counters import zeroed_counters
 from .linear import _check_tensor, validate
 
 _TYPES = {torch.float16: _lib.AWQ_F16, torch.bfloat16: _lib.AWQ_BF16, torch.float32: _lib.AWQ_F32}
@@ -234,6 +235,77 @@ def awq_moe_mlp(x: torch.Tensor, gate_up: tuple, down: tuple, expert_ids: torch.
     _call(_lib.load().awq_moe_mlp, "awq_moe_mlp", dev, x.data_ptr(), _act(x, nan_weights),
           *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down], expert_ids.data_ptr(), weights.data_ptr(),
           T, topk, E, K, inner, N, group_size, out.data_ptr(), ws.data_ptr(), nbytes)
+    return out
+
+
+_layer_sizes = {}  # workspace bytes of awq_moe_layer by device and the call's sizes
+
+
+def _layer_workspace(device, *sizes):
+    """Bytes, or the status with which the library refuses these sizes."""
+    key = (device.index, sizes)
+    need = _layer_sizes.get(key)
+    if need is None:
+        with torch.cuda.device(device):
+            need = _lib.load().awq_moe_layer_workspace(*sizes)
+        if len(_layer_sizes) >= 4096:
+            _layer_sizes.clear()
+        _layer_sizes[key] = need
+    return need
+
+
+def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tuple, topk: int, group_size: int = 128,
+                  *, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1, topk_groups: int = 1,
+                  group_top: int = 1, renormalize: bool = True, scale: float = 1.0, round_logits: bool = False,
+                  residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """A whole routed layer for a few tokens, T * topk <= 64, in two launches: x [T, K] (fp16 or
+    bfloat16), router [E, K] (x's type or fp32), gate_up and down packed weights of K -> 2 I and I -> N
+    columns -> y [T, N] in x's type,
+
+        y = residual + awq_moe_mlp of x and awq_moe_route(x . router^T)
+
+    The logits are fp32; round_logits rounds them to x's type first.  Routing arguments are
+    awq_moe_route's; y is rounded once.  A token whose logits hold a NaN (for the softmax, or +inf)
+    comes out as NaN.  out may be residual or x itself."""
+    _check_act("x", x)
+    dev = x.device
+    T, K = x.shape
+    E, wide = _check_layer("gate_up", gate_up, K, group_size, dev)
+    if wide % 16 != 0:
+        raise ValueError("gate_up: the columns must be two equal halves of whole words")
+    inner = wide // 2
+    E2, N = _check_layer("down", down, inner, group_size, dev)
+    if E2 != E:
+        raise ValueError(f"gate_up has {E} experts, down {E2}")
+    if not (_is(router, x.dtype, dev) or _is(router, torch.float32, dev)):
+        _check_tensor("router", router, torch.float32 if getattr(router, "dtype", None) is torch.float32 else x.dtype, dev)
+    if router.shape != (E, K):
+        raise ValueError(f"router must be [{E}, {K}]")
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    if bias is not None:
+        if not _is(bias, torch.float32, dev):
+            _check_tensor("bias", bias, torch.float32, dev)
+        if bias.shape != (E,):
+            raise ValueError(f"bias must be [{E}]")
+    if topk < 1:
+        raise ValueError("topk must be at least 1")
+    if residual is not None:
+        if not _is(residual, x.dtype, dev):
+            _check_tensor("residual", residual, x.dtype, dev)
+        if residual.shape != (T, N):
+            raise ValueError(f"residual must be [{T}, {N}]")
+    out = _output(out, (T, N), x.dtype, dev)
+    need = _layer_workspace(dev, T, topk, E, K, inner, N, group_size)
+    if need < 0:
+        _lib.check(need, "awq_moe_layer_workspace")
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    counters = zeroed_counters(dev, _lib.AWQ_MOE_LAYER_COUNTERS)
+    _call(_lib.load().awq_moe_layer, "awq_moe_layer", dev, x.data_ptr(), _TYPES[x.dtype], router.data_ptr(),
+          _TYPES[router.dtype], 1 if round_logits else 0, None if bias is None else bias.data_ptr(), _SCORES[score],
+          groups, topk_groups, group_top, topk, 1 if renormalize else 0, scale, *[t.data_ptr() for t in gate_up],
+          *[t.data_ptr() for t in down], None if residual is None else residual.data_ptr(), T, E, K, inner, N,
+          group_size, out.data_ptr(), ws.data_ptr(), need, counters.data_ptr(), _lib.AWQ_MOE_LAYER_COUNTERS)
     return out
 
 
