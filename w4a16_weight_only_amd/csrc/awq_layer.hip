@@ -144,6 +144,7 @@ __global__ __launch_bounds__(256) void layer_router_kernel(const LayerArgs a, co
           a.ids[t * a.topk + j] = id;
           a.weights[t * a.topk + j] = weight;
         });
+    __builtin_amdgcn_wave_barrier();  // the lanes go round together
   }
 }
 
@@ -249,17 +250,18 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
       if (lane == 0) taken = got;
     }
     __syncthreads();
-    const int got = taken;
-    __syncthreads();  // before it is written again, and before the LDS of the last item is
-    return got;
+    return __builtin_amdgcn_readfirstlane(taken);
   };
+  // Each round of the loops below ends in a barrier.  It keeps the LDS of one item from the next, and
+  // it keeps the lanes together: without one the compiler may carry a branch of thread 0's from a
+  // round's end into the next round, and lanes that have to act as one no longer do.
   // Last of n arrivals at a count (the same answer in every thread); the workgroup's stores precede.
   auto last_of = [&](uint32_t* count, int n) {
     stores_done();
     __syncthreads();
     if (tid == 0) last_arrival = count_in(count) == (uint32_t)n - 1u;
     __syncthreads();
-    return last_arrival != 0;
+    return __builtin_amdgcn_readfirstlane((int)last_arrival) != 0;
   };
   uint32_t* const up_tickets = a.counts;
   uint32_t* const down_tickets = up_tickets + 8 * kLayerStride;
@@ -291,6 +293,7 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
     stream_sums<BF16, 1, false>(share, Now{}, part, unit);
     floatx4 sum[SLOTS][2];
     wave_sums<true, RL>(sh.red, part[0], unit, sum);
+    bool mine = true;
     if (a.up_splits > 1) {
       constexpr uint32_t kShare = 2u * SLOTS * kThreads * 16u;
       const int64_t tile_at = (int64_t)entry * a.up_tiles + tile;
@@ -302,52 +305,58 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[k][hf]), prs, at(split, k, hf), 0, kCpolDevice);
-      if (!last_of(up_counts + tile_at, a.up_splits)) continue;
+      mine = last_of(up_counts + tile_at, a.up_splits);
+      if (mine) {
 #pragma unroll
-      for (int k = 0; k < SLOTS; ++k)
+        for (int k = 0; k < SLOTS; ++k)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          sum[k][hf] = floatx4{0.f, 0.f, 0.f, 0.f};
-          for (int s0 = 0; s0 < a.up_splits; s0 += 8) {
-            floatx4 v[8];
+          for (int hf = 0; hf < 2; ++hf) {
+            sum[k][hf] = floatx4{0.f, 0.f, 0.f, 0.f};
+            for (int s0 = 0; s0 < a.up_splits; s0 += 8) {
+              floatx4 v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              v[j] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                     prs, at(min(s0 + j, a.up_splits - 1), k, hf), 0, kCpolDevice));
+              for (int j = 0; j < 8; ++j)
+                v[j] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       prs, at(min(s0 + j, a.up_splits - 1), k, hf), 0, kCpolDevice));
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (s0 + j < a.up_splits) sum[k][hf] += v[j];
+              for (int j = 0; j < 8; ++j)
+                if (s0 + j < a.up_splits) sum[k][hf] += v[j];
+            }
           }
-        }
+      }
     } else {
       __syncthreads();  // the sums are in registers: their LDS takes h
     }
+    if (mine) {
 #pragma unroll
-    for (int k = 0; k < SLOTS; ++k) {
-      const int s = tid + k * kThreads;
+      for (int k = 0; k < SLOTS; ++k) {
+        const int s = tid + k * kThreads;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sh.ys[slot_row(s) + r][0][slot_col(s)] = gated(sum[k][0][r], sum[k][1][r]);
-    }
-    __syncthreads();
-    const int n0 = tile * kExpertStreamCols;
-    for (int i = tid; i < en.rows * (kExpertStreamCols / 8); i += kThreads) {
-      const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
-      if (n0 + cp >= N) continue;
-      const float* v = &sh.ys[row][0][cp];
-      u32x4 term, rest;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        term[j] = pack_act2<BF16>(v[2 * j], v[2 * j + 1]);
-        rest[j] = pack_act2<BF16>(rest_of<BF16>(v[2 * j]), rest_of<BF16>(v[2 * j + 1]));
+        for (int r = 0; r < 4; ++r) sh.ys[slot_row(s) + r][0][slot_col(s)] = gated(sum[k][0][r], sum[k][1][r]);
       }
-      const uint32_t at = ((uint32_t)slots[row] * (uint32_t)N + (uint32_t)(n0 + cp)) * 2u;
-      __builtin_amdgcn_raw_buffer_store_b128(term, hrs, at, 0, kCpolDevice);
-      __builtin_amdgcn_raw_buffer_store_b128(rest, hrs, at + rest_at, 0, kCpolDevice);
+      __syncthreads();
+      const int n0 = tile * kExpertStreamCols;
+      for (int i = tid; i < en.rows * (kExpertStreamCols / 8); i += kThreads) {
+        const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
+        if (n0 + cp >= N) continue;
+        const float* v = &sh.ys[row][0][cp];
+        u32x4 term, rest;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          term[j] = pack_act2<BF16>(v[2 * j], v[2 * j + 1]);
+          rest[j] = pack_act2<BF16>(rest_of<BF16>(v[2 * j]), rest_of<BF16>(v[2 * j + 1]));
+        }
+        const uint32_t at = ((uint32_t)slots[row] * (uint32_t)N + (uint32_t)(n0 + cp)) * 2u;
+        __builtin_amdgcn_raw_buffer_store_b128(term, hrs, at, 0, kCpolDevice);
+        __builtin_amdgcn_raw_buffer_store_b128(rest, hrs, at + rest_at, 0, kCpolDevice);
+      }
+      stores_done();
+      __syncthreads();
+      if (tid == 0) count_in(ready + kLayerStride * entry);
     }
-    stores_done();
     __syncthreads();
-    if (tid == 0) count_in(ready + kLayerStride * entry);
   }
+  __syncthreads();  // `taken` has been read
 
   // ---- The second product.
   for (;;) {
@@ -406,6 +415,7 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
                                              0, kCpolDevice);
     }
     if (last_of(down_counts + tile, entries * a.down_splits)) combine(tile);
+    __syncthreads();
   }
 }
 
