@@ -28,12 +28,12 @@ __device__ __forceinline__ void unpack8(const u32x4& w, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = act_to_float<BF16>((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
 }
 
-// y of eight adjacent columns whose f is formed: joined with the residual, rounded once.
+// y of eight adjacent columns whose f is formed: joined with the residual (raw), rounded once.
 template <bool BF16>
-__device__ __forceinline__ void finish8(const Epilogue& e, int64_t at, const float (&f)[8]) {
+__device__ __forceinline__ void finish8(const Epilogue& e, int64_t at, const float (&f)[8], const u32x4& raw) {
   float r[8];
   if (e.residual != nullptr) {
-    unpack8<BF16>(*reinterpret_cast<const u32x4*>(e.residual + at), r);
+    unpack8<BF16>(raw, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] += e.scale * f[i];
   } else {

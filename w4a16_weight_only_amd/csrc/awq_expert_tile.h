@@ -484,10 +484,13 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
         const int row = (staged >> 5) * kWaveRows + 32 * i + (staged & 31);
         if (row >= rows || n0 + c >= N) continue;
         const float* at = ys + staged * kLd + c;
+        const int64_t out = (int64_t)(first + row) * N + n0 + c;
+        u32x4 res{};
+        if (epi->residual != nullptr) res = *reinterpret_cast<const u32x4*>(epi->residual + out);
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = GATED ? activate(epi->act, at[j]) * at[kOut + j] : activate(epi->act, at[j]);
-        finish8<BF16>(*epi, (int64_t)(first + row) * N + n0 + c, f);
+        finish8<BF16>(*epi, out, f, res);
       }
     }
     return;

@@ -15,14 +15,16 @@ namespace awq {
 
 using namespace stream;
 
-// RB: blocks of 16 rows; RL: lanes whose rows are kept, 16 per four rows.
-template <bool GATED, bool BF16, int RB, int RL>
-__global__ __launch_bounds__(kThreads, 2) void fused_stream_kernel(const DenseProduct p, const Epilogue e, int tiles,
-                                                                   int splits, int steps) {
-  constexpr int PARTS = kParts<GATED>;
-  constexpr int SLOTS = 16 * RL / kThreads, HALVES = GATED ? 2 : 1;
+// RB: blocks of 16 rows; RL: lanes whose rows are kept, 16 per four rows; R: 1 for one row in all.
+template <bool GATED, bool BF16, int RB, int RL, int R>
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void fused_stream_kernel(const DenseProduct p, const Epilogue e, int tiles,
+                                                                     int splits, int steps) {
+  constexpr int WAVES = kStreamWaves, THREADS = 64 * WAVES;
+  constexpr int PARTS = kParts<GATED, WAVES>;
+  constexpr int SLOTS = kSlots<RL, WAVES>, HALVES = GATED ? 2 : 1;
+  constexpr int kPieces = R == 1 ? 1 : (RL / 4 * (kExpertStreamCols / 8) + THREADS - 1) / THREADS;
   __shared__ union {
-    floatx4 red[kWaves][16][RL];
+    Rows<R> red[WAVES][16][RL];
     float ys[RL / 4][HALVES][kYld];
   } sh;
   __shared__ uint32_t last_arrival;
@@ -57,60 +59,109 @@ __global__ __launch_bounds__(kThreads, 2) void fused_stream_kernel(const DensePr
   half8v unit[2];
   stream_sums<BF16, RB, false>(share, Now{}, part, unit);
 
-  // Sums of block rb in registers -> y.
+  // What the epilogue reads is asked for before the splits meet: the biases of the slots' columns, and
+  // the residual of the row pieces that this thread writes (one row: of its column).
   const int n0 = tile * kExpertStreamCols;
-  auto finish = [&](int rb, const floatx4 (&sum)[SLOTS][HALVES]) {
-    const int rows = min(p.M - row0 - 16 * rb, 16);
+  uint16_t braw[SLOTS][HALVES];
 #pragma unroll
-    for (int k = 0; k < SLOTS; ++k) {
-      const int s = tid + k * kThreads;
-      const int col = slot_col(s), row = slot_row(s);
-      const int n = n0 + col;
+  for (int k = 0; k < SLOTS; ++k)
 #pragma unroll
-      for (int hf = 0; hf < HALVES; ++hf) {
-        const float b = e.bias != nullptr && n < N ? act_to_float<BF16>(e.bias[hf * N + n]) : 0.f;
+    for (int hf = 0; hf < HALVES; ++hf) {
+      const int n = n0 + slot_col(tid + k * THREADS);
+      braw[k][hf] = e.bias != nullptr && n < N ? e.bias[hf * N + n] : 0;
+    }
+  auto piece = [&](int i, int rb, int& row, int& col) {  // piece i of this thread: whether it is one
+    const int at = tid + i * THREADS;
+    row = row0 + 16 * rb + at / (kExpertStreamCols / 8);
+    col = n0 + 8 * (at % (kExpertStreamCols / 8));
+    return at < RL / 4 * (kExpertStreamCols / 8) && row < p.M && col < N;
+  };
+  struct Residual {
+    u32x4 w[kPieces];
+    uint16_t one;
+  };
+  auto ask_residual = [&](int rb, Residual& r) {
+    if (e.residual == nullptr) return;
+    if constexpr (R == 1) {
+      const int n = n0 + slot_col(tid);
+      r.one = tid < 16 * RL && n < N ? e.residual[n] : 0;
+    } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sh.ys[row + r][hf][col] = sum[k][hf][r] + b;
+      for (int i = 0; i < kPieces; ++i) {
+        int row, col;
+        if (piece(i, rb, row, col)) r.w[i] = *reinterpret_cast<const u32x4*>(e.residual + (int64_t)row * N + col);
       }
     }
-    __syncthreads();
-    for (int i = tid; i < rows * (kExpertStreamCols / 8); i += kThreads) {
-      const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
-      if (n0 + cp >= N) continue;
-      float f[8];
+  };
+  // Sums of block rb in registers -> y.
+  auto finish = [&](int rb, const Rows<R> (&sum)[SLOTS][HALVES], const Residual& res) {
+    if constexpr (R == 1) {
+      const int n = n0 + slot_col(tid);
+      if (tid >= 16 * RL || n >= N) return;
+      float f = activate(e.act, sum[0][0] + act_to_float<BF16>(braw[0][0]));
+      if constexpr (GATED) f *= sum[0][HALVES - 1] + act_to_float<BF16>(braw[0][HALVES - 1]);
+      e.y[n] = float_to_act<BF16>((e.residual != nullptr ? act_to_float<BF16>(res.one) : 0.f) + e.scale * f);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[j] = activate(e.act, sh.ys[row][0][cp + j]);
-        if constexpr (GATED) f[j] *= sh.ys[row][HALVES - 1][cp + j];
+      for (int k = 0; k < SLOTS; ++k) {
+        const int s = tid + k * THREADS;
+        if (THREADS > 16 * RL && s >= 16 * RL) continue;
+        const int col = slot_col(s), row = slot_row(s);
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            sh.ys[row + r][hf][col] = row_of<R>(sum[k][hf], r) + act_to_float<BF16>(braw[k][hf]);
       }
-      finish8<BF16>(e, (int64_t)(row0 + 16 * rb + row) * N + n0 + cp, f);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        int row, col;
+        if (!piece(i, rb, row, col)) continue;
+        const int at = row - row0 - 16 * rb, cp = col - n0;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[j] = activate(e.act, sh.ys[at][0][cp + j]);
+          if constexpr (GATED) f[j] *= sh.ys[at][HALVES - 1][cp + j];
+        }
+        finish8<BF16>(e, (int64_t)row * N + col, f, res.w[i]);
+      }
     }
   };
 
-  // Sums in the workspace: [row block][tile][split][rb][half][slot][thread] of four rows.
-  constexpr uint32_t kShareBytes = (uint32_t)(RB * HALVES * SLOTS * kThreads * 16);
+  // Sums in the workspace: [row block][tile][split][rb][half][slot][thread] of R rows.
+  constexpr uint32_t kOne = 4u * R;
+  constexpr uint32_t kShareBytes = (uint32_t)(RB * HALVES * 16 * RL) * kOne;
   const int64_t tile_at = (int64_t)block * tiles + tile;
   const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
       p.sums + tile_at * splits * (kShareBytes / 4), (short)0, (int)(kShareBytes * (uint32_t)splits), 0x00020000);
+  // (Threads past the last slot, and slots of rows past M, reach past the buffer: nothing moves.)
   auto share_at = [&](int sp, int rb, int hf, int k) {
-    return (uint32_t)sp * kShareBytes + (uint32_t)(((rb * HALVES + hf) * SLOTS + k) * kThreads + tid) * 16u;
+    const int s = tid + k * THREADS;
+    const uint32_t at = (uint32_t)sp * kShareBytes + (uint32_t)((rb * HALVES + hf) * 16 * RL + s) * kOne;
+    const bool none = (THREADS > 16 * RL && s >= 16 * RL) || row0 + 16 * rb + slot_row(s) >= p.M;
+    return none ? kShareBytes * (uint32_t)splits : at;
   };
+  Residual res;
+  if (splits == 1) ask_residual(0, res);
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     if (row0 + 16 * rb >= p.M) break;  // the same in every wave
-    if (rb > 0) __syncthreads();       // the last block's LDS has been read
-    floatx4 sum[SLOTS][HALVES];
-    wave_sums<GATED, RL>(sh.red, part[rb], unit, sum);
+    if (rb > 0) {
+      if (splits == 1) ask_residual(rb, res);
+      __syncthreads();  // the last block's LDS has been read
+    }
+    Rows<R> sum[SLOTS][HALVES];
+    wave_sums<GATED, RL, WAVES, R>(sh.red, part[rb], unit, sum);
     if (splits == 1) {
       __syncthreads();  // the sums are in registers: their LDS takes the output rows
-      finish(rb, sum);
+      finish(rb, sum, res);
     } else {
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k)
 #pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[k][hf]), prs, share_at(split, rb, hf, k), 0,
-                                                 kCpolDevice);
+        for (int hf = 0; hf < HALVES; ++hf) device_store<R>(prs, share_at(split, rb, hf, k), sum[k][hf]);
     }
   }
   if (splits == 1) return;
@@ -125,43 +176,32 @@ __global__ __launch_bounds__(kThreads, 2) void fused_stream_kernel(const DensePr
     last_arrival = last;
   }
   __syncthreads();
-  if (!last_arrival) return;
+  if (__builtin_amdgcn_readfirstlane((int)last_arrival) == 0) return;
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     if (row0 + 16 * rb >= p.M) break;
+    ask_residual(rb, res);
+    Rows<R> flat[SLOTS * HALVES], sum[SLOTS][HALVES];
+    device_sums<R>(prs, splits, [&](int sp, int i) { return share_at(sp, rb, i % HALVES, i / HALVES); }, flat);
+#pragma unroll
+    for (int i = 0; i < SLOTS * HALVES; ++i) sum[i / HALVES][i % HALVES] = flat[i];
     if (rb > 0) __syncthreads();
-    floatx4 sum[SLOTS][HALVES];
-#pragma unroll
-    for (int k = 0; k < SLOTS; ++k)
-#pragma unroll
-      for (int hf = 0; hf < HALVES; ++hf) {
-        sum[k][hf] = floatx4{0.f, 0.f, 0.f, 0.f};
-        // Eight loads at a time; those past the last split read it again and are dropped.
-        for (int s0 = 0; s0 < splits; s0 += 8) {
-          floatx4 v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[j] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                   prs, share_at(min(s0 + j, splits - 1), rb, hf, k), 0, kCpolDevice));
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (s0 + j < splits) sum[k][hf] += v[j];
-        }
-      }
-    finish(rb, sum);
+    finish(rb, sum, res);
   }
 }
 
 hipError_t launch_fused_stream(const DenseProduct& p, const Epilogue& e, const DensePlan& d, hipStream_t stream) {
   auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)d.grid), dim3(kThreads), 0, stream, p, e, d.col_tiles, d.splits, d.steps);
+    hipLaunchKernelGGL(kern, dim3((unsigned)d.grid), dim3(64 * kStreamWaves), 0, stream, p, e, d.col_tiles, d.splits,
+                       d.steps);
   };
-#define AWQ_FUSED(GATED, BF16)                                            \
-  do {                                                                    \
-    if (d.rows == 4) go(fused_stream_kernel<GATED, BF16, 1, 16>);         \
-    else if (d.rows == 8) go(fused_stream_kernel<GATED, BF16, 1, 32>);    \
-    else if (d.rows == 16) go(fused_stream_kernel<GATED, BF16, 1, 64>);   \
-    else go(fused_stream_kernel<GATED, BF16, 2, 64>);                     \
+#define AWQ_FUSED(GATED, BF16)                                             \
+  do {                                                                     \
+    if (d.rows == 1) go(fused_stream_kernel<GATED, BF16, 1, 16, 1>);       \
+    else if (d.rows == 4) go(fused_stream_kernel<GATED, BF16, 1, 16, 4>);  \
+    else if (d.rows == 8) go(fused_stream_kernel<GATED, BF16, 1, 32, 4>);  \
+    else if (d.rows == 16) go(fused_stream_kernel<GATED, BF16, 1, 64, 4>); \
+    else go(fused_stream_kernel<GATED, BF16, 2, 64, 4>);                   \
   } while (0)
   if (p.gated) {
     if (p.bf16) AWQ_FUSED(true, true);

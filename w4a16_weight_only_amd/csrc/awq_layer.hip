@@ -17,9 +17,9 @@
 // same (kCpolDevice), and is counted in after it is complete.
 //
 // Every wait ends, whatever else runs on the card and however many workgroups are resident: a ticket
-// is taken by a workgroup that runs, a gated item waits for nothing, and a workgroup takes an item of
-// the second product only after it has seen that all gated items are taken.  So does a bound on the
-// polls, behind which y is NaN.  Tickets are eight lists, one per XCD as blocks go round them (one
+// is taken by a workgroup that runs, a gated item waits for nothing, and a workgroup begins with items
+// of the second product only after it has seen that all gated items are taken (it may hold a ticket
+// before: nobody waits for those).  So does a bound on the polls, behind which y is NaN.  Tickets are eight lists, one per XCD as blocks go round them (one
 // list: 18 ns for each workgroup in turn); who finds his own empty takes from the others.
 #include "awq_route.h"
 #include "awq_stream.h"
@@ -29,6 +29,9 @@ namespace awq {
 using namespace stream;
 
 namespace {
+
+constexpr int kRouterWaves = kLayerTokens;  // a token each to route
+constexpr int kRouterThreads = 64 * kRouterWaves;
 
 constexpr uint32_t kMaxPolls = 1u << 18;  // a fifth of a second or more
 
@@ -72,14 +75,14 @@ __device__ __forceinline__ void dots(const LayerArgs& a, int e, int t0, int firs
 }  // namespace
 
 template <typename Key, typename Worth, int VPL, bool GROUPS>
-__global__ __launch_bounds__(256) void layer_router_kernel(const LayerArgs a, const RouteArgs r) {
+__global__ __launch_bounds__(64 * kRouterWaves) void layer_router_kernel(const LayerArgs a, const RouteArgs r) {
   constexpr float kInf = __builtin_inff();
   __shared__ union {
-    float part[4][kLayerTokens];
+    float part[kRouterWaves][kLayerTokens];
     struct {
       float l[64 * VPL];
       route::Scratch<Worth, 64, VPL, GROUPS> scratch;
-    } of[4];
+    } of[kRouterWaves];
   } sh;
   __shared__ uint32_t last_arrival;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -87,11 +90,11 @@ __global__ __launch_bounds__(256) void layer_router_kernel(const LayerArgs a, co
   const int t0 = blockIdx.y * kLayerTokens;
   const int nt = min(a.T - t0, kLayerTokens);
   // The other kernel's counts.
-  for (int64_t i = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 256 + tid; i < a.n_counts;
-       i += (int64_t)gridDim.x * gridDim.y * 256)
+  for (int64_t i = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * kRouterThreads + tid; i < a.n_counts;
+       i += (int64_t)gridDim.x * gridDim.y * kRouterThreads)
     a.counts[i] = 0;
 
-  const int per = 4 / a.router_waves;  // experts of a workgroup
+  const int per = kRouterWaves / a.router_waves;  // experts of a workgroup
   const int e = blockIdx.x * per + wave / a.router_waves, part = wave % a.router_waves;
   const int el = min(e, a.E - 1);
   float acc[kLayerTokens];
@@ -125,7 +128,7 @@ __global__ __launch_bounds__(256) void layer_router_kernel(const LayerArgs a, co
 
   // The LDS accesses of a wave are its own and in order; the compiler keeps them so.
   auto sync = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
-  for (int i = wave; i < nt; i += 4) {
+  for (int i = wave; i < nt; i += kRouterWaves) {
     const int t = t0 + i;
     float l[VPL];
 #pragma unroll
@@ -148,14 +151,15 @@ __global__ __launch_bounds__(256) void layer_router_kernel(const LayerArgs a, co
   }
 }
 
-// RL: lanes whose rows are kept, 16 per four rows; no expert has more than RL / 4 slots.. (16: any).
-template <bool BF16, int RL>
-__global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
-  constexpr int SLOTS = 16 * RL / kThreads;
+// RL: lanes whose rows are kept, 16 per four rows; R: 1 for one token.
+template <bool BF16, int RL, int R>
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const LayerArgs a) {
+  constexpr int WAVES = kStreamWaves, THREADS = 64 * WAVES;
+  constexpr int SLOTS = kSlots<RL, WAVES>;
   constexpr int kEntryRows = 16;
   __shared__ union {
-    floatx4 red[kWaves][16][RL];
-    float ys[RL / 4][2][kYld];
+    Rows<R> red[WAVES][16][RL];
+    float ys[RL / 4][kYld];
   } sh;
   __shared__ int32_t slots[kEntryRows], ids[kExpertRankSlots];
   __shared__ float weights[kExpertRankSlots];
@@ -165,8 +169,67 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, c = lane & 15;
   const int S = a.T * a.topk;
+  const int home = blockIdx.x & 7;
+  uint32_t* const up_tickets = a.counts;
+  uint32_t* const down_tickets = up_tickets + 8 * kLayerStride;
+  uint32_t* const ready = down_tickets + 8 * kLayerStride;
+  uint32_t* const down_counts = ready + kExpertRankSlots * kLayerStride;
+  uint32_t* const up_counts = down_counts + a.down_tiles;
+
+  // A ticket of one's own list, and how far the lists are, asked for ahead of when they are needed.
+  struct Ticket {
+    uint32_t mine, seen;  // (lane 0; lanes 0 to 7) of wave 0
+  };
+  auto ask = [&](uint32_t* tickets) {
+    Ticket t{0, 0};
+    if (wave == 0) {
+      if (lane == 0) t.mine = count_in(tickets + kLayerStride * home);
+      if (lane < 8) t.seen = load_count(tickets + kLayerStride * lane);
+    }
+    return t;
+  };
+  // The item of a ticket, of what the other lists have left if one's own is empty, or -1 when all of
+  // them are.  Item i is in list i % 8.
+  auto settle = [&](const Ticket& ticket, uint32_t* tickets, int total) {
+    if (wave == 0) {
+      int got = -1, list = home;
+      uint32_t v = __builtin_amdgcn_readfirstlane(ticket.mine), seen = ticket.seen;
+      for (;;) {
+        const int n = (total - list + 7) >> 3;  // items of this list
+        if (n > 0 && v < (uint32_t)n) {
+          got = (int)v * 8 + list;
+          break;
+        }
+        const uint64_t left = __ballot(lane < 8 && lane != list && (int64_t)seen < (int64_t)((total - lane + 7) >> 3));
+        if (left == 0) break;
+        // The next list after one's own that has something left.
+        const uint32_t turned = (uint32_t)((left | left << 8) >> home) & 0xFFu;
+        list = (home + __builtin_ctz(turned)) & 7;
+        v = 0;
+        if (lane == 0) v = count_in(tickets + kLayerStride * list);
+        v = __builtin_amdgcn_readfirstlane(v);
+        seen = lane < 8 ? load_count(tickets + kLayerStride * lane) : 0u;
+      }
+      if (lane == 0) taken = got;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(taken);
+  };
+  // Each round of the loops below ends in a barrier.  It keeps the LDS of one item from the next, and
+  // it keeps the lanes together: without one the compiler may carry a branch of thread 0's from a
+  // round's end into the next round, and lanes that have to act as one no longer do.
+
+  // Last of n arrivals at a count (the same answer in every thread); the workgroup's stores precede.
+  auto last_of = [&](uint32_t* count, int n) {
+    stores_done();
+    __syncthreads();
+    if (tid == 0) last_arrival = count_in(count) == (uint32_t)n - 1u;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane((int)last_arrival) != 0;
+  };
 
   // Slots by expert, one per lane, in every wave: blocks of 16 slots of one expert are entries.
+  Ticket ticket = ask(up_tickets);
   const int id = lane < S ? a.ids[lane] : -1;
   if (wave == 0) {
     ids[lane] = id;
@@ -177,104 +240,67 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
   const int up_items = entries * a.up_tiles * a.up_splits, down_items = entries * a.down_tiles * a.down_splits;
   __syncthreads();
 
-  // y of a column tile: every token's slots and splits, in order.  P threads share four columns.
+  // y of a column tile: every token's slots and splits, in order.  P threads share four columns, each
+  // adding every P-th term.
   auto combine = [&](int tile) {
-    const int P = a.T == 1 ? 4 : a.T == 2 ? 2 : 1;
+    int P = 1;
+    while (P < 8 && 2 * P * a.T * (kExpertStreamCols / 4) <= THREADS) P *= 2;
     const int part = tid & (P - 1), terms = entries > 0 ? a.topk * a.down_splits : 0;
+    const float per = 1.f / (float)a.down_splits;
+    auto slot_of = [&](int term) { return (int)(((float)term + 0.5f) * per); };  // term / down_splits (< 2^12)
     const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
         a.down_sums, (short)0, (int)((uint32_t)a.down_splits * (uint32_t)S * (uint32_t)a.N * 4u), 0x00020000);
-    for (int i = tid / P; i < a.T * (kExpertStreamCols / 4); i += kThreads / P) {
+    for (int i = tid / P; i < a.T * (kExpertStreamCols / 4); i += THREADS / P) {
       const int t = i / (kExpertStreamCols / 4);
       const int n = tile * kExpertStreamCols + 4 * (i % (kExpertStreamCols / 4));
       const bool live = n < a.N;
+      const int64_t at = (int64_t)t * a.N + n;
+      u32x2 res = {0u, 0u};
+      if (a.residual != nullptr && live) res = *reinterpret_cast<const u32x2*>(a.residual + at);
       floatx4 sum = {0.f, 0.f, 0.f, 0.f};
-      // Eight terms' loads at a time, routed or not (what no one wrote is dropped).
-      for (int i0 = part; i0 < terms; i0 += 8 * P) {
-        floatx4 v[8];
+      // Terms' loads by the eight, or four, at a time, routed or not (what no one wrote is dropped).
+      auto add = [&](auto count, int i0) {
+        constexpr int B = decltype(count)::value;
+        floatx4 v[B];
+        int s[B];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < B; ++u) {
           const int term = min(i0 + u * P, terms - 1);
-          const int j = term / a.down_splits, sp = term - j * a.down_splits;
-          const uint32_t at = ((uint32_t)(sp * S + t * a.topk + j) * (uint32_t)a.N + (uint32_t)(live ? n : 0)) * 4u;
-          v[u] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(srs, at, 0, kCpolDevice));
+          const int j = slot_of(term), sp = term - j * a.down_splits;
+          s[u] = t * a.topk + j;
+          v[u] = device_read<4>(srs, ((uint32_t)(sp * S + s[u]) * (uint32_t)a.N + (uint32_t)(live ? n : 0)) * 4u);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int term = i0 + u * P;
-          const int s = t * a.topk + min(term, terms - 1) / a.down_splits;
-          if (term < terms && ids[s] >= 0) sum += weights[s] * v[u];
-        }
-      }
+        for (int u = 0; u < B; ++u)
+          if (i0 + u * P < terms && ids[s[u]] >= 0) sum += weights[s[u]] * v[u];
+      };
+      int i0 = part;
+      for (; i0 - part + 4 * P < terms; i0 += 8 * P) add(std::integral_constant<int, 8>{}, i0);
+      if (i0 - part < terms) add(std::integral_constant<int, 4>{}, i0);
       for (int m = 1; m < P; m *= 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], m);
       // A token without scores has NaN weights and no experts.
       const float lost = weights[t * a.topk] != weights[t * a.topk] ? weights[t * a.topk] : 0.f;
-      if (part != 0 || !live) continue;
-      const int64_t at = (int64_t)t * a.N + n;
-      if (a.residual != nullptr) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(a.residual + at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j] += act_to_float<BF16>((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-      }
-      *reinterpret_cast<u32x2*>(a.y + at) = u32x2{pack_act2<BF16>(sum[0] + lost, sum[1] + lost),
-                                                  pack_act2<BF16>(sum[2] + lost, sum[3] + lost)};
+      for (int j = 0; j < 4; ++j) sum[j] += lost + act_to_float<BF16>((uint16_t)(res[j >> 1] >> (16 * (j & 1))));
+      if (part == 0 && live)
+        *reinterpret_cast<u32x2*>(a.y + at) = u32x2{pack_act2<BF16>(sum[0], sum[1]), pack_act2<BF16>(sum[2], sum[3])};
     }
   };
   if (entries == 0) {  // nobody goes anywhere
     for (int tile = blockIdx.x; tile < a.down_tiles; tile += gridDim.x) combine(tile);
     return;
   }
-
-  // The next item of a list, or -1 when all of it is taken.  Item i is in list i % 8.
-  auto take = [&](uint32_t* tickets, int total) {
-    if (wave == 0) {
-      const int home = blockIdx.x & 7;
-      int got = -1, list = home;
-      for (;;) {
-        const int n = (total - list + 7) >> 3;  // items of this list
-        uint32_t v = 0;
-        if (lane == 0 && n > 0) v = count_in(tickets + kLayerStride * list);
-        v = __builtin_amdgcn_readfirstlane(v);
-        if (n > 0 && v < (uint32_t)n) {
-          got = (int)v * 8 + list;
-          break;
-        }
-        const uint32_t seen = lane < 8 ? load_count(tickets + kLayerStride * lane) : 0u;
-        const uint64_t left = __ballot(lane < 8 && (int64_t)seen < (int64_t)((total - lane + 7) >> 3));
-        if (left == 0) break;
-        // The next list after one's own that has something left.
-        const uint32_t turned = (uint32_t)((left | left << 8) >> home) & 0xFFu;
-        list = (home + __builtin_ctz(turned)) & 7;
-      }
-      if (lane == 0) taken = got;
-    }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(taken);
-  };
-  // Each round of the loops below ends in a barrier.  It keeps the LDS of one item from the next, and
-  // it keeps the lanes together: without one the compiler may carry a branch of thread 0's from a
-  // round's end into the next round, and lanes that have to act as one no longer do.
-  // Last of n arrivals at a count (the same answer in every thread); the workgroup's stores precede.
-  auto last_of = [&](uint32_t* count, int n) {
-    stores_done();
-    __syncthreads();
-    if (tid == 0) last_arrival = count_in(count) == (uint32_t)n - 1u;
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane((int)last_arrival) != 0;
-  };
-  uint32_t* const up_tickets = a.counts;
-  uint32_t* const down_tickets = up_tickets + 8 * kLayerStride;
-  uint32_t* const ready = down_tickets + 8 * kLayerStride;
-  uint32_t* const down_counts = ready + kExpertRankSlots * kLayerStride;
-  uint32_t* const up_counts = down_counts + a.down_tiles;
   const __amdgpu_buffer_rsrc_t hrs = __builtin_amdgcn_make_buffer_rsrc(
       a.h, (short)0, (int)(2u * (uint32_t)S * (uint32_t)a.inner * 2u), 0x00020000);
   const uint32_t rest_at = (uint32_t)S * (uint32_t)a.inner * 2u;  // the second term's bytes
 
   // ---- The gated product.
+  Ticket next;  // of the second product
+  bool asked = false;
   for (;;) {
-    const int item = take(up_tickets, up_items);
+    const int item = settle(ticket, up_tickets, up_items);
     if (item < 0) break;
     const int split = item % a.up_splits, tile = item / a.up_splits % a.up_tiles;
     const int entry = item / a.up_splits / a.up_tiles;
@@ -286,60 +312,57 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
     Share<1> share{a.up_qweight + (int64_t)en.expert * K * NW, a.up_qzeros + (int64_t)en.expert * G * NW,
                    a.up_scales + (int64_t)en.expert * G * NW * 8, NW, K, a.g_up, wc, a.x, nullptr, {}, 0, 0};
     share.x_off[0] = ((uint32_t)(slots[c < en.rows ? c : 0] / a.topk) * (uint32_t)K + 8u * q) * 2u;
-    share.kb = min(K / 32, (split * kParts<true> + (wave >> 1)) * a.up_steps);
+    share.kb = min(K / 32, (split * kParts<true, WAVES> + (wave >> 1)) * a.up_steps);
     share.ke = min(K / 32, share.kb + a.up_steps);
     floatx4 part[1][16];
     half8v unit[2];
     stream_sums<BF16, 1, false>(share, Now{}, part, unit);
-    floatx4 sum[SLOTS][2];
-    wave_sums<true, RL>(sh.red, part[0], unit, sum);
+    ticket = ask(up_tickets);
+    Rows<R> sum[SLOTS][2];
+    wave_sums<true, RL, WAVES, R>(sh.red, part[0], unit, sum);
     bool mine = true;
     if (a.up_splits > 1) {
-      constexpr uint32_t kShare = 2u * SLOTS * kThreads * 16u;
+      constexpr uint32_t kShare = 2u * 16 * RL * 4u * R;
       const int64_t tile_at = (int64_t)entry * a.up_tiles + tile;
       const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
           a.up_sums + tile_at * a.up_splits * (kShare / 4), (short)0, (int)(kShare * (uint32_t)a.up_splits), 0x00020000);
-      auto at = [&](int sp, int k, int hf) { return (uint32_t)sp * kShare + (uint32_t)((2 * k + hf) * kThreads + tid) * 16u; };
+      // (Threads past the last slot, and slots of rows past the entry's, reach past the buffer.)
+      auto at = [&](int sp, int k, int hf) {
+        const int s = tid + k * THREADS;
+        const bool none = (THREADS > 16 * RL && s >= 16 * RL) || slot_row(s) >= en.rows;
+        return none ? kShare * (uint32_t)a.up_splits : (uint32_t)sp * kShare + (uint32_t)(hf * 16 * RL + s) * 4u * R;
+      };
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[k][hf]), prs, at(split, k, hf), 0, kCpolDevice);
+        for (int hf = 0; hf < 2; ++hf) device_store<R>(prs, at(split, k, hf), sum[k][hf]);
       mine = last_of(up_counts + tile_at, a.up_splits);
       if (mine) {
+        Rows<R> flat[2 * SLOTS];
+        device_sums<R>(prs, a.up_splits, [&](int sp, int i) { return at(sp, i / 2, i % 2); }, flat);
 #pragma unroll
-        for (int k = 0; k < SLOTS; ++k)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            sum[k][hf] = floatx4{0.f, 0.f, 0.f, 0.f};
-            for (int s0 = 0; s0 < a.up_splits; s0 += 8) {
-              floatx4 v[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                v[j] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       prs, at(min(s0 + j, a.up_splits - 1), k, hf), 0, kCpolDevice));
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (s0 + j < a.up_splits) sum[k][hf] += v[j];
-            }
-          }
+        for (int i = 0; i < 2 * SLOTS; ++i) sum[i / 2][i % 2] = flat[i];
       }
     } else {
       __syncthreads();  // the sums are in registers: their LDS takes h
     }
+    if (!asked) next = ask(down_tickets);
+    asked = true;
     if (mine) {
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k) {
-        const int s = tid + k * kThreads;
+        const int s = tid + k * THREADS;
+        if (THREADS > 16 * RL && s >= 16 * RL) continue;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sh.ys[slot_row(s) + r][0][slot_col(s)] = gated(sum[k][0][r], sum[k][1][r]);
+        for (int r = 0; r < R; ++r)
+          sh.ys[slot_row(s) + r][slot_col(s)] = gated(row_of<R>(sum[k][0], r), row_of<R>(sum[k][1], r));
       }
       __syncthreads();
       const int n0 = tile * kExpertStreamCols;
-      for (int i = tid; i < en.rows * (kExpertStreamCols / 8); i += kThreads) {
+      for (int i = tid; i < en.rows * (kExpertStreamCols / 8); i += THREADS) {
         const int row = i / (kExpertStreamCols / 8), cp = 8 * (i % (kExpertStreamCols / 8));
         if (n0 + cp >= N) continue;
-        const float* v = &sh.ys[row][0][cp];
+        const float* v = &sh.ys[row][cp];
         u32x4 term, rest;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -356,11 +379,12 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
     }
     __syncthreads();
   }
+  if (!asked) next = ask(down_tickets);
   __syncthreads();  // `taken` has been read
 
   // ---- The second product.
   for (;;) {
-    const int item = take(down_tickets, down_items);
+    const int item = settle(next, down_tickets, down_items);
     if (item < 0) break;
     const int split = item % a.down_splits, tile = item / a.down_splits % a.down_tiles;
     const int entry = item / a.down_splits / a.down_tiles;
@@ -373,7 +397,7 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
                    a.down_scales + (int64_t)en.expert * G * NW * 8, NW, K, a.g_down, wc, a.h,
                    a.h + (int64_t)S * a.inner, {}, 0, 0};
     share.x_off[0] = ((uint32_t)slots[c < en.rows ? c : 0] * (uint32_t)K + 8u * q) * 2u;
-    share.kb = min(K / 32, (split * kParts<false> + wave) * a.down_steps);
+    share.kb = min(K / 32, (split * kParts<false, WAVES> + wave) * a.down_steps);
     share.ke = min(K / 32, share.kb + a.down_steps);
     bool whole = true;
     auto wait = [&] {
@@ -390,29 +414,30 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
     floatx4 part[1][16];
     half8v unit[2];
     stream_sums<BF16, 1, true>(share, wait, part, unit);
+    next = ask(down_tickets);
     if (!whole) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) part[0][v] = floatx4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
     }
-    floatx4 sum[SLOTS][1];
-    wave_sums<false, RL>(sh.red, part[0], unit, sum);
+    Rows<R> sum[SLOTS][1];
+    wave_sums<false, RL, WAVES, R>(sh.red, part[0], unit, sum);
     __syncthreads();  // the sums are in registers: their LDS takes the output rows
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
-      const int s = tid + k * kThreads;
+      const int s = tid + k * THREADS;
+      if (THREADS > 16 * RL && s >= 16 * RL) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sh.ys[slot_row(s) + r][0][slot_col(s)] = sum[k][0][r];
+      for (int r = 0; r < R; ++r) sh.ys[slot_row(s) + r][slot_col(s)] = row_of<R>(sum[k][0], r);
     }
     __syncthreads();
     const int n0 = tile * kExpertStreamCols;
     const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
         a.down_sums, (short)0, (int)((uint32_t)a.down_splits * (uint32_t)S * (uint32_t)N * 4u), 0x00020000);
-    for (int i = tid; i < en.rows * (kExpertStreamCols / 4); i += kThreads) {
+    for (int i = tid; i < en.rows * (kExpertStreamCols / 4); i += THREADS) {
       const int row = i / (kExpertStreamCols / 4), cp = 4 * (i % (kExpertStreamCols / 4));
       if (n0 + cp >= N) continue;
-      __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(&sh.ys[row][0][cp]), srs,
-                                             ((uint32_t)(split * S + slots[row]) * (uint32_t)N + (uint32_t)(n0 + cp)) * 4u,
-                                             0, kCpolDevice);
+      device_store<4>(srs, ((uint32_t)(split * S + slots[row]) * (uint32_t)N + (uint32_t)(n0 + cp)) * 4u,
+                      *reinterpret_cast<const floatx4*>(&sh.ys[row][cp]));
     }
     if (last_of(down_counts + tile, entries * a.down_splits)) combine(tile);
     __syncthreads();
@@ -420,8 +445,8 @@ __global__ __launch_bounds__(kThreads, 2) void layer_kernel(const LayerArgs a) {
 }
 
 hipError_t launch_layer(const LayerArgs& a, RouteArgs r, const LayerPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.E * a.router_waves + 3) / 4), (unsigned)((a.T + kLayerTokens - 1) / kLayerTokens));
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, a, r); };
+  const dim3 grid((unsigned)((a.E * a.router_waves + kRouterWaves - 1) / kRouterWaves), (unsigned)((a.T + kLayerTokens - 1) / kLayerTokens));
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kRouterThreads), 0, stream, a, r); };
   auto sized = [&](auto key, auto worth, auto groups) {
     using Key = decltype(key);
     using Worth = decltype(worth);
@@ -439,13 +464,14 @@ hipError_t launch_layer(const LayerArgs& a, RouteArgs r, const LayerPlan& p, hip
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   auto main_kernel = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)p.workgroups), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)p.workgroups), dim3(64 * kStreamWaves), 0, stream, a);
   };
   auto by_rows = [&](auto bf16) {
     constexpr bool B = decltype(bf16)::value;
-    if (p.rows == 4) main_kernel(layer_kernel<B, 16>);
-    else if (p.rows == 8) main_kernel(layer_kernel<B, 32>);
-    else main_kernel(layer_kernel<B, 64>);
+    if (p.rows == 1) main_kernel(layer_kernel<B, 16, 1>);
+    else if (p.rows == 4) main_kernel(layer_kernel<B, 16, 4>);
+    else if (p.rows == 8) main_kernel(layer_kernel<B, 32, 4>);
+    else main_kernel(layer_kernel<B, 64, 4>);
   };
   a.bf16 ? by_rows(yes{}) : by_rows(no{});
   return hipGetLastError();

@@ -477,6 +477,45 @@ int64_t entry_bound(int64_t S, int64_t E, int64_t rows) {
   return b < S ? b : S;
 }
 
+// Entries of `rows` rows, about, that T tokens' slots make.
+int64_t active_entries(int64_t T, int64_t topk, int64_t E, int64_t rows) {
+  // Experts with rows, about, where a token's are distinct: E (1 - (1 - topk / E)^T).
+  const int64_t S = T * topk;
+  double idle = 1.0;
+  for (int64_t t = 0; t < T && idle > 1e-3; ++t) idle *= topk < E ? 1.0 - (double)topk / (double)E : 0.0;
+  int64_t active = (int64_t)((double)E * (1.0 - idle) + 0.5);
+  if (active < 1) active = 1;
+  // Their entries: one each, or, of several, half an entry more than the rows fill (one expert's
+  // last is as full as its rows make it).
+  const int64_t full = (2 * S + (active - 1) * rows + 2 * rows - 1) / (2 * rows);
+  return full > active ? full : active;
+}
+
+// K splits of `tiles` column tiles on workgroups of kStreamWaves waves, one per compute unit at a time,
+// that meet inside the kernel.  In hundredths of a microsecond (MI355X): a k-step of 32 takes a
+// compute unit's waves 100, or what HBM gives where more than half of the units have one (180 with
+// all of them); a round of workgroups 300 beside; and each split its share of the join, by the rows
+// kept.  Measured against forced split counts, us per call in a graph: 1 x 4096 -> 4096 fp16, 4, 8, 12, 16
+// splits 10.4, 8.3, 8.2, 8.9 (12 chosen); 16 x 4096 -> 4096 bf16, 4, 8, 12, 16: 13.0, 12.1, 11.8, 14.0 (8);
+// 4 x 4096 -> 2 x 11008, 3, 4, 5, 6: 20.7, 16.7, 16.4, 23.0 (5); 1 x 11008 -> 4096, 4, 8, 12, 16: 19.2, 13.1,
+// 11.4, 11.9; 16 x 8192 -> 28672, 1, 2, 3, 4: 55.0, 34.9, 42.7, 39.0 (2).
+void choose_splits8(int64_t tiles, int64_t ksteps, bool gated, int rows, int64_t cus, int& splits, int& steps) {
+  const int64_t parts = gated ? kStreamWaves / 2 : kStreamWaves;
+  const int64_t join = (rows == 1 ? 15 : rows <= 8 ? 32 : rows == 16 ? 55 : 75) * (gated ? 2 : 1);
+  int64_t best = -1;
+  for (int64_t want = 1; want <= kExpertMaxSplits; ++want) {
+    const int64_t st = (ksteps + want * parts - 1) / (want * parts);
+    const int64_t sp = (ksteps + st * parts - 1) / (st * parts);
+    const int64_t rounds = (tiles * sp + cus - 1) / cus;
+    const int64_t hbm = 180 * tiles * sp / (rounds * cus);
+    const int64_t cost = rounds * (st * (hbm > 100 ? hbm : 100) + 300) + (sp > 1 ? sp * join : 0);
+    if (best >= 0 && cost >= best) continue;
+    best = cost;
+    steps = (int)st;
+    splits = (int)sp;
+  }
+}
+
 // K splits of a streaming plan.  In tenths of a microsecond (MI355X): a workgroup alone on a
 // compute unit takes 7 per k-step and wave, two together 12, and each round of two 30 for its
 // fixed part, so the busiest compute unit's n workgroups decide; every split also writes and
@@ -486,17 +525,8 @@ int64_t entry_bound(int64_t S, int64_t E, int64_t rows) {
 // over 64 x 2048 -> 1408: 1, 2, 3, 9 splits 65.3, 67.4, 70.5, 71.3 (1 chosen); one expert 4096 ->
 // 4096, 256 rows: 2, 3 splits 33.5, 37.3 (2), 1024 rows: 1, 2 splits 80, 88 (1).
 void choose_splits(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t wide, int64_t cus, bool gated, ExpertPlan& p) {
-  // Experts with rows, about, where a token's are distinct: E (1 - (1 - topk / E)^T).
   const int64_t S = T * topk;
-  double idle = 1.0;
-  for (int64_t t = 0; t < T && idle > 1e-3; ++t) idle *= topk < E ? 1.0 - (double)topk / (double)E : 0.0;
-  int64_t active = (int64_t)((double)E * (1.0 - idle) + 0.5);
-  if (active < 1) active = 1;
-  // Their entries: one each, or, of several, half an entry more than the rows fill (one expert's
-  // last is as full as its rows make it).
-  const int64_t rows = p.block_rows;
-  const int64_t full = (2 * S + (active - 1) * rows + 2 * rows - 1) / (2 * rows);
-  const int64_t entries = full > active ? full : active;
+  const int64_t entries = active_entries(T, topk, E, p.block_rows);
   const int64_t parts = gated ? 2 : 4;  // waves of a workgroup along K
   const int64_t ksteps = K / 32;
   int64_t best = -1;
@@ -600,29 +630,24 @@ int plan_layer(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int
   const int64_t S = T * topk;
   if (S > kExpertRankSlots) return AWQ_ERR_UNSUPPORTED;
   if (cus < 1) cus = 1;
-  p.rows = T <= 4 ? 4 : T <= 8 ? 8 : 16;  // a token goes to an expert once
-  p.router_waves = E <= 32 ? 4 : 1;
-  ExpertPlan up, down;
-  up.block_rows = down.block_rows = 16;
-  up.col_tiles = p.up_tiles = (int)((inner + kExpertStreamCols - 1) / kExpertStreamCols);
-  down.col_tiles = p.down_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
-  choose_splits(T, topk, E, K, 2 * inner, cus, true, up);
-  choose_splits(T, topk, E, inner, N, cus, false, down);
-  p.up_splits = up.splits;
-  p.up_steps = up.steps;
-  p.down_splits = down.splits;
-  p.down_steps = down.steps;
+  p.rows = T == 1 ? 1 : T <= 4 ? 4 : T <= 8 ? 8 : 16;  // a token goes to an expert once
+  p.router_waves = E <= 16 ? 8 : E <= 64 ? 4 : E <= 128 ? 2 : 1;
+  p.up_tiles = (int)((inner + kExpertStreamCols - 1) / kExpertStreamCols);
+  p.down_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
+  const int64_t active = active_entries(T, topk, E, 16);
+  choose_splits8(active * p.up_tiles, K / 32, true, p.rows, cus, p.up_splits, p.up_steps);
+  choose_splits8(active * p.down_tiles, inner / 32, false, p.rows, cus, p.down_splits, p.down_steps);
   const int64_t entries = entry_bound(S, E, 16);
   const int64_t up_items = entries * p.up_tiles * p.up_splits, down_items = entries * p.down_tiles * p.down_splits;
   const int64_t items = up_items > down_items ? up_items : down_items;
   if (up_items >= (int64_t(1) << 30) || down_items >= (int64_t(1) << 30)) return AWQ_ERR_UNSUPPORTED;
-  p.workgroups = items < 2 * (int64_t)cus ? items : 2 * (int64_t)cus;
+  p.workgroups = items < cus ? items : cus;  // one per compute unit
   p.n_counts = (16 + kExpertRankSlots) * kLayerStride + p.down_tiles + (p.up_splits > 1 ? entries * p.up_tiles : 0);
   p.counts_bytes = round_up(p.n_counts * 4, 256);
   p.logits_bytes = round_up(T * E * 4, 256);
   p.ids_bytes = round_up(S * 4, 256);
   p.h_bytes = round_up(2 * S * inner * 2, 256);
-  if (p.up_splits > 1) p.up_bytes = entries * p.up_tiles * p.up_splits * 2 * (p.rows / 4) * 256 * 16;
+  if (p.up_splits > 1) p.up_bytes = round_up(entries * p.up_tiles * p.up_splits * 2 * p.rows * kExpertStreamCols * 4, 256);
   p.down_bytes = round_up(p.down_splits * S * N * 4, 256);
   // 32-bit offsets into h and the sums.
   if (2 * S * inner * 2 >= k2p32 || p.down_splits * S * N * 4 >= k2p32) return AWQ_ERR_UNSUPPORTED;
@@ -645,20 +670,15 @@ int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, boo
   p.stream = M <= kExpertStreamRows || 3 * row_tiles <= cus;
   if (p.stream) {
     if (M * K * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into x
-    ExpertPlan e;
-    p.rows = M <= 4 ? 4 : M <= 8 ? 8 : M <= 16 ? 16 : 32;
-    e.block_rows = p.rows == 32 ? 32 : 16;
-    e.col_tiles = p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
-    choose_splits(M, 1, 1, K, wide, cus, gated, e);
-    p.splits = e.splits;
-    p.steps = e.steps;
-    const int64_t tiles = (M + e.block_rows - 1) / e.block_rows * p.col_tiles;
+    p.rows = M == 1 ? 1 : M <= 4 ? 4 : M <= 8 ? 8 : M <= 16 ? 16 : 32;
+    const int64_t block_rows = p.rows == 32 ? 32 : 16;
+    p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
+    const int64_t tiles = (M + block_rows - 1) / block_rows * p.col_tiles;
+    choose_splits8(tiles, K / 32, gated, p.rows, cus, p.splits, p.steps);
     p.grid = tiles * p.splits;
     if (p.splits > 1) {
-      // Four rows of a column per thread and slot, in every half and block of 16 rows.
-      const int64_t slots = p.rows == 4 ? 1 : p.rows == 8 ? 2 : p.rows == 16 ? 4 : 8;
       p.counter_bytes = tiles * 4;
-      p.sums_bytes = p.grid * slots * (gated ? 2 : 1) * 256 * 16;
+      p.sums_bytes = p.grid * p.rows * (gated ? 2 : 1) * kExpertStreamCols * 4;
     }
   } else {
     // The height of the tiles: rounds of the card times what a tile takes (in hundredths of one of
@@ -676,7 +696,7 @@ int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, boo
     }
     p.col_tiles = (int)tiles_n;
   }
-  return grid_fits(p.grid, 1, p.stream ? 256 : 512) && p.grid < (int64_t(1) << 31) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
+  return grid_fits(p.grid, 1, 512) && p.grid < (int64_t(1) << 31) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
 }
 
 int plan_rtn(int64_t K, int64_t N, int64_t group_size, int sym, RtnPlan& p) {

@@ -240,8 +240,13 @@ struct ExpertsPlan {
   int64_t sorted_bytes = 0, h_bytes = 0, sums_bytes = 0;
   int64_t workspace_bytes() const { return sorted_bytes + h_bytes + sums_bytes; }
 };
+// Waves of a workgroup of awq_gemm_fused and awq_moe_layer: eight, so that a compute unit has as many
+// loads in flight as with two workgroups of four, and half the splits to join.  Four / eight, us per call in
+// a graph, each with its best splits: 1 x 4096 -> 4096 8.6 / 8.4, 19 x 4096 -> 2 x 11008 38 / 31, 200 x 2048 -> 8192
+// 24.0 / 21.6; layers of 7 tokens 64 x 2048 -> 1408 top 8 87 / 69, of one 8 x 4096 -> 14336 top 2 77 / 67.
+constexpr int kStreamWaves = 8;
 // A dense product with its epilogue (awq_gemm_fused).
-//   stream   up to `rows` (4, 8, 16, 32) rows and 256 columns per workgroup, `steps` k-steps per
+//   stream   up to `rows` (1, 4, 8, 16, 32) rows and 256 columns per workgroup, `steps` k-steps per
 //            wave, `splits` K splits that meet over the workspace
 //   else     row tiles of up to `rows` (64, 128, 192, 256) rows
 struct DensePlan {
@@ -260,7 +265,7 @@ int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, boo
 constexpr int kLayerTokens = 8;    // tokens a workgroup of the router kernel takes
 constexpr int kLayerStride = 32;   // 32-bit counts that many workgroups touch: a 128-byte line each
 struct LayerPlan {
-  int rows = 0;          // rows kept per entry: 4, 8 or 16
+  int rows = 0;          // rows kept per entry: 1, 4, 8 or 16
   int router_waves = 1;  // waves per expert
   int up_tiles = 0, up_splits = 1, up_steps = 0, down_tiles = 0, down_splits = 1, down_steps = 0;
   int64_t workgroups = 0;

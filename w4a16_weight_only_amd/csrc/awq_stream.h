@@ -357,38 +357,108 @@ __device__ __forceinline__ void stream_sums(const Share<RB>& s, Ready ready, flo
   }
 }
 
-// Waves along K of a workgroup: all, or gated every other one (even ones the gate's columns, odd
-// ones the up projection's).
-template <bool GATED>
-constexpr int kParts = GATED ? kWaves / 2 : kWaves;
+// Waves along K of a workgroup of WAVES: all, or gated every other one (even ones the gate's columns,
+// odd ones the up projection's).
+template <bool GATED, int WAVES = kWaves>
+constexpr int kParts = GATED ? WAVES / 2 : WAVES;
 
-// The waves' sums of one block of 16 rows, over LDS: sum k of thread i, slot s = i + 256 k, is
-// column entry (s / 16) % 16 of word pair s % 16, rows 4 (s / 256) ...  Only RL lanes' rows are kept.
-// The caller sees to it that nothing else uses red before and after (barriers).
-template <bool GATED, int RL>
-__device__ __forceinline__ void wave_sums(floatx4 (&red)[kWaves][16][RL], const floatx4 (&part)[16],
+// The sums of a column in R adjacent rows (4, or 1 where there is one row in all).
+template <int R>
+struct RowsOf {
+  using type = floatx4;
+};
+template <>
+struct RowsOf<1> {
+  using type = float;
+};
+template <int R>
+using Rows = typename RowsOf<R>::type;
+template <int R>
+__device__ __forceinline__ float row_of(const Rows<R>& v, int r) {
+  if constexpr (R == 1) return v;
+  else return v[r];
+}
+// Slots per thread (see wave_sums).
+template <int RL, int WAVES>
+constexpr int kSlots = (16 * RL + 64 * WAVES - 1) / (64 * WAVES);
+
+// The waves' sums of one block of 16 rows, over LDS: sum k of thread i, slot s = i + 64 WAVES k (of
+// 16 RL), is column entry (s / 16) % 16 of word pair s % 16, rows 4 (s / 256) ...  Only RL lanes' rows are
+// kept.  The caller sees to it that nothing else uses red before and after (barriers).
+template <bool GATED, int RL, int WAVES = kWaves, int R = 4>
+__device__ __forceinline__ void wave_sums(Rows<R> (&red)[WAVES][16][RL], const floatx4 (&part)[16],
                                           const half8v (&unit)[2],
-                                          floatx4 (&sum)[16 * RL / kThreads][GATED ? 2 : 1]) {
+                                          Rows<R> (&sum)[kSlots<RL, WAVES>][GATED ? 2 : 1]) {
+  static_assert(R == 4 || RL == 16, "one row is in the first 16 lanes");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (lane < RL) {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) red[wave][v][lane] = part[v] * (float)unit[v >> 3][col_of(v)];
+    for (int v = 0; v < 16; ++v) {
+      const float u = (float)unit[v >> 3][col_of(v)];
+      if constexpr (R == 1) red[wave][v][lane] = part[v][0] * u;
+      else red[wave][v][lane] = part[v] * u;
+    }
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 16 * RL / kThreads; ++k) {
-    const int i = tid + k * kThreads;
+  for (int k = 0; k < kSlots<RL, WAVES>; ++k) {
+    const int i = 64 * WAVES > 16 * RL ? min(tid, 16 * RL - 1) : tid + k * 64 * WAVES;
     const int v = (i >> 4) & 15, ln = (i >> 8) * 16 + (i & 15);
 #pragma unroll
     for (int hf = 0; hf < (GATED ? 2 : 1); ++hf) {
-      floatx4 a = red[hf][v][ln];
+      Rows<R> a = red[hf][v][ln];
 #pragma unroll
-      for (int w = 1; w < kParts<GATED>; ++w) a += red[GATED ? 2 * w + hf : w][v][ln];
+      for (int w = 1; w < kParts<GATED, WAVES>; ++w) a += red[GATED ? 2 * w + hf : w][v][ln];
       sum[k][hf] = a;
     }
   }
 }
+// R floats to and from where every XCD sees the same.
+template <int R>
+__device__ __forceinline__ void device_store(const __amdgpu_buffer_rsrc_t& rs, uint32_t at, const Rows<R>& v) {
+  if constexpr (R == 1) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rs, at, 0, kCpolDevice);
+  else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at, 0, kCpolDevice);
+}
+template <int R>
+__device__ __forceinline__ Rows<R> device_read(const __amdgpu_buffer_rsrc_t& rs, uint32_t at) {
+  if constexpr (R == 1) return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, kCpolDevice));
+  else return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, kCpolDevice));
+}
+// sum[i] = sum in order of the n Rows at at(split, i), for COUNT of them side by side: the loads of a
+// few splits of all of them go out together (a join is a matter of latency: 19 rows of 4096 -> 2 x 11008, four
+// splits, one sum after another / together: 7 / 2.5 us of the call).
+template <int R, int COUNT, typename At>
+__device__ __forceinline__ void device_sums(const __amdgpu_buffer_rsrc_t& rs, int n, At at, Rows<R> (&sum)[COUNT]) {
+  constexpr int B = COUNT * R >= 32 ? 2 : COUNT * R >= 8 ? 4 : 8;
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) sum[i] = Rows<R>{};
+  int s0 = 0;
+  for (; s0 + B <= n; s0 += B) {
+    Rows<R> v[COUNT][B];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+      for (int j = 0; j < B; ++j) v[i][j] = device_read<R>(rs, at(s0 + j, i));
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+      for (int j = 0; j < B; ++j) sum[i] += v[i][j];
+  }
+  if (s0 < n) {  // the last few: those past the last read it again and are dropped
+    Rows<R> v[COUNT][B - 1];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+      for (int j = 0; j < B - 1; ++j) v[i][j] = device_read<R>(rs, at(min(s0 + j, n - 1), i));
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+      for (int j = 0; j < B - 1; ++j)
+        if (s0 + j < n) sum[i] += v[i][j];
+  }
+}
+
 // Column within the tile of slot s (see wave_sums), its first row within the block.
 __device__ __forceinline__ int slot_col(int s) {
   const int v = (s >> 4) & 15;
