@@ -493,7 +493,7 @@ int64_t active_entries(int64_t T, int64_t topk, int64_t E, int64_t rows) {
 
 // K splits of `tiles` column tiles on workgroups of kStreamWaves waves, one per compute unit at a time,
 // that meet inside the kernel.  In hundredths of a microsecond (MI355X): a k-step of 32 takes a
-// compute unit's waves 100, or what HBM gives where more than half of the units have one (180 with
+// compute unit's waves 100, or what HBM gives where more than half of the units have one (160 with
 // all of them); a round of workgroups 300 beside; and each split its share of the join, by the rows
 // kept.  Measured against forced split counts, us per call in a graph: 1 x 4096 -> 4096 fp16, 4, 8, 12, 16
 // splits 10.4, 8.3, 8.2, 8.9 (12 chosen); 16 x 4096 -> 4096 bf16, 4, 8, 12, 16: 13.0, 12.1, 11.8, 14.0 (8);
@@ -501,13 +501,15 @@ int64_t active_entries(int64_t T, int64_t topk, int64_t E, int64_t rows) {
 // 11.4, 11.9; 16 x 8192 -> 28672, 1, 2, 3, 4: 55.0, 34.9, 42.7, 39.0 (2).
 void choose_splits8(int64_t tiles, int64_t ksteps, bool gated, int rows, int64_t cus, int& splits, int& steps) {
   const int64_t parts = gated ? kStreamWaves / 2 : kStreamWaves;
-  const int64_t join = (rows == 1 ? 15 : rows <= 8 ? 32 : rows == 16 ? 55 : 75) * (gated ? 2 : 1);
-  int64_t best = -1;
-  for (int64_t want = 1; want <= kExpertMaxSplits; ++want) {
+  const int64_t join = (rows == 1 ? 15 : rows <= 8 ? 32 : rows == 16 ? 45 : 75) * (gated ? 2 : 1);
+  int64_t best = -1, last = 0;
+  for (int64_t want = 1; want <= kExpertMaxSplits && last != 1; ++want) {
     const int64_t st = (ksteps + want * parts - 1) / (want * parts);
+    if (best >= 0 && st == last) continue;  // the same splits
+    last = st;
     const int64_t sp = (ksteps + st * parts - 1) / (st * parts);
     const int64_t rounds = (tiles * sp + cus - 1) / cus;
-    const int64_t hbm = 180 * tiles * sp / (rounds * cus);
+    const int64_t hbm = 160 * tiles * sp / (rounds * cus);
     const int64_t cost = rounds * (st * (hbm > 100 ? hbm : 100) + 300) + (sp > 1 ? sp * join : 0);
     if (best >= 0 && cost >= best) continue;
     best = cost;
@@ -581,9 +583,11 @@ int plan_expert(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t N, int cu
 
 }  // namespace
 
-int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
-                 int cus, bool up, bool down, ExpertsPlan& p) {
-  p = ExpertsPlan{};
+namespace {
+
+// The sizes of one or both products of routed experts.
+int check_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size, bool up,
+                  bool down) {
   if (T < 0 || topk < 1 || E < 1) return AWQ_ERR_SHAPE;
   if (inner < 1 || inner > kMaxDim) return inner < 1 ? AWQ_ERR_SHAPE : AWQ_ERR_UNSUPPORTED;
   if (T > kMaxDim || topk > kMaxDim || E > 1024) return AWQ_ERR_UNSUPPORTED;
@@ -601,6 +605,17 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
     if (st != AWQ_OK) return st;
     if (T * (N / 4) + 256 >= k2p32) return AWQ_ERR_UNSUPPORTED;  // one thread per four outputs
   }
+  return AWQ_OK;
+}
+
+}  // namespace
+
+int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size,
+                 int cus, bool up, bool down, ExpertsPlan& p) {
+  p = ExpertsPlan{};
+  const int ok = check_experts(T, topk, E, K, inner, N, group_size, up, down);
+  if (ok != AWQ_OK) return ok;
+  const int64_t S = T * topk;
   if (T == 0) return AWQ_OK;
   if (cus < 1) cus = 1;
   if (up) {
@@ -624,11 +639,11 @@ int plan_experts(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, i
 int plan_layer(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int64_t N, int64_t group_size, int cus,
                LayerPlan& p) {
   p = LayerPlan{};
-  ExpertsPlan sizes;  // every check of the products
-  int st = plan_experts(T, topk, E, K, inner, N, group_size, cus, true, true, sizes);
+  int st = check_experts(T, topk, E, K, inner, N, group_size, true, true);
   if (st != AWQ_OK || T == 0) return st;
   const int64_t S = T * topk;
   if (S > kExpertRankSlots) return AWQ_ERR_UNSUPPORTED;
+  if (K * inner >= k2p32 - 4096 || inner * (N / 2) >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // one expert's weight
   if (cus < 1) cus = 1;
   p.rows = T == 1 ? 1 : T <= 4 ? 4 : T <= 8 ? 8 : 16;  // a token goes to an expert once
   p.router_waves = E <= 16 ? 8 : E <= 64 ? 4 : E <= 128 ? 2 : 1;

@@ -1,8 +1,8 @@
 """Dense products with their epilogue: torch tensors in, C ABI calls out.
 
 Work runs on the current stream of the tensors' device.  Where K is split, a call needs scratch
-memory, which comes from torch's allocator on that stream, and counters that are zero between
-calls (counters.py), so calls may be captured into graphs without a call before.
+memory, and counters that are zero between calls (scratch.py); calls may be captured into graphs
+without a call before.
 """
 from __future__ import annotations
 
@@ -11,9 +11,9 @@ import ctypes
 import torch
 
 from . import _lib
-from .counters import zeroed_counters
 from .linear import _check_tensor, validate
-from .moe import _TYPES, _call, _is, _output
+from .moe import _TYPES, _is, _output
+from .scratch import counters_and_scratch
 
 _ACTIVATIONS = {None: _lib.AWQ_ACT_NONE, "relu": _lib.AWQ_ACT_RELU, "silu": _lib.AWQ_ACT_SILU,
                 "gelu": _lib.AWQ_ACT_GELU, "gelu_tanh": _lib.AWQ_ACT_GELU_TANH}
@@ -22,12 +22,12 @@ _plans = {}  # (workspace, counter) bytes by device and the call's sizes
 
 
 def _plan(device, *sizes):
+    """(workspace, counter) bytes of these sizes on the device, the current one."""
     key = (device.index, sizes)
     need = _plans.get(key)
     if need is None:
         ws, count = ctypes.c_int64(), ctypes.c_int64()
-        with torch.cuda.device(device):
-            status = _lib.load().awq_gemm_fused_plan(*sizes, ctypes.byref(ws), ctypes.byref(count))
+        status = _lib.load().awq_gemm_fused_plan(*sizes, ctypes.byref(ws), ctypes.byref(count))
         _lib.check(status, "awq_gemm_fused_plan")
         if len(_plans) >= 4096:
             _plans.clear()
@@ -87,13 +87,31 @@ def awq_gemm_fused(x: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
         if residual.shape != shape:
             raise ValueError(f"residual must be {list(shape)}")
     M = x.numel() // K
-    out = _output(out, shape, dtype, dev)
-    ws_bytes, count_bytes = _plan(dev, M, K, N, group_size, 1 if gated else 0)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    counters = zeroed_counters(dev, count_bytes) if count_bytes else None
-    _call(_lib.load().awq_gemm_fused, "awq_gemm_fused", dev, x.data_ptr(), _TYPES[dtype], qweight.data_ptr(),
-          qzeros.data_ptr(), scales.data_ptr(), None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation],
-          1 if gated else 0, None if residual is None else residual.data_ptr(), scale, M, K, N, group_size,
-          out.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes,
-          None if counters is None else counters.data_ptr(), count_bytes)
+    if out is None:
+        out = torch.empty_like(residual) if residual is not None else torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        out = _output(out, shape, dtype, dev)
+    sizes = (M, K, N, group_size, 1 if gated else 0)
+    if torch.cuda.current_device() == dev.index:
+        _launch(x, qweight, qzeros, scales, bias, activation, residual, scale, out, sizes)
+    else:
+        with torch.cuda.device(dev):
+            _launch(x, qweight, qzeros, scales, bias, activation, residual, scale, out, sizes)
     return out
+
+
+def _launch(x, qweight, qzeros, scales, bias, activation, residual, scale, out, sizes):
+    dev = x.device
+    M, K, N, group_size, gated = sizes
+    ws_bytes, count_bytes = _plan(dev, *sizes)
+    counters = ws = hold = None
+    if count_bytes:
+        counters, ws, hold = counters_and_scratch(dev, count_bytes, ws_bytes)
+    status = _lib.load().awq_gemm_fused(
+        x.data_ptr(), _TYPES[x.dtype], qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
+        None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation], gated,
+        None if residual is None else residual.data_ptr(), scale, M, K, N, group_size, out.data_ptr(), ws, ws_bytes,
+        counters, count_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != 0:
+        _lib.check(status, "awq_gemm_fused")
+    del hold

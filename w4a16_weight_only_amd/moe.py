@@ -11,8 +11,8 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .counters import zeroed_counters
 from .linear import _check_tensor, validate
+from .scratch import counters_and_scratch
 
 _TYPES = {torch.float16: _lib.AWQ_F16, torch.bfloat16: _lib.AWQ_BF16, torch.float32: _lib.AWQ_F32}
 _SCORES = {"softmax": _lib.AWQ_SOFTMAX, "sigmoid": _lib.AWQ_SIGMOID}
@@ -295,17 +295,32 @@ def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: t
             _check_tensor("residual", residual, x.dtype, dev)
         if residual.shape != (T, N):
             raise ValueError(f"residual must be [{T}, {N}]")
-    out = _output(out, (T, N), x.dtype, dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=x.dtype, device=dev)
+    else:
+        out = _output(out, (T, N), x.dtype, dev)
     need = _layer_workspace(dev, T, topk, E, K, inner, N, group_size)
     if need < 0:
         _lib.check(need, "awq_moe_layer_workspace")
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    counters = zeroed_counters(dev, _lib.AWQ_MOE_LAYER_COUNTERS)
-    _call(_lib.load().awq_moe_layer, "awq_moe_layer", dev, x.data_ptr(), _TYPES[x.dtype], router.data_ptr(),
-          _TYPES[router.dtype], 1 if round_logits else 0, None if bias is None else bias.data_ptr(), _SCORES[score],
-          groups, topk_groups, group_top, topk, 1 if renormalize else 0, scale, *[t.data_ptr() for t in gate_up],
-          *[t.data_ptr() for t in down], None if residual is None else residual.data_ptr(), T, E, K, inner, N,
-          group_size, out.data_ptr(), ws.data_ptr(), need, counters.data_ptr(), _lib.AWQ_MOE_LAYER_COUNTERS)
+
+    def launch():
+        counters, ws, hold = counters_and_scratch(dev, _lib.AWQ_MOE_LAYER_COUNTERS, need)
+        status = _lib.load().awq_moe_layer(
+            x.data_ptr(), _TYPES[x.dtype], router.data_ptr(), _TYPES[router.dtype], 1 if round_logits else 0,
+            None if bias is None else bias.data_ptr(), _SCORES[score], groups, topk_groups, group_top, topk,
+            1 if renormalize else 0, scale, *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down],
+            None if residual is None else residual.data_ptr(), T, E, K, inner, N, group_size, out.data_ptr(), ws, need,
+            counters, _lib.AWQ_MOE_LAYER_COUNTERS, torch._C._cuda_getCurrentRawStream(dev.index))
+        del hold
+        return status
+
+    if torch.cuda.current_device() == dev.index:
+        status = launch()
+    else:
+        with torch.cuda.device(dev):
+            status = launch()
+    if status != 0:
+        _lib.check(status, "awq_moe_layer")
     return out
 
 

@@ -15,6 +15,10 @@ def _rows(name, t, dtypes, device=None):
     2-D with adjacent elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype in dtypes and t.is_cuda and t.is_contiguous() and (device is None or t.device == device):
+        shape = t.shape
+        if len(shape) == 2 and shape[1] >= 1:
+            return shape
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.device.type != "cuda":
@@ -65,9 +69,11 @@ def _run(x, residual, weight, bias, gate, scale, post_weight, post_bias, kind, e
             raise ValueError(f"gate must be [{H}], or [B, {H}] with B a divisor of the {T} rows")
     vectors = [_vector(n, t, H, dtype, dev) for n, t in (("post_weight", post_weight), ("post_bias", post_bias),
                                                          ("weight", weight), ("bias", bias))]
-    y = _output(y, x.shape, dtype, dev)
+    whole = x_stride == H  # then x is contiguous
+    y = torch.empty_like(x) if y is None and whole else _output(y, x.shape, dtype, dev)
     if keep_r:
-        r = _output(r, x.shape, stream_type, dev)
+        whole = residual_stride == H
+        r = torch.empty_like(residual) if r is None and whole else _output(r, x.shape, stream_type, dev)
     _call(_lib.load().awq_add_norm, "awq_add_norm", dev, x.data_ptr(), _TYPES[dtype], T, H, x_stride,
           None if residual is None else residual.data_ptr(), _TYPES[stream_type], residual_stride,
           None if gate is None else gate.data_ptr(), gates, scale, *vectors, _KINDS[kind], 1 if unit_offset else 0, eps,
