@@ -178,8 +178,9 @@ struct LayerArgs {
   int router_waves;  // waves per expert of the first kernel: 1 or 4
   int up_tiles, up_splits, up_steps, down_tiles, down_splits, down_steps;
   bool bf16, router32, round_logits;
+  bool route_inside;  // set by the launch: the second kernel routes
 };
-hipError_t launch_layer(const LayerArgs& a, RouteArgs r, const LayerPlan& p, hipStream_t stream);
+hipError_t launch_layer(LayerArgs a, const RouteArgs& r, const LayerPlan& p, hipStream_t stream);
 
 // Norms on the residual stream (awq_add_norm).  x, gate, weights, biases and y are fp16 or (bf16)
 // bfloat16; residual and r too, or (r32) fp32.  Strides in elements; gate row t / gate_rows.

@@ -2,8 +2,9 @@
 //   y[t] = residual[t] + sum over j of weights[t, j] * down[e](silu(gate[e](x[t])) * up[e](x[t])),
 //   e and weights of slot (t, j) from the logits x . router^T
 //
-// layer_router_kernel: a wave per expert (four for few experts) forms the logits of eight tokens; the
-// workgroup that finishes last routes those tokens, a wave per token (awq_route.h).
+// layer_router_kernel: a wave per expert (up to eight for few experts) forms the logits of eight tokens;
+// the workgroup that finishes last routes those tokens, a wave per token (awq_route.h), where the
+// next kernel does not.
 //
 // layer_kernel: both products, streamed (awq_stream.h) in items of (up to 16 slots of one expert, 256
 // columns, K split).  Workgroups take the items of the gated product first, then those of the
@@ -11,6 +12,8 @@
 //   - Splits of a gated tile meet in the workspace; the last to arrive adds them in order and writes h.
 //   - An item of the second product waits until h of its slots is whole, with its first weights already
 //     on their way.
+//   - One token: no one joins the splits for all; an item of the second product adds and gates what it
+//     multiplies.
 //   - The last item of a column tile of the second product adds the slots and splits of every token in a fixed
 //     order, and the residual, and writes y.
 // What workgroups hand to each other goes through to, and comes from, where every XCD's L2 sees the
@@ -116,6 +119,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void layer_router_kernel(const L
     if (a.round_logits) v = a.bf16 ? act_to_float<true>(float_to_act<true>(v)) : act_to_float<false>(float_to_act<false>(v));
     __hip_atomic_store(a.logits + (int64_t)(t0 + lane) * a.E + e, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  if (a.route_inside) return;
   stores_done();
   __syncthreads();
   if (tid == 0) {
@@ -153,7 +157,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void layer_router_kernel(const L
 
 // RL: lanes whose rows are kept, 16 per four rows; R: 1 for one token.
 template <bool BF16, int RL, int R>
-__global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const LayerArgs a) {
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const LayerArgs a, const RouteArgs r) {
   constexpr int WAVES = kStreamWaves, THREADS = 64 * WAVES;
   constexpr int SLOTS = kSlots<RL, WAVES>;
   constexpr int kEntryRows = 16;
@@ -161,8 +165,10 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
     Rows<R> red[WAVES][16][RL];
     float ys[RL / 4][kYld];
   } sh;
+  __shared__ __attribute__((aligned(16))) uint16_t hs[2][R == 1 ? kLayerCols : 8];
   __shared__ int32_t slots[kEntryRows], ids[kExpertRankSlots];
   __shared__ float weights[kExpertRankSlots];
+  __shared__ route::Scratch<float, 64, 1, false> chosen[WAVES];
   __shared__ int taken;
   __shared__ uint32_t last_arrival;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -229,11 +235,46 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
   };
 
   // Slots by expert, one per lane, in every wave: blocks of 16 slots of one expert are entries.
-  Ticket ticket = ask(up_tickets);
-  const int id = lane < S ? a.ids[lane] : -1;
-  if (wave == 0) {
-    ids[lane] = id;
-    weights[lane] = lane < S ? a.weights[lane] : 0.f;
+  // What routing needs is asked for first: loads come back in order, and the tickets' atomics take longer.
+  Ticket ticket;
+  int id;
+  if (a.route_inside) {
+    // A wave per token; the LDS accesses of a wave are its own and in order.  (Where the first kernel
+    // routes, us: one token 64 x 2048 -> 1408 33.4, here 32.6; one of 8 x 4096 -> 14336 64.1, 63.4.)
+    if (wave < a.T) {
+      auto route = [&](auto vpl) {
+        constexpr int VPL = decltype(vpl)::value;
+        float l[VPL];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+          const int e = lane * VPL + j;
+          l[j] = a.logits[(int64_t)wave * a.E + min(e, a.E - 1)];
+        }
+        ticket = ask(up_tickets);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) l[j] = lane * VPL + j < a.E ? l[j] : -__builtin_inff();
+        route::route_tokens<float, float, 64, VPL, false>(
+            r, l, [&](int e) { return a.logits[(int64_t)wave * a.E + e]; },
+            [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); },
+            chosen[wave], true,
+            [&](int j, int e, float weight) {
+              ids[wave * a.topk + j] = e;
+              weights[wave * a.topk + j] = weight;
+            });
+      };
+      if (a.E <= 64) route(std::integral_constant<int, 1>{});
+      else route(std::integral_constant<int, 4>{});
+    }
+    __syncthreads();
+    id = lane < S ? ids[lane] : -1;
+  } else {
+    id = lane < S ? a.ids[lane] : -1;
+    const float weight = lane < S ? a.weights[lane] : 0.f;
+    ticket = ask(up_tickets);
+    if (wave == 0 && lane < S) {
+      ids[lane] = id;
+      weights[lane] = weight;
+    }
   }
   const Ranks ranks = rank_slots<kEntryRows>(id, a.E);
   const int entries = ranks.entries;
@@ -295,6 +336,12 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
   const __amdgpu_buffer_rsrc_t hrs = __builtin_amdgcn_make_buffer_rsrc(
       a.h, (short)0, (int)(2u * (uint32_t)S * (uint32_t)a.inner * 2u), 0x00020000);
   const uint32_t rest_at = (uint32_t)S * (uint32_t)a.inner * 2u;  // the second term's bytes
+  // One token: the gated product's sums, [slot][split][half][column].
+  const __amdgpu_buffer_rsrc_t grs = __builtin_amdgcn_make_buffer_rsrc(
+      a.up_sums, (short)0, (int)((uint32_t)(S * a.up_splits) * 2u * (uint32_t)a.inner * 4u), 0x00020000);
+  auto gate_at = [&](int slot, int split, int hf, int n) {
+    return ((uint32_t)((slot * a.up_splits + split) * 2 + hf) * (uint32_t)a.inner + (uint32_t)n) * 4u;
+  };
 
   // ---- The gated product.
   Ticket next;  // of the second product
@@ -318,8 +365,24 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
     half8v unit[2];
     stream_sums<BF16, 1, false>(share, Now{}, part, unit);
     ticket = ask(up_tickets);
+    if (!asked) next = ask(down_tickets);
+    asked = true;
     Rows<R> sum[SLOTS][2];
     wave_sums<true, RL, WAVES, R>(sh.red, part[0], unit, sum);
+    if constexpr (R == 1) {
+      // One token: its sums leave as they are, by column, and whoever takes a part of the second product
+      // joins what it needs of them.
+      const int n = tile * kExpertStreamCols + slot_col(tid);
+      if (tid < 16 * RL && n < N) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) device_store<1>(grs, gate_at(slots[0], split, hf, n), sum[0][hf]);
+      }
+      stores_done();
+      __syncthreads();
+      if (tid == 0) count_in(ready + kLayerStride * entry);
+      __syncthreads();
+      continue;
+    }
     bool mine = true;
     if (a.up_splits > 1) {
       constexpr uint32_t kShare = 2u * 16 * RL * 4u * R;
@@ -346,8 +409,6 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
     } else {
       __syncthreads();  // the sums are in registers: their LDS takes h
     }
-    if (!asked) next = ask(down_tickets);
-    asked = true;
     if (mine) {
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k) {
@@ -400,9 +461,10 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
     share.kb = min(K / 32, (split * kParts<false, WAVES> + wave) * a.down_steps);
     share.ke = min(K / 32, share.kb + a.down_steps);
     bool whole = true;
+    const uint32_t parts_of_h = (uint32_t)(R == 1 ? a.up_tiles * a.up_splits : a.up_tiles);
     auto wait = [&] {
       uint32_t polls = 0;
-      while (load_count(ready + kLayerStride * entry) < (uint32_t)a.up_tiles) {
+      while (load_count(ready + kLayerStride * entry) < parts_of_h) {
         if (++polls == kMaxPolls) {
           whole = false;
           break;
@@ -413,7 +475,35 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
     };
     floatx4 part[1][16];
     half8v unit[2];
-    stream_sums<BF16, 1, true>(share, wait, part, unit);
+    if constexpr (R == 1) {
+      // This split's part of h, joined and gated into LDS; four columns a thread at a time.
+      const int k0 = split * WAVES * a.down_steps * 32, cols = min(K - k0, WAVES * a.down_steps * 32);
+      const int slot = slots[0];
+      auto join = [&] {
+        wait();
+        for (int c0 = tid; c0 < cols; c0 += 4 * THREADS) {
+          float flat[8];
+          device_sums<1>(grs, a.up_splits, [&](int sp, int i) {
+            return gate_at(slot, sp, i & 1, k0 + min(c0 + (i >> 1) * THREADS, cols - 1));
+          }, flat);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = c0 + j * THREADS;
+            const float h = gated(flat[2 * j], flat[2 * j + 1]);
+            if (at < cols) {
+              hs[0][at] = float_to_act<BF16>(h);
+              hs[1][at] = float_to_act<BF16>(rest_of<BF16>(h));
+            }
+          }
+        }
+        __syncthreads();
+      };
+      stream_sums<BF16, 1, true>(share, join, part, unit, [&](int k, bool rest) {
+        return *reinterpret_cast<const half8v*>(&hs[rest][k - k0]);
+      });
+    } else {
+      stream_sums<BF16, 1, true>(share, wait, part, unit);
+    }
     next = ask(down_tickets);
     if (!whole) {
 #pragma unroll
@@ -444,8 +534,11 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
   }
 }
 
-hipError_t launch_layer(const LayerArgs& a, RouteArgs r, const LayerPlan& p, hipStream_t stream) {
+hipError_t launch_layer(LayerArgs a, const RouteArgs& r, const LayerPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((a.E * a.router_waves + kRouterWaves - 1) / kRouterWaves), (unsigned)((a.T + kLayerTokens - 1) / kLayerTokens));
+  // Routing by the logits alone, of few tokens and experts, takes every workgroup of the second kernel
+  // less time than handing the ids over takes the first.
+  a.route_inside = r.bias == nullptr && r.groups == 1 && a.E <= 256 && a.T <= kStreamWaves;
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kRouterThreads), 0, stream, a, r); };
   auto sized = [&](auto key, auto worth, auto groups) {
     using Key = decltype(key);
@@ -464,7 +557,7 @@ hipError_t launch_layer(const LayerArgs& a, RouteArgs r, const LayerPlan& p, hip
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   auto main_kernel = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)p.workgroups), dim3(64 * kStreamWaves), 0, stream, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)p.workgroups), dim3(64 * kStreamWaves), 0, stream, a, r);
   };
   auto by_rows = [&](auto bf16) {
     constexpr bool B = decltype(bf16)::value;

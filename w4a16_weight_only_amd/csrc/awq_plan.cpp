@@ -652,20 +652,22 @@ int plan_layer(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int
   const int64_t active = active_entries(T, topk, E, 16);
   choose_splits8(active * p.up_tiles, K / 32, true, p.rows, cus, p.up_splits, p.up_steps);
   choose_splits8(active * p.down_tiles, inner / 32, false, p.rows, cus, p.down_splits, p.down_steps);
+  if (p.rows == 1 && p.down_steps * kStreamWaves * 32 > kLayerCols) p.rows = 4;
   const int64_t entries = entry_bound(S, E, 16);
   const int64_t up_items = entries * p.up_tiles * p.up_splits, down_items = entries * p.down_tiles * p.down_splits;
   const int64_t items = up_items > down_items ? up_items : down_items;
   if (up_items >= (int64_t(1) << 30) || down_items >= (int64_t(1) << 30)) return AWQ_ERR_UNSUPPORTED;
   p.workgroups = items < cus ? items : cus;  // one per compute unit
-  p.n_counts = (16 + kExpertRankSlots) * kLayerStride + p.down_tiles + (p.up_splits > 1 ? entries * p.up_tiles : 0);
+  p.n_counts = (16 + kExpertRankSlots) * kLayerStride + p.down_tiles + (p.up_splits > 1 && p.rows > 1 ? entries * p.up_tiles : 0);
   p.counts_bytes = round_up(p.n_counts * 4, 256);
   p.logits_bytes = round_up(T * E * 4, 256);
   p.ids_bytes = round_up(S * 4, 256);
   p.h_bytes = round_up(2 * S * inner * 2, 256);
-  if (p.up_splits > 1) p.up_bytes = round_up(entries * p.up_tiles * p.up_splits * 2 * p.rows * kExpertStreamCols * 4, 256);
+  if (p.rows == 1) p.up_bytes = round_up(S * p.up_splits * 2 * inner * 4, 256);
+  else if (p.up_splits > 1) p.up_bytes = round_up(entries * p.up_tiles * p.up_splits * 2 * p.rows * kExpertStreamCols * 4, 256);
   p.down_bytes = round_up(p.down_splits * S * N * 4, 256);
   // 32-bit offsets into h and the sums.
-  if (2 * S * inner * 2 >= k2p32 || p.down_splits * S * N * 4 >= k2p32) return AWQ_ERR_UNSUPPORTED;
+  if (2 * S * inner * 2 >= k2p32 || p.down_splits * S * N * 4 >= k2p32 || p.up_bytes >= k2p32) return AWQ_ERR_UNSUPPORTED;
   return AWQ_OK;
 }
 

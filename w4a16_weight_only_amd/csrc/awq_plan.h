@@ -264,6 +264,7 @@ int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, boo
 // order: counts, logits, ids, weights, h, and the sums of both products' splits.
 constexpr int kLayerTokens = 8;    // tokens a workgroup of the router kernel takes
 constexpr int kLayerStride = 32;   // 32-bit counts that many workgroups touch: a 128-byte line each
+constexpr int kLayerCols = 8192;   // columns of h that a split of one token's second product takes at most
 struct LayerPlan {
   int rows = 0;          // rows kept per entry: 1, 4, 8 or 16
   int router_waves = 1;  // waves per expert

@@ -51,13 +51,15 @@ struct Two {
 };
 
 // LDS of the tokens of one wave.
-template <typename Worth, int LPT, int VPL, bool GROUPS>
-struct Scratch {
+template <typename Worth, int LPT, int KEYS>
+struct ScratchOf {
   static constexpr int kTokens = 64 / LPT;
-  Worth keys[GROUPS ? kTokens : 1][GROUPS ? LPT * VPL : 1];
-  Worth worth[GROUPS ? kTokens : 1][kRouteMaxGroups];
+  Worth keys[KEYS > 1 ? kTokens : 1][KEYS];
+  Worth worth[KEYS > 1 ? kTokens : 1][kRouteMaxGroups];
   int chosen[kTokens][kRouteMaxTopk];
 };
+template <typename Worth, int LPT, int VPL, bool GROUPS>
+using Scratch = ScratchOf<Worth, LPT, GROUPS ? LPT * VPL : 1>;
 
 // Key: float (keys are the logits) or double (keys are choices).  Worth, of groups: float (their
 // best logit) or double (choices).  GROUPS: expert groups.  One token per LPT lanes of a wave: l holds

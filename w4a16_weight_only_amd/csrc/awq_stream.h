@@ -194,11 +194,15 @@ __device__ __forceinline__ half8v device_load(const uint16_t* base, uint64_t at)
   return __builtin_bit_cast(half8v, __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)at, 0, kCpolDevice));
 }
 
+struct NoSource {};
+
 // part[rb][v] * unit: sums of entry v's column and four rows (4 (lane / 16) ..) of block rb.
-// ready(): called before anything of x is read, behind the first loads of the weights.
-template <bool BF16, int RB, bool REST, typename Ready>
+// ready(): called by every wave before anything of x is read, behind the first loads of the weights.
+// source(k, rest), if given, is x[k ..] (or the second term's) of every row in place of memory.
+template <bool BF16, int RB, bool REST, typename Ready, typename Source = NoSource>
 __device__ __forceinline__ void stream_sums(const Share<RB>& s, Ready ready, floatx4 (&part)[RB][16],
-                                            half8v (&unit)[2]) {
+                                            half8v (&unit)[2], Source source = Source{}) {
+  constexpr bool kSource = !__is_same(Source, NoSource);
   constexpr bool kWaits = !__is_same(Ready, Now);
   const int q = (threadIdx.x & 63) >> 4;
   const int K = s.K, NW = s.NW, wc = s.wc, gsteps = s.g / 32, kb = s.kb, ke = s.ke;
@@ -244,7 +248,12 @@ __device__ __forceinline__ void stream_sums(const Share<RB>& s, Ready ready, flo
     const uint32_t r0 = !kAlways || ks < ke ? (uint32_t)ks * 32u : 0u;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-      const uint64_t at = (uint64_t)s.x_off[rb] + r0 * 2u;
+      [[maybe_unused]] const uint64_t at = (uint64_t)s.x_off[rb] + r0 * 2u;
+      if constexpr (kSource) {
+        st.x[rb] = source((int)r0 + 8 * q, false);
+        if constexpr (REST) st.rest[rb] = source((int)r0 + 8 * q, true);
+        continue;
+      }
       if constexpr (kWaits) {  // written by this kernel's other workgroups
         st.x[rb] = device_load(s.x, at);
         if constexpr (REST) st.rest[rb] = device_load(s.x_rest, at);
