@@ -438,7 +438,7 @@ int awq_gemm_fused(const void* x, int act, const int32_t* qweight, const int32_t
  *                rows of x (1: all of them, T: each its own; T % gates == 0)
  *   post_weight, post_bias, weight, bias   device [H] of act; all but weight may be NULL
  *                (post_bias needs post_weight)
- *   y            device [T, H] of act
+ *   y            device [T, H] of act; or NULL, and weight and bias too: r alone is wanted
  *   r            device [T, H] of residual_type, or NULL: not written
  * Pointers need their element's alignment only; rows that all begin on 16 bytes, with H % 8 == 0,
  * are read and written 16 bytes at a time.  Sums, statistics and r are fp32; r and y are rounded

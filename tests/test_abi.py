@@ -283,7 +283,8 @@ def test_norm_argument_errors_touch_no_device(lib):
     assert call(gate=base * 6, gates=3) == call(gate=base * 6, gates=0) == _lib.AWQ_ERR_SHAPE
     assert call(H=32769, xs=32769, rs=32769) == call(T=(1 << 24) + 1) == _lib.AWQ_ERR_UNSUPPORTED
     assert call(act=2) == call(rt=1) == call(kind=2) == _lib.AWQ_ERR_UNSUPPORTED
-    assert call(x=None) == call(w=None) == call(y=None) == call(pb=base * 6) == _lib.AWQ_ERR_NULL
+    assert call(x=None) == call(w=None) == call(y=None, r=None) == call(pb=base * 6) == _lib.AWQ_ERR_NULL
+    assert call(y=None, b=base * 6) == _lib.AWQ_ERR_NULL
     assert call(x=base + 1) == call(rt=2, res=base * 2 + 2) == call(rt=2, r=base * 5 + 2) == _lib.AWQ_ERR_ALIGN
     # y in x's place or r in residual's would be taken; every other overlap is not.
     assert call(y=base + 2) == call(y=base * 2) == call(r=base) == call(r=base * 4 + 510) == _lib.AWQ_ERR_UNSUPPORTED

@@ -11,6 +11,7 @@ from .moe import (  # noqa: F401
     AwqMoe, awq_moe_down, awq_moe_gate_up, awq_moe_layer, awq_moe_mlp, awq_moe_route,
 )
 from .fused import awq_gemm_fused  # noqa: F401
+from .mlp import AwqMlp  # noqa: F401
 from .norm import awq_add_norm, awq_norm  # noqa: F401
 from .linear import (  # noqa: F401
     AwqLinear, awq_dequant, awq_gemm, awq_moe_align, awq_moe_gemm, awq_quantize_rtn, group_size_from_config, plan, validate,

@@ -512,7 +512,7 @@ int awq_add_norm(const void* x, int act, int64_t T, int64_t H, int64_t x_stride,
   if (kind != AWQ_RMS && kind != AWQ_LAYER) return AWQ_ERR_UNSUPPORTED;
   if (gate && gates == 0) return AWQ_ERR_SHAPE;
   if (T == 0) return AWQ_OK;
-  if (!x || !weight || !y || (post_bias && !post_weight)) return AWQ_ERR_NULL;
+  if (!x || (!y && !r) || (y && !weight) || (post_bias && !post_weight) || (bias && !y)) return AWQ_ERR_NULL;
   const uintptr_t unit = r32 ? 4 : 2;
   for (const void* p : {x, gate, post_weight, post_bias, weight, bias, (const void*)y})
     if (reinterpret_cast<uintptr_t>(p) % 2 != 0) return AWQ_ERR_ALIGN;

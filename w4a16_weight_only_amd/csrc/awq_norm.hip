@@ -137,7 +137,7 @@ __global__ __launch_bounds__(norm_threads(WAVES)) void norm_kernel(const NormArg
     if (has_post) pw[p] = at.load16(a.post_weight);
     if (has_pb) pb[p] = at.load16(a.post_bias);
     if (has_gate) gw[p] = at.load16(gate);
-    ww[p] = at.load16(a.weight);
+    if (a.y != nullptr) ww[p] = at.load16(a.weight);
     if (has_bias) bw[p] = at.load16(a.bias);
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -193,6 +193,7 @@ __global__ __launch_bounds__(norm_threads(WAVES)) void norm_kernel(const NormArg
       else at.template store16<BF16>(static_cast<uint16_t*>(a.r) + t * H, r[p]);
     }
   }
+  if (a.y == nullptr) return;
   float mean, inv;
   statistics(r, 2, mean, inv);
 #pragma unroll

@@ -240,17 +240,24 @@ def awq_moe_gemm(x: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor, s
 
 
 class AwqLinear(torch.nn.Module):
-    """Inference-only linear layer holding one AWQ GEMM-layout weight."""
+    """Inference-only linear layer holding one AWQ GEMM-layout weight.  activation (awq_gemm_fused's) is
+    applied to the product, and forward's residual, of the output's shape, added to it, in the
+    same kernel."""
 
-    def __init__(self, qweight, qzeros, scales, bias=None, group_size=128):
+    def __init__(self, qweight, qzeros, scales, bias=None, group_size=128, activation=None):
         super().__init__()
         self.register_buffer("qweight", qweight)
         self.register_buffer("qzeros", qzeros)
         self.register_buffer("scales", scales)
         self.register_buffer("bias", bias)
         self.group_size = group_size
+        self.activation = activation
         self.in_features = qweight.shape[0]
         self.out_features = qweight.shape[1] * 8
 
-    def forward(self, x):
-        return awq_gemm(x.contiguous(), self.qweight, self.qzeros, self.scales, self.bias, self.group_size)
+    def forward(self, x, residual=None):
+        if self.activation is None and residual is None:
+            return awq_gemm(x.contiguous(), self.qweight, self.qzeros, self.scales, self.bias, self.group_size)
+        from .fused import awq_gemm_fused  # fused.py imports this module
+        return awq_gemm_fused(x.contiguous(), self.qweight, self.qzeros, self.scales, self.bias, self.group_size,
+                              activation=self.activation, residual=residual)

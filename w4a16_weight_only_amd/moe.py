@@ -328,9 +328,13 @@ class AwqMoe(torch.nn.Module):
     """Inference-only routed-expert layer: a dense router [E, K] and the experts' packed gate_up and
     down weights.  A router in the activations' type gives logits rounded to it; one in fp32 gives
     fp32 logits, which do not tie experts that are a 16-bit rounding apart.  Routing arguments are awq_moe_route's.  A token
-    whose logits hold a NaN (for the softmax, or +inf) comes out as NaN."""
+    whose logits hold a NaN (for the softmax, or +inf) comes out as NaN.
 
-    def __init__(self, router, gate_up, down, topk, group_size=128, bias=None, **routing):
+    one_call: few tokens, T * topk <= 64, take awq_moe_layer, two launches in all, and forward's
+    residual (of the output's shape) is joined before y is rounded; the values are the same, the
+    bits not always.  Otherwise the residual is added to y."""
+
+    def __init__(self, router, gate_up, down, topk, group_size=128, bias=None, one_call=False, **routing):
         super().__init__()
         self.register_buffer("router", router)
         self.register_buffer("bias", bias)
@@ -339,15 +343,26 @@ class AwqMoe(torch.nn.Module):
                 self.register_buffer(f"{name}_{part}", t)
         self.topk = topk
         self.group_size = group_size
+        self.one_call = one_call
         self.routing = routing
 
-    def forward(self, x):
+    def forward(self, x, residual=None):
         rows = x.reshape(-1, x.shape[-1]).contiguous()
         if self.router.dtype is not rows.dtype and self.router.dtype is not torch.float32:
             raise TypeError(f"router must be {rows.dtype} or float32, got {self.router.dtype}")
+        gate_up = (self.gate_up_qweight, self.gate_up_qzeros, self.gate_up_scales)
+        down = (self.down_qweight, self.down_qzeros, self.down_scales)
+        shape = x.shape[:-1] + (8 * down[0].shape[-1],)
+        if residual is not None and residual.shape != shape:
+            raise ValueError(f"residual must be {list(shape)}")
+        if self.one_call and rows.shape[0] * self.topk <= 64:
+            y = awq_moe_layer(rows, self.router, gate_up, down, self.topk, self.group_size, bias=self.bias,
+                              round_logits=self.router.dtype is rows.dtype,
+                              residual=None if residual is None else residual.reshape(rows.shape[0], -1).contiguous(),
+                              **self.routing)
+            return y.reshape(shape)
         logits = torch.nn.functional.linear(rows.to(self.router.dtype), self.router)
         weights, ids = awq_moe_route(logits, self.topk, bias=self.bias, **self.routing)
-        y = awq_moe_mlp(rows, (self.gate_up_qweight, self.gate_up_qzeros, self.gate_up_scales),
-                        (self.down_qweight, self.down_qzeros, self.down_scales), ids, weights, self.group_size,
-                        nan_weights=True)
-        return y.reshape(x.shape[:-1] + (y.shape[-1],))
+        y = awq_moe_mlp(rows, gate_up, down, ids, weights, self.group_size, nan_weights=True)
+        y = y.reshape(shape)
+        return y if residual is None else residual + y

@@ -50,7 +50,7 @@ def _run(x, residual, weight, bias, gate, scale, post_weight, post_bias, kind, e
     H, dtype, dev = x.shape[-1], x.dtype, x.device
     if kind not in _KINDS:
         raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
-    if weight is None:
+    if weight is None and (bias is not None or not keep_r or y is not None):
         raise TypeError("weight must be a torch.Tensor")
     if post_bias is not None and post_weight is None:
         raise ValueError("post_bias needs post_weight")
@@ -70,14 +70,15 @@ def _run(x, residual, weight, bias, gate, scale, post_weight, post_bias, kind, e
     vectors = [_vector(n, t, H, dtype, dev) for n, t in (("post_weight", post_weight), ("post_bias", post_bias),
                                                          ("weight", weight), ("bias", bias))]
     whole = x_stride == H  # then x is contiguous
-    y = torch.empty_like(x) if y is None and whole else _output(y, x.shape, dtype, dev)
+    if weight is not None:
+        y = torch.empty_like(x) if y is None and whole else _output(y, x.shape, dtype, dev)
     if keep_r:
         whole = residual_stride == H
         r = torch.empty_like(residual) if r is None and whole else _output(r, x.shape, stream_type, dev)
     _call(_lib.load().awq_add_norm, "awq_add_norm", dev, x.data_ptr(), _TYPES[dtype], T, H, x_stride,
           None if residual is None else residual.data_ptr(), _TYPES[stream_type], residual_stride,
           None if gate is None else gate.data_ptr(), gates, scale, *vectors, _KINDS[kind], 1 if unit_offset else 0, eps,
-          y.data_ptr(), r.data_ptr() if keep_r else None)
+          None if y is None else y.data_ptr(), r.data_ptr() if keep_r else None)
     return y, r
 
 
@@ -89,7 +90,7 @@ def awq_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = 
     return _run(x, None, weight, bias, None, 1.0, None, None, kind, eps, unit_offset, out, None, False)[0]
 
 
-def awq_add_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, *,
+def awq_add_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor | None, bias: torch.Tensor | None = None, *,
                  gate: torch.Tensor | None = None, scale: float = 1.0, post_weight: torch.Tensor | None = None,
                  post_bias: torch.Tensor | None = None, kind: str = "rms", eps: float = 1e-6,
                  unit_offset: bool = False, out: tuple | None = None) -> tuple:
@@ -99,7 +100,8 @@ def awq_add_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, 
         r = residual + scale * gate * z,  z = x or, with post_weight, norm(x) * post_weight + post_bias
         y = norm(r) * weight + bias       (of r before it is rounded to residual's type)
 
-    kind, eps and unit_offset as for awq_norm, for both norms.  gate: [H], or [B, H] for B equal runs
+    With weight None there is no second norm, and y is None.  kind, eps and unit_offset as for
+    awq_norm, for both norms.  gate: [H], or [B, H] for B equal runs
     of rows (sequences, or with B = T every row).  out, if given, is (y, r) to write into: r may be
     residual itself, y may be x itself."""
     if residual is None:
