@@ -23,6 +23,7 @@ import torch
 
 import w4a16_weight_only_amd as awq
 from oracle import awq_ref as oracle
+from tests.fused_sizes import GATED_TILES, TILES
 from w4a16_weight_only_amd import synth
 
 pytestmark = pytest.mark.gpu
@@ -130,11 +131,6 @@ STREAM = [(1, 32, 32, 32), (1, 4096, 4096, 128), (2, 96, 288, 32), (3, 2048, 140
           (5, 192, 512, 64), (8, 4096, 2048, 128), (9, 512, 544, 32), (16, 11008, 256, 64), (17, 1024, 1024, 128),
           (33, 2048, 320, -1), (64, 4096, 1408, 128), (72, 64, 4096, 32), (73, 320, 544, 64), (200, 2048, 1024, 64),
           (500, 1408, 2048, 128)]
-# Row tiles of heights 64 (two and a part), 128, 192, 256, and products of few, odd and half k-tiles.
-TILES = [(100, 64, 22528, 32), (130, 96, 22528, 32), (600, 320, 22528, 64), (380, 128, 22528, 128),
-         (1000, 192, 22528, -1), (390, 160, 22560, 32)]
-GATED_TILES = [(100, 64, 11264, 32), (600, 320, 11264, 64), (380, 128, 11264, 128), (1000, 192, 11264, -1),
-               (391, 160, 11296, 32)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -147,7 +143,7 @@ def test_few_rows(M, K, N, g, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,K,N,g", TILES)
+@pytest.mark.parametrize("M,K,N,g", sum(TILES.values(), []))
 def test_row_tiles(M, K, N, g, dtype):
     w = Weight(K, N, g, M + K)
     check(M, K, N, g, dtype, w=w)
@@ -155,7 +151,7 @@ def test_row_tiles(M, K, N, g, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,K,N,g", GATED_TILES)
+@pytest.mark.parametrize("M,K,N,g", sum(GATED_TILES.values(), []))
 def test_gated_row_tiles(M, K, N, g, dtype):
     w = Weight(K, 2 * N, g, M + K)
     check(M, K, N, g, dtype, "silu", True, w=w)
@@ -164,10 +160,9 @@ def test_gated_row_tiles(M, K, N, g, dtype):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("M,K,N", [(7, 256, 288), (90, 64, 22016)])
+@pytest.mark.parametrize("M,K,N", [(7, 256, 288), (75, 320, 22016)])
 def test_activations(M, K, N, gated, act):
     """Every activation with and without each of its companions; values from far below to far above 0."""
-    N = N // 2 if gated and N > 1000 else N
     w = Weight(K, 2 * N if gated else N, 64, 5, edit=lambda w: w.sc.__imul__(np.float16(6.0)))
     for bias in (False, True):
         for residual in (False, True):

@@ -87,7 +87,8 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
 // begin at even k-tiles only (2: g is a multiple of 128, or there is one group), at any k-tile
 // (1: a multiple of 64), or also in the middle of one (0).  WHOLE: turns of whole k-tiles (K is
 // a multiple of 64 and BEGINS is not 0).  DENSE: the rows are first, first + 1, ... themselves, and
-// the epilogue epi takes the products; else they are slots sorted[first], ...
+// the epilogue epi takes the products (with p.sums a K split's sums leave as they are, fp32 rows of all the
+// weight's columns); else they are slots sorted[first], ...
 template <int FM, bool GATED, bool BF16, int BEGINS, bool WHOLE, bool DENSE = false>
 __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, int e, int first, int rows, int tile,
                                             const int32_t* __restrict__ sorted, const Epilogue* epi = nullptr) {
@@ -467,7 +468,7 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
       const int n = min(n0 + tcol(GATED ? 0 : j) + lc, N - 1) + (GATED ? j * N : 0);
-      b[j] = epi->bias != nullptr ? act_to_float<BF16>(epi->bias[n]) : 0.f;
+      b[j] = epi->bias != nullptr && p.sums == nullptr ? act_to_float<BF16>(epi->bias[n]) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -478,6 +479,17 @@ __device__ __forceinline__ void expert_tile(const ExpertProduct& p, char* lds, i
         for (int j = 0; j < kFN; ++j)
           ys[(32 * wm + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * kLd + tcol(j) + lc] = acc[i][j][r] * unit[j] + b[j];
       __syncthreads();
+      if (p.sums != nullptr) {
+#pragma unroll 1
+        for (int q = tid; q < 64 * (kCols / 4); q += kThreads) {
+          const int staged = q / (kCols / 4), c = 4 * (q % (kCols / 4));
+          const int row = (staged >> 5) * kWaveRows + 32 * i + (staged & 31), n = n0 + c % kOut;
+          if (row >= rows || n >= N) continue;
+          *reinterpret_cast<floatx4*>(p.sums + (int64_t)(first + row) * (NW * 8) + c / kOut * N + n) =
+              *reinterpret_cast<const floatx4*>(ys + staged * kLd + c);
+        }
+        continue;
+      }
 #pragma unroll 1
       for (int q = tid; q < 64 * (kOut / 8); q += kThreads) {
         const int staged = q / (kOut / 8), c = 8 * (q % (kOut / 8));

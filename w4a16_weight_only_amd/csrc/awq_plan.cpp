@@ -492,16 +492,20 @@ int64_t active_entries(int64_t T, int64_t topk, int64_t E, int64_t rows) {
 }
 
 // K splits of `tiles` column tiles on workgroups of kStreamWaves waves, one per compute unit at a time,
-// that meet inside the kernel.  In hundredths of a microsecond (MI355X): a k-step of 32 takes a
-// compute unit's waves 100, or what HBM gives where more than half of the units have one (160 with
-// all of them); a round of workgroups 300 beside; and each split its share of the join, by the rows
-// kept.  Measured against forced split counts, us per call in a graph: 1 x 4096 -> 4096 fp16, 4, 8, 12, 16
-// splits 10.4, 8.3, 8.2, 8.9 (12 chosen); 16 x 4096 -> 4096 bf16, 4, 8, 12, 16: 13.0, 12.1, 11.8, 14.0 (8);
-// 4 x 4096 -> 2 x 11008, 3, 4, 5, 6: 20.7, 16.7, 16.4, 23.0 (5); 1 x 11008 -> 4096, 4, 8, 12, 16: 19.2, 13.1,
-// 11.4, 11.9; 16 x 8192 -> 28672, 1, 2, 3, 4: 55.0, 34.9, 42.7, 39.0 (2).
-void choose_splits8(int64_t tiles, int64_t ksteps, bool gated, int rows, int64_t cus, int& splits, int& steps) {
+// that meet inside the kernel; returns the cost in hundredths of a microsecond (MI355X, a call in a
+// graph).  350 beside the stream; a k-step of 32 takes a compute unit's waves 100 to 125 by the rows (32
+// rows, which unpacking and rescaling bound: 120 and 220 for every 32 rows of a group), or what HBM gives (160 with all
+// of the units at it); a round of workgroups 100 beside; the join of the splits 250 (32 rows 450) and
+// a share by the rows for each.  Measured against forced split counts, us: 1 x 4096 -> 4096 fp16, 4, 8, 12, 16
+// splits 10.4, 8.3, 8.2, 8.9 (8 chosen); 16 x 4096 -> 4096 bf16, 4, 8, 12, 16: 13.0, 12.1, 11.8, 14.0 (8);
+// 4 x 4096 -> 2 x 11008, 3, 4, 5, 6: 20.7, 16.7, 16.4, 23.0 (4); 32 x 4096 -> 2 x 11008, 2, 3, 4, 5: 35.9, 30.6,
+// 27.9, 28.4 (4); 1 x 11008 -> 4096, 4, 8, 12, 16: 19.2, 13.1, 11.4, 11.9 (11); 16 x 8192 -> 28672, 1, 2, 3, 4:
+// 55.0, 34.9, 42.7, 39.0 (2).
+int64_t choose_splits8(int64_t tiles, int64_t ksteps, int64_t g, bool gated, int rows, int64_t cus, int& splits,
+                       int& steps) {
   const int64_t parts = gated ? kStreamWaves / 2 : kStreamWaves;
-  const int64_t join = (rows == 1 ? 15 : rows <= 8 ? 32 : rows == 16 ? 45 : 75) * (gated ? 2 : 1);
+  const int64_t step = rows == 1 ? 100 : rows <= 8 ? 105 : rows == 16 ? 125 : 120 + 220 * 32 / g;
+  const int64_t share = rows == 1 ? 20 : rows <= 8 ? 25 : rows == 16 ? 37 : gated ? 95 : 70;
   int64_t best = -1, last = 0;
   for (int64_t want = 1; want <= kExpertMaxSplits && last != 1; ++want) {
     const int64_t st = (ksteps + want * parts - 1) / (want * parts);
@@ -510,11 +514,50 @@ void choose_splits8(int64_t tiles, int64_t ksteps, bool gated, int rows, int64_t
     const int64_t sp = (ksteps + st * parts - 1) / (st * parts);
     const int64_t rounds = (tiles * sp + cus - 1) / cus;
     const int64_t hbm = 160 * tiles * sp / (rounds * cus);
-    const int64_t cost = rounds * (st * (hbm > 100 ? hbm : 100) + 300) + (sp > 1 ? sp * join : 0);
+    int64_t cost = 350 + rounds * (st * (hbm > step ? hbm : step) + 100);
+    if (sp > 1) cost += (rows == 32 ? 450 : 250) + sp * share * (gated ? 2 : 1);
     if (best >= 0 && cost >= best) continue;
     best = cost;
     steps = (int)st;
     splits = (int)sp;
+  }
+  return best;
+}
+
+// Row tiles of M rows, where they cost less than `best`: their height and K splits.  In hundredths of a
+// microsecond: a k-tile of 64 takes a tile of 256, 192, 128, 64 rows 166, 145, 110, 88 (unpacking the
+// weights is the same for all), and 0.4 more with groups of 32; a round of tiles 800 beside; the
+// splits' fp32 sums are written and read at 6 TB/s by a kernel more.  Streamed / best tiles (height / splits),
+// us in a graph: 4096 -> 4096 fp16, 500 rows 31.9 / 36.5 (128 / 4), 750 59.7 / 45.9 (192 / 4), 1500 92 / 71.5 (192 / 2);
+// 11008 -> 4096 bfloat16, 80 rows 32.2 / 34.9 (64 / 8), 200 49.3 / 42.0 (128 / 8), 1000 158 / 110 (256 / 4); 4096 ->
+// 2 x 11008, 80 rows 57.0 / 46.1 (128 / 2), 500 182 / 111 (256 / 1); 2048 -> 8192, g 64, 200 rows 21.4 / 30.3, 300
+// 40.3 / 34.8 (192 / 4), 1000 80 / 50.6 (128 / 1).
+void choose_tiles(int64_t M, int64_t K, int64_t N, int64_t g, int64_t cus, bool gated, int64_t best, DensePlan& p) {
+  const int64_t cols = gated ? kExpertTileCols / 2 : kExpertTileCols, wide = gated ? 2 * N : N;
+  const int64_t tiles_n = (N + cols - 1) / cols;
+  // Splits are whole groups and whole k-tiles; one group, pairs of k-tiles.
+  int64_t unit = g == K ? 128 : g;
+  if (unit % 64 != 0) unit *= 2;
+  const int heights[4] = {256, 192, 128, 64}, cost[4] = {166, 145, 110, 88};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t tiles = (M + heights[i] - 1) / heights[i] * tiles_n;
+    for (int64_t want = 1; want <= 8; ++want) {
+      const int64_t kps = want == 1 ? K : (K / want + unit - 1) / unit * unit;
+      const int64_t splits = (K + kps - 1) / kps;
+      if (splits != want) continue;
+      const int64_t rounds = (tiles * splits + cus - 1) / cus;
+      int64_t c = rounds * ((kps + 63) / 64 * (cost[i] + cost[i] * 2 / 5 * 32 / g) + 800);
+      if (splits > 1) c += 400 + 2 * splits * M * wide * 4 / 60000;
+      if (best >= 0 && c >= best) continue;
+      best = c;
+      p = DensePlan{};
+      p.rows = heights[i];
+      p.col_tiles = (int)tiles_n;
+      p.splits = (int)splits;
+      p.kps = (int)kps;
+      p.grid = tiles * splits;
+      if (splits > 1) p.sums_bytes = splits * M * wide * 4;
+    }
   }
 }
 
@@ -650,8 +693,9 @@ int plan_layer(int64_t T, int64_t topk, int64_t E, int64_t K, int64_t inner, int
   p.up_tiles = (int)((inner + kExpertStreamCols - 1) / kExpertStreamCols);
   p.down_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
   const int64_t active = active_entries(T, topk, E, 16);
-  choose_splits8(active * p.up_tiles, K / 32, true, p.rows, cus, p.up_splits, p.up_steps);
-  choose_splits8(active * p.down_tiles, inner / 32, false, p.rows, cus, p.down_splits, p.down_steps);
+  choose_splits8(active * p.up_tiles, K / 32, eff_group(K, group_size), true, p.rows, cus, p.up_splits, p.up_steps);
+  choose_splits8(active * p.down_tiles, inner / 32, eff_group(inner, group_size), false, p.rows, cus, p.down_splits,
+                 p.down_steps);
   if (p.rows == 1 && p.down_steps * kStreamWaves * 32 > kLayerCols) p.rows = 4;
   const int64_t entries = entry_bound(S, E, 16);
   const int64_t up_items = entries * p.up_tiles * p.up_splits, down_items = entries * p.down_tiles * p.down_splits;
@@ -681,38 +725,26 @@ int plan_dense(int64_t M, int64_t K, int64_t N, int64_t group_size, int cus, boo
   if (K * (wide / 2) >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into the weight
   if (M == 0) return AWQ_OK;
   if (cus < 1) cus = 1;
-  const int64_t tile_cols = gated ? kExpertTileCols / 2 : kExpertTileCols;
-  const int64_t tiles_n = (N + tile_cols - 1) / tile_cols;
-  const int64_t row_tiles = (M + kExpertTileRows - 1) / kExpertTileRows * tiles_n;
-  p.stream = M <= kExpertStreamRows || 3 * row_tiles <= cus;
-  if (p.stream) {
-    if (M * K * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into x
+  // 32-bit offsets into x (streamed) or a tile's rows of it.
+  const bool can_stream = M * K * 2 < k2p32 - 4096, can_tile = int64_t(kExpertTileRows) * K * 2 < k2p32 - 4096;
+  int64_t best = -1;
+  if (can_stream) {
+    p.stream = true;
     p.rows = M == 1 ? 1 : M <= 4 ? 4 : M <= 8 ? 8 : M <= 16 ? 16 : 32;
     const int64_t block_rows = p.rows == 32 ? 32 : 16;
     p.col_tiles = (int)((N + kExpertStreamCols - 1) / kExpertStreamCols);
     const int64_t tiles = (M + block_rows - 1) / block_rows * p.col_tiles;
-    choose_splits8(tiles, K / 32, gated, p.rows, cus, p.splits, p.steps);
+    best = choose_splits8(tiles, K / 32, eff_group(K, group_size), gated, p.rows, cus, p.splits, p.steps);
     p.grid = tiles * p.splits;
     if (p.splits > 1) {
       p.counter_bytes = tiles * 4;
       p.sums_bytes = p.grid * p.rows * (gated ? 2 : 1) * kExpertStreamCols * 4;
     }
-  } else {
-    // The height of the tiles: rounds of the card times what a tile takes (in hundredths of one of
-    // 256 rows).
-    if (int64_t(kExpertTileRows) * K * 2 >= k2p32 - 4096) return AWQ_ERR_UNSUPPORTED;  // 32-bit offsets into a tile's rows
-    const int heights[4] = {256, 192, 128, 64}, cost[4] = {100, 83, 70, 60};
-    int64_t best = -1;
-    for (int i = 0; i < 4; ++i) {
-      const int64_t tiles = (M + heights[i] - 1) / heights[i] * tiles_n;
-      const int64_t c = (tiles + cus - 1) / cus * cost[i];
-      if (best >= 0 && c >= best) continue;
-      best = c;
-      p.rows = heights[i];
-      p.grid = tiles;
-    }
-    p.col_tiles = (int)tiles_n;
   }
+  if (can_tile && M > kExpertStreamRows) choose_tiles(M, K, N, eff_group(K, group_size), cus, gated, best, p);
+  if (p.grid == 0) return AWQ_ERR_UNSUPPORTED;
+  const bool join = !p.stream && p.splits > 1;  // a thread per eight columns
+  if (join && !grid_fits((M * (N / 8) + 255) / 256, 1, 256)) return AWQ_ERR_UNSUPPORTED;
   return grid_fits(p.grid, 1, 512) && p.grid < (int64_t(1) << 31) ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
 }
 

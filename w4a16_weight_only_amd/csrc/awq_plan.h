@@ -248,12 +248,13 @@ constexpr int kStreamWaves = 8;
 // A dense product with its epilogue (awq_gemm_fused).
 //   stream   up to `rows` (1, 4, 8, 16, 32) rows and 256 columns per workgroup, `steps` k-steps per
 //            wave, `splits` K splits that meet over the workspace
-//   else     row tiles of up to `rows` (64, 128, 192, 256) rows
+//   else     row tiles of up to `rows` (64, 128, 192, 256) rows, `splits` K splits of `kps` rows of the
+//            weight, whose sums a second kernel joins
 struct DensePlan {
   bool stream = false;
   int rows = 0;
   int col_tiles = 0;
-  int splits = 1, steps = 0;
+  int splits = 1, steps = 0, kps = 0;
   int64_t grid = 0;           // workgroups
   int64_t counter_bytes = 0;  // zero between calls: one 32-bit count per row block and column tile
   int64_t sums_bytes = 0;     // fp32 sums of all splits

@@ -107,6 +107,9 @@ def _launch(x, qweight, qzeros, scales, bias, activation, residual, scale, out, 
     counters = ws = hold = None
     if count_bytes:
         counters, ws, hold = counters_and_scratch(dev, count_bytes, ws_bytes)
+    elif ws_bytes:
+        hold = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws = hold.data_ptr()
     status = _lib.load().awq_gemm_fused(
         x.data_ptr(), _TYPES[x.dtype], qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
         None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation], gated,
