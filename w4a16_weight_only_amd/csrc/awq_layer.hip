@@ -24,6 +24,7 @@
 // of the second product only after it has seen that all gated items are taken (it may hold a ticket
 // before: nobody waits for those).  So does a bound on the polls, behind which y is NaN.  Tickets are eight lists, one per XCD as blocks go round them (one
 // list: 18 ns for each workgroup in turn); who finds his own empty takes from the others.
+#include "awq_epilogue.h"
 #include "awq_route.h"
 #include "awq_stream.h"
 
@@ -47,12 +48,19 @@ __device__ __forceinline__ uint32_t count_in(uint32_t* p) {
 // Stores of this wave are complete where every XCD sees them.
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-template <bool BF16, bool R32>
+// A lane's share of the logits of TOKENS tokens (those past the last: the last again, so that no load
+// waits behind a branch).
+template <bool BF16, bool R32, int TOKENS>
 __device__ __forceinline__ void dots(const LayerArgs& a, int e, int t0, int first, int step, float (&acc)[kLayerTokens]) {
   const char* row = static_cast<const char*>(a.router) + (int64_t)e * a.K * (R32 ? 4 : 2);
-  const int nt = min(a.T - t0, kLayerTokens);
+  const uint16_t* x[TOKENS];
+#pragma unroll
+  for (int t = 0; t < TOKENS; ++t) x[t] = a.x + (int64_t)min(t0 + t, a.T - 1) * a.K;
 #pragma unroll 2
   for (int k = first; k < a.K; k += step) {
+    u32x4 v[TOKENS];
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) v[t] = *reinterpret_cast<const u32x4*>(x[t] + k);
     float w[8];
     if constexpr (R32) {
       const floatx4* p = reinterpret_cast<const floatx4*>(row + 4 * (int64_t)k);
@@ -60,19 +68,23 @@ __device__ __forceinline__ void dots(const LayerArgs& a, int e, int t0, int firs
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = lo[i], w[4 + i] = hi[i];
     } else {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(row + 2 * (int64_t)k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = act_to_float<BF16>((uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+      unpack8<BF16>(*reinterpret_cast<const u32x4*>(row + 2 * (int64_t)k), w);
     }
 #pragma unroll
-    for (int t = 0; t < kLayerTokens; ++t) {
-      if (t < nt) {  // the same in every lane
-        const u32x4 v = *reinterpret_cast<const u32x4*>(a.x + (int64_t)(t0 + t) * a.K + k);
+    for (int t = 0; t < TOKENS; ++t) {
+      float f[8];
+      unpack8<BF16>(v[t], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[t] = fmaf(act_to_float<BF16>((uint16_t)(v[i >> 1] >> (16 * (i & 1)))), w[i], acc[t]);
-      }
+      for (int i = 0; i < 8; ++i) acc[t] = fmaf(f[i], w[i], acc[t]);
     }
   }
+}
+
+template <bool BF16, bool R32>
+__device__ __forceinline__ void dots(const LayerArgs& a, int e, int t0, int nt, int first, int step,
+                                     float (&acc)[kLayerTokens]) {
+  if (nt == 1) dots<BF16, R32, 1>(a, e, t0, first, step, acc);
+  else dots<BF16, R32, kLayerTokens>(a, e, t0, first, step, acc);
 }
 
 }  // namespace
@@ -104,8 +116,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void layer_router_kernel(const L
 #pragma unroll
   for (int t = 0; t < kLayerTokens; ++t) acc[t] = 0.f;
   const int first = 8 * (part * 64 + lane), step = 512 * a.router_waves;
-  if (a.bf16) a.router32 ? dots<true, true>(a, el, t0, first, step, acc) : dots<true, false>(a, el, t0, first, step, acc);
-  else a.router32 ? dots<false, true>(a, el, t0, first, step, acc) : dots<false, false>(a, el, t0, first, step, acc);
+  if (a.bf16) a.router32 ? dots<true, true>(a, el, t0, nt, first, step, acc) : dots<true, false>(a, el, t0, nt, first, step, acc);
+  else a.router32 ? dots<false, true>(a, el, t0, nt, first, step, acc) : dots<false, false>(a, el, t0, nt, first, step, acc);
 #pragma unroll
   for (int t = 0; t < kLayerTokens; ++t) acc[t] = lanes_sum<64>(acc[t]);
   if (lane == 0) {
