@@ -18,6 +18,11 @@
 // bfloat16 sums of 32 rows leave no registers for two sets of those: there the next group's are
 // asked for when a group begins (both ways: 64 tokens through 8 x 4096 -> 14336 209 -> 187 us in
 // bfloat16, which had spilled; one token through 64 x 2048 -> 1408 25.0 -> 27.0 in fp16).
+// Of the waves of a SIMD the oldest goes first, and ends far ahead of the others, which then are too few to keep
+// the memory busy.  So a wave's priority falls where a half, a quarter and an eighth of its run are left: who is
+// behind goes first, and all end together (without / with, us in a graph: one token through 8 x 4096 -> 14336, whose
+// gated product's waves ended 10 us apart and now 1.3, 63.4 / 58.7; 16 tokens 169 / 160; 7 tokens through 64 x
+// 2048 -> 1408 68.3 / 64.7; 19 x 4096 -> 2 x 11008 29.6 / 28.1; 1 x 8192 -> 28672 32.0 / 30.9).
 // A decoding step's h may be two terms, h rounded and what that left out (REST): a second MFMA
 // on the same operand, whose result's error is y's rounding alone (with one term 1.3 to 1.5 times
 // that).
@@ -346,7 +351,16 @@ __device__ __forceinline__ void stream_sums(const Share<RB>& s, Ready ready, flo
       if constexpr (kAlways) __builtin_amdgcn_sched_barrier(0);
     }
   }
+  int level = 3, fall = ke - (ke - kb) / 2;
+  __builtin_amdgcn_s_setprio(3);
   for (int base = kb; base < ke; base += kPF) {
+    if (base >= fall) {
+      fall = ke - (ke - fall) / 2;
+      --level;
+      if (level == 2) __builtin_amdgcn_s_setprio(2);
+      else if (level == 1) __builtin_amdgcn_s_setprio(1);
+      else __builtin_amdgcn_s_setprio(0);
+    }
 #pragma unroll
     for (int j = 0; j < kPF; ++j) {
       const int ks = base + j;
@@ -364,6 +378,7 @@ __device__ __forceinline__ void stream_sums(const Share<RB>& s, Ready ready, flo
       if (kAlways) issue(ring[j], j, ks + kPF);
     }
   }
+  __builtin_amdgcn_s_setprio(0);
 }
 
 // Waves along K of a workgroup of WAVES: all, or gated every other one (even ones the gate's columns,
