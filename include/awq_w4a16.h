@@ -414,8 +414,8 @@ int awq_moe_layer(const void* x, int act, const void* router, int router_type, i
  * The product is a sum of x times the integers (q - z), scaled per group in fp32; bias, activation
  * and residual are applied in fp32 and y is rounded once.  The result is deterministic.  A NaN or
  * infinity in a row of x reaches only that row.
- * Limits: those of awq_gemm with the weight's C columns, N % 32 == 0, qweight below 4 GiB, K < 2^23
- * (above 72 rows).  M == 0 enqueues nothing.
+ * Limits: those of awq_gemm with the weight's C columns, N % 32 == 0, qweight below 4 GiB, and x below
+ * 4 GiB or, above 72 rows, K < 2^23.  M == 0 enqueues nothing.
  */
 int awq_gemm_fused_plan(int64_t M, int64_t K, int64_t N, int64_t group_size, int gated, int64_t* workspace_bytes,
                         int64_t* counter_bytes);

@@ -8,6 +8,14 @@
 // that arrives last adds all of them in split order (the same bits whatever the order of arrival)
 // and applies the epilogue.  Each XCD has its own L2: sums and counters go through to, and come
 // from, where all of them see the same.  The counters are zero between calls.
+//
+// Eight waves, one workgroup to a compute unit, rather than two of four: half the shares to join (us in
+// a graph, four / eight waves: 1 x 4096 -> 4096 fp16 12.1 / 8.3, with its splits; 19 x 4096 -> 2 x 11008
+// bfloat16 36 / 28).  256 columns a wave, so that 16 lanes read whole 128-byte lines of a row.
+// Bound: one row of 4096 x 4096 (8.0 us, 8.7 MB) by latency, one after another of the weights, the
+// waves' and the splits' sums; 19 rows through 4096 -> 2 x 11008 (25.3 us, 47 MB) and 200 rows of 2048 -> 8192
+// (20.2 us) by unpacking: VALU 60% and the matrix cores 25% of a busy compute unit's time.  Whether these or
+// row tiles take a call: choose_tiles.
 #include "awq_epilogue.h"
 #include "awq_stream.h"
 
