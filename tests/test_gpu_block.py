@@ -94,6 +94,8 @@ def test_moe_in_one_call(dtype):
         assert torch.equal(layer(x, residual=x), x + parts(x))
         with pytest.raises(ValueError):
             layer(x, residual=x[:4])
+        for module in (layer, parts):
+            assert module(x[:0], residual=x[:0]).shape == (0, 1, K)
 
 
 def float64_chain(x, norms, dense, moe):

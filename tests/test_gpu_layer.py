@@ -8,6 +8,8 @@ splits (topk + 34) u of its terms, the residual 2 u (|residual| + |y|); y is rou
 """
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -216,6 +218,26 @@ def test_streams_at_once():
                 got.append(case.run(8))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[i % 3]) for i, y in enumerate(got))
+
+
+def test_threads_on_one_stream():
+    """Two threads' calls on one stream share its scratch; a call's two launches stay together."""
+    cases = [Case(4, 16, 256, 128, 256, 64, torch.float16, torch.float32, seed) for seed in (71, 72)]
+    want = [c.run(4) for c in cases]
+    torch.cuda.synchronize()
+    wrong = [-1, -1]
+
+    def calls(i):
+        got = [cases[i].run(4) for _ in range(300)]
+        torch.cuda.synchronize()
+        wrong[i] = sum(not torch.equal(y, want[i]) for y in got)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
 
 
 def test_empty_and_refusals():

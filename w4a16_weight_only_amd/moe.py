@@ -3,10 +3,13 @@
 Like linear.py this module marshals torch tensors into the C ABI and computes nothing
 itself.  A packed weight is the triple (qweight, qzeros, scales) stacked over the experts:
 int32 [E, K, N/8], int32 [E, G, N/8], fp16 [E, G, N].  Work runs on the current stream of
-the tensors' device; each call's workspace comes from torch's allocator on that stream, so
-calls may be captured into graphs without a call before.
+the tensors' device; each call's workspace comes from torch's allocator on that stream
+(awq_moe_layer's is kept for the stream: scratch.py), so calls may be captured into graphs
+without a call before.
 """
 from __future__ import annotations
+
+import threading
 
 import torch
 
@@ -254,6 +257,11 @@ def _layer_workspace(device, *sizes):
     return need
 
 
+# The layer's two launches have scratch in common that a stream's calls share: a thread makes both before
+# another one's.
+_layer_launch = threading.Lock()
+
+
 def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tuple, topk: int, group_size: int = 128,
                   *, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1, topk_groups: int = 1,
                   group_top: int = 1, renormalize: bool = True, scale: float = 1.0, round_logits: bool = False,
@@ -304,15 +312,16 @@ def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: t
         _lib.check(need, "awq_moe_layer_workspace")
 
     def launch():
-        counters, ws, hold = counters_and_scratch(dev, _lib.AWQ_MOE_LAYER_COUNTERS, need)
-        status = _lib.load().awq_moe_layer(
-            x.data_ptr(), _TYPES[x.dtype], router.data_ptr(), _TYPES[router.dtype], 1 if round_logits else 0,
-            None if bias is None else bias.data_ptr(), _SCORES[score], groups, topk_groups, group_top, topk,
-            1 if renormalize else 0, scale, *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down],
-            None if residual is None else residual.data_ptr(), T, E, K, inner, N, group_size, out.data_ptr(), ws, need,
-            counters, _lib.AWQ_MOE_LAYER_COUNTERS, torch._C._cuda_getCurrentRawStream(dev.index))
-        del hold
-        return status
+        with _layer_launch:
+            counters, ws, hold = counters_and_scratch(dev, _lib.AWQ_MOE_LAYER_COUNTERS, need)
+            status = _lib.load().awq_moe_layer(
+                x.data_ptr(), _TYPES[x.dtype], router.data_ptr(), _TYPES[router.dtype], 1 if round_logits else 0,
+                None if bias is None else bias.data_ptr(), _SCORES[score], groups, topk_groups, group_top, topk,
+                1 if renormalize else 0, scale, *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down],
+                None if residual is None else residual.data_ptr(), T, E, K, inner, N, group_size, out.data_ptr(), ws, need,
+                counters, _lib.AWQ_MOE_LAYER_COUNTERS, torch._C._cuda_getCurrentRawStream(dev.index))
+            del hold
+            return status
 
     if torch.cuda.current_device() == dev.index:
         status = launch()
@@ -358,7 +367,7 @@ class AwqMoe(torch.nn.Module):
         if self.one_call and rows.shape[0] * self.topk <= 64:
             y = awq_moe_layer(rows, self.router, gate_up, down, self.topk, self.group_size, bias=self.bias,
                               round_logits=self.router.dtype is rows.dtype,
-                              residual=None if residual is None else residual.reshape(rows.shape[0], -1).contiguous(),
+                              residual=None if residual is None else residual.reshape(rows.shape[0], shape[-1]).contiguous(),
                               **self.routing)
             return y.reshape(shape)
         logits = torch.nn.functional.linear(rows.to(self.router.dtype), self.router)
