@@ -11,10 +11,10 @@
 // lane); above, the table of launch_moe_align in blocks of 16 or 32 rows.
 //
 // Bound by HBM from a few rows on (medians of 27 calls): one token's two experts of 4096 -> 2 x
-// 14336, 117 MB, 29.7 us (4.0 TB/s; a copy of 2 GiB 4.96, of which half are writes); 19 rows of
-// 14336 -> 4096 over 8 experts, 235 MB, 48.2 us (4.9).  By latency below that (8 slots of 2048 -> 2 x
-// 1408, 23 MB, 12.3 us), and by unpacking beside HBM at 32 rows and in bfloat16 (16 tokens' 8 x
-// 4096 -> 2 x 14336, 470 MB, 115 us, 4.1 TB/s; 107 at best).
+// 14336, 117 MB, 28.2 us (4.2 TB/s; a copy of 2 GiB 4.96, of which half are writes); 19 rows of
+// 14336 -> 4096 over 8 experts, 235 MB, 46.7 us (5.0).  By latency below that (8 slots of 2048 -> 2 x
+// 1408, 23 MB, 13.3 us), and by unpacking beside HBM at 32 rows and in bfloat16 (16 tokens' 8 x
+// 4096 -> 2 x 14336, 470 MB, 109 us, 4.3 TB/s; 101 at best).
 #include "awq_stream.h"
 
 namespace awq {

@@ -26,8 +26,9 @@
 // Tickets are eight lists, one per XCD as blocks go round them (one list: 18 ns for each workgroup in
 // turn); who finds his own empty takes from the others.
 //
-// Bound (us, router and layer kernel): one token through 64 x 2048 -> 1408 top 8 (3 + 28, 36 MB) latency, of six
-// steps that wait for each other: logits, routing, the gated product, its sums, the second product, its sums; one token
+// Bound (us, router and layer kernel): one token through 64 x 2048 -> 1408 top 8 (3 + 28, 36 MB) latency,
+// of six steps that wait for each other: logits, routing, the gated product, its sums, the second
+// product, its sums; one token
 // through 8 x 4096 -> 14336 top 2 (5 + 53, 183 MB), 7 tokens of 64 x 2048 -> 1408 (8 + 53, 182 MB) and 16 of
 // 8 x 4096 -> 14336 (6 + 152, 730 MB) HBM, at 3.4, 3.4 and 4.8 TB/s with the fill and drain of each phase;
 // bfloat16 unpacks beside it.
