@@ -375,8 +375,9 @@ int awq_moe_mlp(const void* x, int act, const int32_t* up_qweight, const int32_t
  *   y              device [T, N].  It may be residual itself, and may overlap x
  *   workspace      as for awq_moe_mlp, awq_moe_layer_workspace bytes
  *   counters       device memory of AWQ_MOE_LAYER_COUNTERS bytes, zero before the call and zero again
- *                  after it, for this call alone until then.  (Calls in one stream's order may
- *                  share it.)
+ *                  after it, for this call alone until then.  (Calls that one thread makes on one
+ *                  stream, one after another, may share workspace and counters.  Two threads' may
+ *                  not: the launches of one's call may come between those of the other's.)
  * h is not rounded on the way (two terms, as for awq_moe_mlp): y is rounded once.  A token whose
  * logits hold a NaN (for the softmax, or +inf) comes out as NaN, one without experts as its residual.
  * The result is deterministic.  The second launch's workgroups wait for each other's parts of h;
@@ -409,7 +410,8 @@ int awq_moe_layer(const void* x, int act, const void* router, int router_type, i
  *                  aligned, for this call alone until its work on the stream is done.  It needs no
  *                  contents and keeps none
  *   counters       device memory of counter_bytes, zero before the call and zero again after it, for
- *                  this call alone until then.  (Calls in one stream's order may share both.)
+ *                  this call alone until then.  (Calls that one thread makes on one stream, one after
+ *                  another, may share both; two threads' may not, see awq_moe_layer.)
  * Either may be NULL where the plan's bytes are 0.
  * The product is a sum of x times the integers (q - z), scaled per group in fp32; bias, activation
  * and residual are applied in fp32 and y is rounded once.  The result is deterministic.  A NaN or

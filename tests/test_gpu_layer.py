@@ -240,6 +240,35 @@ def test_threads_on_one_stream():
     assert wrong == [0, 0]
 
 
+def test_a_layer_beside_a_fused_product_from_two_threads():
+    """Calls of several kinds from two threads on one stream: each call's launches may come between those
+    of the other thread's, whose scratch they leave alone."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    w = (torch.randint(-(1 << 31), 1 << 31, (4096, 512), dtype=torch.int32, device="cuda", generator=gen),
+         torch.randint(-(1 << 31), 1 << 31, (32, 512), dtype=torch.int32, device="cuda", generator=gen),
+         torch.rand((32, 4096), device="cuda", generator=gen).mul_(0.004).half())
+    x = torch.randn((1, 4096), device="cuda", generator=gen).half()
+    layers = [Case(T, 64, 2048, 1408, 2048, 128, torch.float16, torch.float32, T) for T in (1, 7)]
+    bias = torch.zeros(64, device="cuda")  # (with a bias the first kernel hands the ids over)
+    fused = lambda: awq.awq_gemm_fused(x, *w, None, 128)  # noqa: E731  (K splits: sums in the scratch)
+    kinds = [[lambda c=c, b=b: c.run(8, bias=b) for c in layers for b in (None, bias)], [fused, fused]]
+    want = [[f() for f in calls] for calls in kinds]
+    torch.cuda.synchronize()
+    wrong = [-1, -1]
+
+    def calls(i):
+        got = [[f() for f in kinds[i]] for _ in range(200)]
+        torch.cuda.synchronize()
+        wrong[i] = sum(not torch.equal(y, v) for ys in got for y, v in zip(ys, want[i]))
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
+
+
 def test_empty_and_refusals():
     case = Case(9, 8, 256, 96, 288, 32, torch.float16, torch.float16, 1)
     call = lambda x=case.x, router=case.router, up=case.up.dev, down=case.down.dev, topk=2, g=32, **k: awq.awq_moe_layer(  # noqa: E731

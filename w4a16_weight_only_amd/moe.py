@@ -4,12 +4,10 @@ Like linear.py this module marshals torch tensors into the C ABI and computes no
 itself.  A packed weight is the triple (qweight, qzeros, scales) stacked over the experts:
 int32 [E, K, N/8], int32 [E, G, N/8], fp16 [E, G, N].  Work runs on the current stream of
 the tensors' device; each call's workspace comes from torch's allocator on that stream
-(awq_moe_layer's is kept for the stream: scratch.py), so calls may be captured into graphs
+(awq_moe_layer's is kept for the thread and the stream: scratch.py), so calls may be captured into graphs
 without a call before.
 """
 from __future__ import annotations
-
-import threading
 
 import torch
 
@@ -257,11 +255,6 @@ def _layer_workspace(device, *sizes):
     return need
 
 
-# The layer's two launches have scratch in common that a stream's calls share: a thread makes both before
-# another one's.
-_layer_launch = threading.Lock()
-
-
 def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tuple, topk: int, group_size: int = 128,
                   *, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1, topk_groups: int = 1,
                   group_top: int = 1, renormalize: bool = True, scale: float = 1.0, round_logits: bool = False,
@@ -312,16 +305,15 @@ def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: t
         _lib.check(need, "awq_moe_layer_workspace")
 
     def launch():
-        with _layer_launch:
-            counters, ws, hold = counters_and_scratch(dev, _lib.AWQ_MOE_LAYER_COUNTERS, need)
-            status = _lib.load().awq_moe_layer(
-                x.data_ptr(), _TYPES[x.dtype], router.data_ptr(), _TYPES[router.dtype], 1 if round_logits else 0,
-                None if bias is None else bias.data_ptr(), _SCORES[score], groups, topk_groups, group_top, topk,
-                1 if renormalize else 0, scale, *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down],
-                None if residual is None else residual.data_ptr(), T, E, K, inner, N, group_size, out.data_ptr(), ws, need,
-                counters, _lib.AWQ_MOE_LAYER_COUNTERS, torch._C._cuda_getCurrentRawStream(dev.index))
-            del hold
-            return status
+        counters, ws, hold = counters_and_scratch(dev, _lib.AWQ_MOE_LAYER_COUNTERS, need)
+        status = _lib.load().awq_moe_layer(
+            x.data_ptr(), _TYPES[x.dtype], router.data_ptr(), _TYPES[router.dtype], 1 if round_logits else 0,
+            None if bias is None else bias.data_ptr(), _SCORES[score], groups, topk_groups, group_top, topk,
+            1 if renormalize else 0, scale, *[t.data_ptr() for t in gate_up], *[t.data_ptr() for t in down],
+            None if residual is None else residual.data_ptr(), T, E, K, inner, N, group_size, out.data_ptr(), ws, need,
+            counters, _lib.AWQ_MOE_LAYER_COUNTERS, torch._C._cuda_getCurrentRawStream(dev.index))
+        del hold
+        return status
 
     if torch.cuda.current_device() == dev.index:
         status = launch()
