@@ -29,7 +29,9 @@
  *   - Every argument is checked before anything is enqueued; a failed check returns
  *     a negative status and enqueues nothing.  No entry point aborts, prints or
  *     throws.  awq_status_string() names a status.
- *   - Entry points are safe to call from several host threads.
+ *   - Entry points are safe to call from several host threads.  Two threads' calls on one
+ *     stream are enqueued whole, one after the other, where they share the library's
+ *     workspace.
  */
 #ifndef AWQ_W4A16_H
 #define AWQ_W4A16_H

@@ -54,12 +54,18 @@ int query_cus() {
 // into it); awq_release_workspace() frees retired and current buffers on request.  A
 // stream that is being captured cannot grow its workspace: that call fails with
 // AWQ_ERR_UNSUPPORTED before enqueueing anything.
+// Some calls are several launches that hand something over in these buffers (partial sums,
+// an alignment's table).  Of two threads' calls on one stream each makes all of its launches
+// before the other begins: a call holds the workspace's `launches` from when it gets the
+// buffers until its last launch.
+typedef std::unique_lock<std::mutex> Launches;
 struct Buffer {
   void* ptr = nullptr;
   int64_t bytes = 0;
 };
 struct Workspace {
   Buffer accum, partial;
+  std::mutex launches;
 };
 
 std::mutex g_ws_mu;
@@ -85,30 +91,43 @@ int ensure(int dev, Buffer& b, int64_t need, bool zero, hipStream_t stream) {
   return AWQ_OK;
 }
 
-int get_workspace(const Plan& p, hipStream_t stream, uint64_t** accum, float** partial) {
+// The workspace of the current device and the stream, whose launches the caller then holds.
+int hold_workspace(hipStream_t stream, int* dev, Workspace** ws, Launches& held) {
+  if (hipGetDevice(dev) != hipSuccess) return AWQ_ERR_HIP;
+  {
+    std::lock_guard<std::mutex> lock(g_ws_mu);
+    *ws = &g_ws[{*dev, stream}];
+  }
+  held = Launches((*ws)->launches);
+  return AWQ_OK;
+}
+
+int get_workspace(const Plan& p, hipStream_t stream, uint64_t** accum, float** partial, Launches& held) {
   int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return AWQ_ERR_HIP;
+  Workspace* ws = nullptr;
+  int st = hold_workspace(stream, &dev, &ws, held);
+  if (st != AWQ_OK) return st;
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace& ws = g_ws[{dev, stream}];
-  int st = ensure(dev, ws.accum, p.accum_bytes, true, stream);
+  st = ensure(dev, ws->accum, p.accum_bytes, true, stream);
   if (st != AWQ_OK) return st;
-  st = ensure(dev, ws.partial, p.partial_bytes, false, stream);
+  st = ensure(dev, ws->partial, p.partial_bytes, false, stream);
   if (st != AWQ_OK) return st;
-  *accum = reinterpret_cast<uint64_t*>(ws.accum.ptr);
-  *partial = reinterpret_cast<float*>(ws.partial.ptr);
+  *accum = reinterpret_cast<uint64_t*>(ws->accum.ptr);
+  *partial = reinterpret_cast<float*>(ws->partial.ptr);
   return AWQ_OK;
 }
 
 // Scratch that is fully written before it is read within one call: the partial
 // buffer of the same (device, stream) workspace.
-int get_scratch(int64_t bytes, hipStream_t stream, void** out) {
+int get_scratch(int64_t bytes, hipStream_t stream, void** out, Launches& held) {
   int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return AWQ_ERR_HIP;
-  std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace& ws = g_ws[{dev, stream}];
-  const int st = ensure(dev, ws.partial, bytes, false, stream);
+  Workspace* ws = nullptr;
+  int st = hold_workspace(stream, &dev, &ws, held);
   if (st != AWQ_OK) return st;
-  *out = ws.partial.ptr;
+  std::lock_guard<std::mutex> lock(g_ws_mu);
+  st = ensure(dev, ws->partial, bytes, false, stream);
+  if (st != AWQ_OK) return st;
+  *out = ws->partial.ptr;
   return AWQ_OK;
 }
 
@@ -130,32 +149,42 @@ __global__ void zero_words_kernel(u32x4_t* p, int64_t n) {
 }
 
 std::mutex g_scratch_mu;
-std::map<int, void*> g_scratch;  // device -> address of `scratch` on that device
+struct StaticScratch {
+  void* ptr;  // address of `scratch` on the device
+  std::mutex launches;
+};
+std::map<int, StaticScratch> g_scratch;  // by device
 
-int get_static_scratch(hipStream_t stream, void** out) {
+int get_static_scratch(hipStream_t stream, void** out, Launches& held) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return AWQ_ERR_HIP;
-  std::lock_guard<std::mutex> lock(g_scratch_mu);
-  auto it = g_scratch.find(dev);
-  if (it == g_scratch.end()) {
-    void* ptr = nullptr;
-    if (hipGetSymbolAddress(&ptr, HIP_SYMBOL(scratch)) != hipSuccess || ptr == nullptr) return AWQ_ERR_HIP;
-    hipLaunchKernelGGL(zero_words_kernel, dim3(256), dim3(256), 0, stream, static_cast<u32x4_t*>(ptr),
-                       kScratchWordBytes / 16);
-    if (hipGetLastError() != hipSuccess) return AWQ_ERR_HIP;
-    it = g_scratch.emplace(dev, ptr).first;
+  StaticScratch* at = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(g_scratch_mu);
+    auto it = g_scratch.find(dev);
+    if (it == g_scratch.end()) {
+      void* ptr = nullptr;
+      if (hipGetSymbolAddress(&ptr, HIP_SYMBOL(scratch)) != hipSuccess || ptr == nullptr) return AWQ_ERR_HIP;
+      hipLaunchKernelGGL(zero_words_kernel, dim3(256), dim3(256), 0, stream, static_cast<u32x4_t*>(ptr),
+                         kScratchWordBytes / 16);
+      if (hipGetLastError() != hipSuccess) return AWQ_ERR_HIP;
+      it = g_scratch.try_emplace(dev).first;
+      it->second.ptr = ptr;
+    }
+    at = &it->second;
   }
-  *out = it->second;
+  held = Launches(at->launches);
+  *out = at->ptr;
   return AWQ_OK;
 }
 
 // The split-K buffers of plan p: the stream's grown workspace, or (noalloc) the static
 // scratch, AWQ_ERR_UNSUPPORTED when the plan needs more than it holds.
-int workspace_for(const Plan& p, hipStream_t stream, bool noalloc, uint64_t** accum, float** partial) {
-  if (!noalloc) return get_workspace(p, stream, accum, partial);
+int workspace_for(const Plan& p, hipStream_t stream, bool noalloc, uint64_t** accum, float** partial, Launches& held) {
+  if (!noalloc) return get_workspace(p, stream, accum, partial, held);
   if (p.accum_bytes > kScratchWordBytes || p.partial_bytes > kScratchPartialBytes) return AWQ_ERR_UNSUPPORTED;
   void* base = nullptr;
-  const int st = get_static_scratch(stream, &base);
+  const int st = get_static_scratch(stream, &base, held);
   if (st != AWQ_OK) return st;
   *accum = static_cast<uint64_t*>(base);
   *partial = reinterpret_cast<float*>(static_cast<unsigned char*>(base) + kScratchWordBytes);
@@ -275,8 +304,9 @@ int awq_quantize_rtn(const void* w_f16, int64_t K, int64_t N, int64_t group_size
   if (!aligned16(w_f16) || !aligned16(qweight) || !aligned16(qzeros) || !aligned16(scales_f16))
     return AWQ_ERR_ALIGN;
   void* scratch = nullptr;
+  Launches held;
   if (p.scratch_bytes > 0) {
-    st = get_scratch(p.scratch_bytes, stream, &scratch);
+    st = get_scratch(p.scratch_bytes, stream, &scratch, held);
     if (st != AWQ_OK) return st;
   }
   hipError_t e = awq::launch_quantize_rtn(static_cast<const uint16_t*>(w_f16), (int)K, (int)N, g, sym != 0, qweight,
@@ -304,11 +334,12 @@ int gemm_common(const void* x_f16, const int32_t* qweight, const int32_t* qzeros
   const auto* b = static_cast<const uint16_t*>(bias_f16);
   auto* y = static_cast<uint16_t*>(y_f16);
   hipError_t e;
+  Launches held;
   if (p.family == 2) {
     uint64_t* accum = nullptr;
     float* partial = nullptr;
     if (p.dp.splits > 1) {
-      const int ws = workspace_for(p, stream, noalloc, &accum, &partial);
+      const int ws = workspace_for(p, stream, noalloc, &accum, &partial, held);
       if (ws != AWQ_OK) return ws;
     }
     float* side = accum ? reinterpret_cast<float*>(accum + decode_entries(p.dp)) : nullptr;
@@ -317,7 +348,7 @@ int gemm_common(const void* x_f16, const int32_t* qweight, const int32_t* qzeros
     uint64_t* accum = nullptr;
     float* partial = nullptr;
     if (p.sk.splits > 1) {
-      const int ws = workspace_for(p, stream, noalloc, &accum, &partial);
+      const int ws = workspace_for(p, stream, noalloc, &accum, &partial, held);
       if (ws != AWQ_OK) return ws;
     }
     // Fixed-point plans: the float side words follow the accumulator words.
@@ -329,7 +360,7 @@ int gemm_common(const void* x_f16, const int32_t* qweight, const int32_t* qzeros
     uint64_t* accum = nullptr;
     float* partial = nullptr;
     if (p.tp.splits > 1 || p.tail.tp.splits > 1) {
-      const int ws = workspace_for(p, stream, noalloc, &accum, &partial);
+      const int ws = workspace_for(p, stream, noalloc, &accum, &partial, held);
       if (ws != AWQ_OK) return ws;
     }
     e = awq::launch_tile(x, qweight, qzeros, sc, b, (int)p.rows1, (int)K, (int)N, g, p.tp, bf16, partial, y,
@@ -374,6 +405,7 @@ int awq_moe_gemm(const void* x_f16, const int32_t* qweight, const int32_t* qzero
   const auto* x = static_cast<const uint16_t*>(x_f16);
   const auto* sc = static_cast<const uint16_t*>(scales_f16);
   auto* y = static_cast<uint16_t*>(y_f16);
+  Launches held;
   if (mp.skinny) {
     Plan p;
     p.accum_bytes = mp.accum_bytes;
@@ -381,7 +413,7 @@ int awq_moe_gemm(const void* x_f16, const int32_t* qweight, const int32_t* qzero
     uint64_t* accum = nullptr;
     float* partial = nullptr;
     if (mp.sk.splits > 1) {
-      st = get_workspace(p, stream, &accum, &partial);
+      st = get_workspace(p, stream, &accum, &partial, held);
       if (st != AWQ_OK) return st;
       if (mp.sk.atomic) partial = reinterpret_cast<float*>(accum + skinny_accum_entries(mp.sk));
     }
@@ -394,7 +426,7 @@ int awq_moe_gemm(const void* x_f16, const int32_t* qweight, const int32_t* qzero
   // Scratch: tile table (16-byte entries), offsets, sorted slots; written by the
   // alignment kernel before the product reads it, on the same stream.
   void* scratch = nullptr;
-  st = get_scratch(mp.scratch_bytes, stream, &scratch);
+  st = get_scratch(mp.scratch_bytes, stream, &scratch, held);
   if (st != AWQ_OK) return st;
   int32_t* table = static_cast<int32_t*>(scratch);
   int32_t* offsets = table + 4 * mp.tiles;
