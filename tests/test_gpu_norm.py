@@ -127,6 +127,26 @@ def test_many_rows():
     check(make(5003, 384, torch.float16, torch.float32, 3, post=True), "rms", 1.0, False, "5003 rows")
 
 
+def test_more_rows_than_a_launch_holds():
+    """2^24 rows of 256 threads each are 2^32 work-items, one too many: the last row is a second launch's."""
+    T, H = 1 << 24, 1032
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GiB of free device memory")
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    rows = torch.tensor([0, 1, 12345, 1 << 22, T - 3, T - 2, T - 1], device="cuda")
+    some, weight = (torch.randn(s, device="cuda", generator=gen).half() for s in ((len(rows), H), (H,)))
+    x = torch.zeros((T, H), dtype=torch.float16, device="cuda")
+    x[rows] = some
+    y = awq.awq_norm(x, weight, eps=EPS, out=x)
+    _, (want, dy) = expected(some, None, weight, None, None, 1.0, None, None, "rms", False)
+    close(y[rows], want, dy, "y")
+    y[rows] = 0
+    for at in range(0, T, 1 << 21):  # rows of zeros stay zeros
+        assert not y[at:at + (1 << 21)].view(torch.int64).any()
+    del x, y
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("H", [96, 1500, 4096])
 def test_rows_apart_and_unaligned(H):
     """Rows of a wider tensor, and pointers that are aligned to an element only."""

@@ -86,19 +86,17 @@ __device__ __forceinline__ float half_of(const u32x4& w, int i) {
   return act_to_float<BF16>((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
 }
 
-constexpr int norm_threads(int waves) { return waves == 1 ? 256 : 64 * waves; }
-
 }  // namespace
 
 // WAVES of a row (1: four rows per workgroup), PIECES of 8 elements per lane.  R32: the stream
-// is fp32.
+// is fp32.  first: the launch's first row.
 template <bool BF16, bool R32, int WAVES, int PIECES, bool WIDE>
-__global__ __launch_bounds__(norm_threads(WAVES)) void norm_kernel(const NormArgs a) {
+__global__ __launch_bounds__(norm_threads(WAVES)) void norm_kernel(const NormArgs a, int64_t first) {
   constexpr int TPR = 64 * WAVES;
-  constexpr int ROWS = norm_threads(WAVES) / TPR;
+  constexpr int ROWS = norm_rows(WAVES);
   __shared__ float red[4][WAVES];
   const int lane = threadIdx.x % TPR;
-  const int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  const int64_t t = first + (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   if (t >= a.T) return;  // whole waves, and with several waves a row there is one row
   const int H = a.H;
   auto sum_row = [&](float v, int which) {
@@ -219,10 +217,14 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
                     wide16(a.r, stream_size * a.H);
   auto go = [&](auto bf16, auto r32, auto waves, auto pieces, auto w) {
     constexpr int W = decltype(waves)::value;
-    constexpr int rows = norm_threads(W) / (64 * W);
-    hipLaunchKernelGGL((norm_kernel<decltype(bf16)::value, decltype(r32)::value, W, decltype(pieces)::value,
-                                    decltype(w)::value>),
-                       dim3((unsigned)((a.T + rows - 1) / rows)), dim3(norm_threads(W)), 0, stream, a);
+    constexpr int64_t most = norm_launch_rows(W);
+    for (int64_t first = 0; first < a.T; first += most) {
+      const int64_t rows = a.T - first < most ? a.T - first : most;
+      hipLaunchKernelGGL((norm_kernel<decltype(bf16)::value, decltype(r32)::value, W, decltype(pieces)::value,
+                                      decltype(w)::value>),
+                         dim3((unsigned)((rows + norm_rows(W) - 1) / norm_rows(W))), dim3(norm_threads(W)), 0, stream,
+                         a, first);
+    }
   };
   auto sized = [&](auto bf16, auto r32, auto w) {
     using I1 = std::integral_constant<int, 1>;
@@ -230,13 +232,14 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     using I4 = std::integral_constant<int, 4>;
     using I8 = std::integral_constant<int, 8>;
     using I16 = std::integral_constant<int, 16>;
-    if (a.H <= 512) go(bf16, r32, I1{}, I1{}, w);
-    else if (a.H <= 1024) go(bf16, r32, I1{}, I2{}, w);
-    else if (a.H <= 2048) go(bf16, r32, I4{}, I1{}, w);
-    else if (a.H <= 4096) go(bf16, r32, I4{}, I2{}, w);
-    else if (a.H <= 8192) go(bf16, r32, I4{}, I4{}, w);
-    else if (a.H <= 16384) go(bf16, r32, I8{}, I4{}, w);
-    else go(bf16, r32, I16{}, I4{}, w);
+    switch (norm_waves(a.H)) {
+      case 1: return a.H <= 512 ? go(bf16, r32, I1{}, I1{}, w) : go(bf16, r32, I1{}, I2{}, w);
+      case 4:
+        if (a.H <= 2048) return go(bf16, r32, I4{}, I1{}, w);
+        return a.H <= 4096 ? go(bf16, r32, I4{}, I2{}, w) : go(bf16, r32, I4{}, I4{}, w);
+      case 8: return go(bf16, r32, I8{}, I4{}, w);
+      default: return go(bf16, r32, I16{}, I4{}, w);
+    }
   };
   auto typed = [&](auto bf16, auto r32) { wide ? sized(bf16, r32, std::true_type{}) : sized(bf16, r32, std::false_type{}); };
   using yes = std::true_type;

@@ -183,6 +183,14 @@ int plan_route(int64_t T, int64_t E, int64_t row_stride, int64_t groups, int64_t
 // awq_add_norm: the longest row that its kernels hold in registers.
 constexpr int64_t kNormMaxH = 32768;
 int plan_norm(int64_t T, int64_t H, int64_t x_stride, int64_t residual_stride, int64_t gates);
+// Waves of a row of H elements, a workgroup's threads and rows, and the rows of one launch, whose size HIP
+// takes in 32-bit counts: more rows take several.
+constexpr int norm_waves(int64_t H) { return H <= 1024 ? 1 : H <= 8192 ? 4 : H <= 16384 ? 8 : 16; }
+constexpr int norm_threads(int waves) { return waves == 1 ? 256 : 64 * waves; }
+constexpr int norm_rows(int waves) { return norm_threads(waves) / (64 * waves); }
+constexpr int64_t norm_launch_rows(int waves) {
+  return ((int64_t(1) << 32) - 1) / norm_threads(waves) * norm_rows(waves);
+}
 
 // One product of routed rows with their experts' weights (gated: N pairs of columns of a
 // 2 N wide weight).  Entries are up to `rows` routed rows of one expert:
