@@ -175,7 +175,7 @@ struct LayerArgs {
   uint32_t *counts, *arrivals;
   int64_t n_counts;
   int T, topk, E, K, inner, N, g_up, g_down;
-  int router_waves;  // waves per expert of the first kernel: 1 or 4
+  int router_waves;  // waves per expert of the first kernel: 1, 2, 4 or 8, a divisor of its workgroups' 8
   int up_tiles, up_splits, up_steps, down_tiles, down_splits, down_steps;
   bool bf16, router32, round_logits;
   bool route_inside;  // set by the launch: the second kernel routes

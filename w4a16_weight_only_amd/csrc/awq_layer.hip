@@ -555,6 +555,7 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void layer_kernel(const Layer
 }
 
 hipError_t launch_layer(LayerArgs a, const RouteArgs& r, const LayerPlan& p, hipStream_t stream) {
+  if (a.router_waves < 1 || kRouterWaves % a.router_waves != 0) return hipErrorInvalidValue;  // whole experts a workgroup
   const dim3 grid((unsigned)((a.E * a.router_waves + kRouterWaves - 1) / kRouterWaves), (unsigned)((a.T + kLayerTokens - 1) / kLayerTokens));
   // Routing by the logits alone, of few tokens and experts, takes every workgroup of the second kernel
   // less time than handing the ids over takes the first.
