@@ -98,6 +98,33 @@ def test_moe_in_one_call(dtype):
             assert module(x[:0], residual=x[:0]).shape == (0, 1, K)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_moe_residuals_whatever_the_token_count(dtype):
+    """16 tokens take one call, 17 the calls of the default: both take a residual in fp32 (and give fp32), one
+    that begins on its element's alignment only, one with its columns apart; the one call such a router too."""
+    E, topk, K, inner, g = 16, 4, 256, 128, 64
+    up, down = Layer(E, K, 2 * inner, g, 1), Layer(E, inner, K, g, 2)
+    router = rand(E, K, dtype=dtype, seed=3) / 8
+    layer = awq.AwqMoe(router, up.dev, down.dev, topk, g, one_call=True)
+    apart = rand(K, E, dtype=dtype, seed=3).t()
+    apart.copy_(router)
+    odd = torch.empty(E * K + 1, dtype=dtype, device="cuda")[1:].view(E, K)
+    odd.copy_(router)
+    for T in (16, 17):
+        x, r = rand(T, K, dtype=dtype, seed=T), rand(T, K, dtype=torch.float32, seed=T + 1)
+        y = layer(x)
+        got = layer(x, residual=r)
+        assert got.dtype == torch.float32 and torch.equal(got, r + y)
+        want = layer(x, residual=r.to(dtype))
+        off = torch.empty(T * K + 1, dtype=dtype, device="cuda")[1:].view(T, K)
+        off.copy_(r)
+        assert torch.equal(layer(x, residual=off), want)
+        assert torch.equal(layer(x, residual=r.to(dtype).t().contiguous().t()), want)
+        for same in (apart, odd) if T == 16 else ():
+            other = awq.AwqMoe(same, up.dev, down.dev, topk, g, one_call=True)
+            assert torch.equal(other(x, residual=r.to(dtype)), want)
+
+
 def float64_chain(x, norms, dense, moe):
     """Two dense blocks around a routed one, in float64."""
     def rms(v, w):

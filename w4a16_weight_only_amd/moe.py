@@ -325,6 +325,12 @@ def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: t
     return out
 
 
+def _laid_out(t):
+    """t as the kernels read it: contiguous, and beginning on 16 bytes."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class AwqMoe(torch.nn.Module):
     """Inference-only routed-expert layer: a dense router [E, K] and the experts' packed gate_up and
     down weights.  A router in the activations' type gives logits rounded to it; one in fp32 gives
@@ -332,8 +338,9 @@ class AwqMoe(torch.nn.Module):
     whose logits hold a NaN (for the softmax, or +inf) comes out as NaN.
 
     one_call: few tokens, T * topk <= 64, take awq_moe_layer, two launches in all, and forward's
-    residual (of the output's shape) is joined before y is rounded; the values are the same, the
-    bits not always.  Otherwise the residual is added to y."""
+    residual (of the output's shape) is joined before y is rounded, where it has x's type; the values
+    are the same, the bits not always.  Otherwise the residual is added to y (and one of fp32 gives
+    fp32)."""
 
     def __init__(self, router, gate_up, down, topk, group_size=128, bias=None, one_call=False, **routing):
         super().__init__()
@@ -357,11 +364,13 @@ class AwqMoe(torch.nn.Module):
         if residual is not None and residual.shape != shape:
             raise ValueError(f"residual must be {list(shape)}")
         if self.one_call and rows.shape[0] * self.topk <= 64:
-            y = awq_moe_layer(rows, self.router, gate_up, down, self.topk, self.group_size, bias=self.bias,
+            joined = residual is not None and residual.dtype is rows.dtype
+            y = awq_moe_layer(rows, _laid_out(self.router), gate_up, down, self.topk, self.group_size, bias=self.bias,
                               round_logits=self.router.dtype is rows.dtype,
-                              residual=None if residual is None else residual.reshape(rows.shape[0], shape[-1]).contiguous(),
+                              residual=_laid_out(residual.reshape(rows.shape[0], shape[-1])) if joined else None,
                               **self.routing)
-            return y.reshape(shape)
+            y = y.reshape(shape)
+            return y if residual is None or joined else residual + y
         logits = torch.nn.functional.linear(rows.to(self.router.dtype), self.router)
         weights, ids = awq_moe_route(logits, self.topk, bias=self.bias, **self.routing)
         y = awq_moe_mlp(rows, gate_up, down, ids, weights, self.group_size, nan_weights=True)
