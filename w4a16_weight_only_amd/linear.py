@@ -244,6 +244,8 @@ class AwqLinear(torch.nn.Module):
     applied to the product, and forward's residual, of the output's shape, added to it, in the
     same kernel."""
 
+    activation = None  # of modules that were saved whole before there was one
+
     def __init__(self, qweight, qzeros, scales, bias=None, group_size=128, activation=None):
         super().__init__()
         self.register_buffer("qweight", qweight)

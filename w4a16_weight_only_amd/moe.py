@@ -342,6 +342,8 @@ class AwqMoe(torch.nn.Module):
     are the same, the bits not always.  Otherwise the residual is added to y (and one of fp32 gives
     fp32)."""
 
+    one_call = False  # of modules that were saved whole before there was one
+
     def __init__(self, router, gate_up, down, topk, group_size=128, bias=None, one_call=False, **routing):
         super().__init__()
         self.register_buffer("router", router)
