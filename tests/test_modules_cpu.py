@@ -36,3 +36,14 @@ def test_modules_saved_before_their_options(monkeypatch):
     layer = saved_and_loaded(awq.AwqMoe(torch.ones(4, 32, dtype=torch.float16), packed(32, 64, 4), packed(32, 32, 4), 2,
                                         -1), "one_call")
     assert torch.equal(layer(x), x) and calls == ["gemm", "route", "mlp"]
+
+
+def test_a_norm_that_the_block_does_not_have_is_refused():
+    """AwqMlp.forward's normed stands for norm(x); without a norm it would be left out."""
+    mlp = awq.AwqMlp(packed(32, 64), packed(32, 32), -1)
+    x = torch.ones(3, 32, dtype=torch.float16)
+    with pytest.raises(ValueError, match="normed"):
+        mlp(x, normed=x)
+    for wrong in (x[:2], x.float()):
+        with pytest.raises(ValueError, match="normed"):
+            awq.AwqMlp(packed(32, 64), packed(32, 32), -1, norm=torch.ones(32, dtype=torch.float16))(x, normed=wrong)

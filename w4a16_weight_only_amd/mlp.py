@@ -39,6 +39,8 @@ class AwqMlp(torch.nn.Module):
         self.scale = scale
 
     def forward(self, x, normed=None, then=None):
+        if normed is not None and (self.norm is None or normed.shape != x.shape or normed.dtype is not x.dtype):
+            raise ValueError("normed must be norm(x), of x's shape and type, of a block with a norm")
         x = x.contiguous()
         h = x if self.norm is None else awq_norm(x, self.norm, **self.norms) if normed is None else normed.contiguous()
         h = awq_gemm_fused(h, self.up_qweight, self.up_qzeros, self.up_scales, self.up_bias, self.group_size,
