@@ -269,6 +269,28 @@ def test_a_layer_beside_a_fused_product_from_two_threads():
     assert wrong == [0, 0]
 
 
+def test_streams_from_outside():
+    """A stream that torch did not make: nothing is kept for its handle, the bits are the same."""
+    from w4a16_weight_only_amd import scratch
+
+    case = Case(3, 64, 2048, 1408, 2048, 128, torch.bfloat16, torch.bfloat16, 4)
+    want = case.run(8)
+    torch.cuda.synchronize()
+    inner = torch.cuda.Stream()
+    outside = torch.cuda.ExternalStream(inner.cuda_stream)
+    kept = dict(scratch._kept.blocks)
+    kept.pop((0, inner.cuda_stream), None)
+    scratch._kept.blocks = dict(kept)
+    with torch.cuda.stream(outside):
+        got = [case.run(8) for _ in range(20)]
+    outside.synchronize()
+    assert all(torch.equal(y, want) for y in got) and scratch._kept.blocks.keys() == kept.keys()
+    with torch.cuda.stream(inner):
+        got = [case.run(8) for _ in range(20)]
+    inner.synchronize()
+    assert all(torch.equal(y, want) for y in got) and (0, inner.cuda_stream) in scratch._kept.blocks
+
+
 def test_empty_and_refusals():
     case = Case(9, 8, 256, 96, 288, 32, torch.float16, torch.float16, 1)
     call = lambda x=case.x, router=case.router, up=case.up.dev, down=case.down.dev, topk=2, g=32, **k: awq.awq_moe_layer(  # noqa: E731

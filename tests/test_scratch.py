@@ -20,6 +20,7 @@ def stream(monkeypatch):
     now = {"raw": 0, "capturing": False}
     monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: now["capturing"], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: now["raw"], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentStream", lambda device: (now.get("id", 0), 0, 1), raising=False)
     return now
 
 
@@ -92,3 +93,16 @@ def test_blocks_go_with_their_thread(stream):
     assert alive() is not None
     end()
     assert alive() is None
+
+
+def test_streams_from_outside_keep_nothing(stream):
+    """Their handles come back for other streams, in no order with what ran before: torch gives such a stream its
+    handle for an id, its own streams small ones."""
+    stream.update(raw=1 << 40, id=1 << 40)
+    first = counters_and_scratch(CPU, *LAYER)
+    second = counters_and_scratch(CPU, *LAYER)
+    assert apart(ranges(first, LAYER), ranges(second, LAYER)) and not second[2][:LAYER[0]].any()
+    stream.update(raw=1 << 41, id=35)
+    assert counters_and_scratch(CPU, *LAYER)[:2] == counters_and_scratch(CPU, *LAYER)[:2]
+    stream.update(raw=0, id=0)  # the default stream
+    assert counters_and_scratch(CPU, *LAYER)[:2] == counters_and_scratch(CPU, *LAYER)[:2]
