@@ -496,11 +496,15 @@ int64_t active_entries(int64_t T, int64_t topk, int64_t E, int64_t rows) {
 // graph).  350 beside the stream; a k-step of 32 takes a compute unit's waves 100 to 125 by the rows (32
 // rows, which unpacking and rescaling bound: 120 and 220 for every 32 rows of a group), or what HBM gives (160 with all
 // of the units at it); a round of workgroups 100 beside; the join of the splits 250 (32 rows 450) and
-// a share by the rows for each.  Measured against forced split counts, us: 1 x 4096 -> 4096 fp16, 4, 8, 12, 16
+// a share by the rows for each, and of 32 rows 900 for every round after the first: its workgroups begin anew
+// and leave 32 or 64 KB of sums each (us, fp16, splits over rounds: 300 x 2048 -> 8192, g 64, 1 over 2 38, 2 over
+// 3 46, 4 over 5 66; 96 x 8192 -> 8192, 2 over 1 35, 3 over 2 50, 8 over 3 55).  Measured against forced split counts, us: 1 x 4096 -> 4096 fp16, 4, 8, 12, 16
 // splits 10.4, 8.3, 8.2, 8.9 (8 chosen); 16 x 4096 -> 4096 bf16, 4, 8, 12, 16: 13.0, 12.1, 11.8, 14.0 (8);
 // 4 x 4096 -> 2 x 11008, 3, 4, 5, 6: 20.7, 16.7, 16.4, 23.0 (4); 32 x 4096 -> 2 x 11008, 2, 3, 4, 5: 35.9, 30.6,
 // 27.9, 28.4 (4); 1 x 11008 -> 4096, 4, 8, 12, 16: 19.2, 13.1, 11.4, 11.9 (11); 16 x 8192 -> 28672, 1, 2, 3, 4:
-// 55.0, 34.9, 42.7, 39.0 (2).
+// 55.0, 34.9, 42.7, 39.0 (2).  (The stream's part is from before the waves' priorities: one round without
+// splits takes 0.75 to 0.95 of what it says.  Over ten weights, 17 to 1400 rows and both types the choice of splits and
+// tiles is 1.8% slower than the best of all of them in the mean, 36% at most.)
 int64_t choose_splits8(int64_t tiles, int64_t ksteps, int64_t g, bool gated, int rows, int64_t cus, int& splits,
                        int& steps) {
   const int64_t parts = gated ? kStreamWaves / 2 : kStreamWaves;
@@ -516,6 +520,7 @@ int64_t choose_splits8(int64_t tiles, int64_t ksteps, int64_t g, bool gated, int
     const int64_t hbm = 160 * tiles * sp / (rounds * cus);
     int64_t cost = 350 + rounds * (st * (hbm > step ? hbm : step) + 100);
     if (sp > 1) cost += (rows == 32 ? 450 : 250) + sp * share * (gated ? 2 : 1);
+    if (sp > 1 && rows == 32) cost += (rounds - 1) * 900;
     if (best >= 0 && cost >= best) continue;
     best = cost;
     steps = (int)st;
