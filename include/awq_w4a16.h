@@ -380,10 +380,13 @@ int awq_moe_mlp(const void* x, int act, const int32_t* up_qweight, const int32_t
  *                  after it, for this call alone until then.  (Calls that one thread makes on one
  *                  stream, one after another, may share workspace and counters.  Two threads' may
  *                  not: the launches of one's call may come between those of the other's.)
- * h is not rounded on the way (two terms, as for awq_moe_mlp): y is rounded once.  A token whose
- * logits hold a NaN (for the softmax, or +inf) comes out as NaN, one without experts as its residual.
+ * h stays as two terms of act, good to 2^-22 (fp16) or 2^-16 (bfloat16) of itself, as for awq_moe_mlp, and
+ * y is rounded once.  A token whose logits hold a NaN (for the softmax, or +inf) comes out as NaN, one
+ * without experts as its residual.
  * The result is deterministic.  The second launch's workgroups wait for each other's parts of h;
- * they need not all be resident, and calls may run side by side.
+ * they need not all be resident, and calls may run side by side.  Nobody who is waited for waits, so
+ * a wait lasts some microseconds; one that finds nothing in 2^18 looks (a fifth of a second or more, as
+ * where the card is stopped beneath a call) gives up, and what it would have made of y is NaN.
  * Limits: those of awq_moe_route and awq_moe_mlp.  T == 0 enqueues nothing.
  */
 enum { AWQ_MOE_LAYER_COUNTERS = 256 };

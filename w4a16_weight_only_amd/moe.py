@@ -267,7 +267,9 @@ def awq_moe_layer(x: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: t
 
     The logits are fp32; round_logits rounds them to x's type first.  Routing arguments are
     awq_moe_route's; y is rounded once.  A token whose logits hold a NaN (for the softmax, or +inf)
-    comes out as NaN.  out may be residual or x itself."""
+    comes out as NaN, and so does what a workgroup gave up waiting for (a fifth of a second, where
+    a wait takes microseconds).  h stays as two terms, good to 2^-22 (fp16) or 2^-16 (bfloat16) of
+    itself.  out may be residual or x itself."""
     _check_act("x", x)
     dev = x.device
     T, K = x.shape
