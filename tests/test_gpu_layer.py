@@ -167,6 +167,29 @@ def test_against_the_parts():
         assert float((got.double() - want.double()).norm() / want.double().norm()) <= 2 * HALF[dtype]
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_token_whose_h_is_long(dtype):
+    """So many experts that K of the second product is not split, and more columns of h than one token's form
+    keeps: the form of several tokens.  Against routing and MLP in calls of their own, within two roundings."""
+    E, topk, K, inner, N, g = 64, 64, 64, 8224, 1024, 32
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    words = lambda *s: torch.randint(-(1 << 31), 1 << 31, s, dtype=torch.int32, device="cuda", generator=gen)  # noqa: E731
+
+    def packed(rows, cols):
+        scales = torch.rand((E, rows // g, cols), device="cuda", generator=gen).add_(0.5).mul_(1 / (6.5 * rows ** 0.5))
+        return words(E, rows, cols // 8), words(E, rows // g, cols // 8), scales.half()
+
+    up, down = packed(K, 2 * inner), packed(inner, N)
+    x = torch.randn((1, K), device="cuda", generator=gen).to(dtype)
+    router = torch.randn((E, K), device="cuda", generator=gen)
+    weights, ids = awq.awq_moe_route(x.float() @ router.t(), topk)
+    want = awq.awq_moe_mlp(x, up, down, ids, weights, g)
+    first = awq.awq_moe_layer(x, router, up, down, topk, g)
+    assert float((first.double() - want.double()).norm() / want.double().norm()) <= 2 * HALF[dtype]
+    for _ in range(10):
+        assert torch.equal(awq.awq_moe_layer(x, router, up, down, topk, g), first)
+
+
 def test_same_bits_and_in_place():
     case = Case(5, 64, 2048, 1408, 2048, 128, torch.float16, torch.float16, 2)
     first = case.run(8)

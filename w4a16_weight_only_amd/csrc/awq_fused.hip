@@ -12,8 +12,9 @@
 // Eight waves, one workgroup to a compute unit, rather than two of four: half the shares to join (us in
 // a graph, four / eight waves: 1 x 4096 -> 4096 fp16 12.1 / 8.3, with its splits; 19 x 4096 -> 2 x 11008
 // bfloat16 36 / 28).  256 columns a wave, so that 16 lanes read whole 128-byte lines of a row.
-// Bound: one row of 4096 x 4096 (8.0 us, 8.7 MB) by latency, one after another of the weights, the
-// waves' and the splits' sums; 19 rows through 4096 -> 2 x 11008 (25.3 us, 47 MB) and 200 rows of 2048 -> 8192
+// Bound: one row of 4096 x 4096 (8.0 us, 8.7 MB) by this form, one after another of the weights, the waves' and the
+// splits' sums, on half of the compute units (awq_decode.hip, lighter workgroups and no sums read back, takes 4.6
+// there, without the epilogue); 19 rows through 4096 -> 2 x 11008 (25.3 us, 47 MB, 172 workgroups) and 200 rows of 2048 -> 8192
 // (20.2 us) by unpacking: VALU 60% and the matrix cores 25% of a busy compute unit's time.  Whether these or
 // row tiles take a call: choose_tiles.
 #include "awq_epilogue.h"
